@@ -1,4 +1,4 @@
-"""ctypes binding of libpf8 (include/pf8.h): the C entry points under the same names.
+"""ctypes binding of libpf8 (include/pf8.h, include/pf8_train.h): the C entry points under the same names.
 
 Argument marshalling only: pointers are passed as Python ints (device addresses), sizes as
 ints, the stream as a hipStream_t handle (int, 0 = null stream). Every function returns the
@@ -23,11 +23,14 @@ PF8_OK, PF8_EINVAL, PF8_ESHAPE, PF8_EALIGN, PF8_ENODEV, PF8_ELAUNCH = range(6)
 PF8_ALONG_COLS, PF8_ALONG_ROWS = 0, 1
 PF8_FPROP, PF8_DGRAD, PF8_WGRAD = 0, 1, 2
 PF8_GEMM_AUTO, PF8_GEMM_MX_SCALED, PF8_GEMM_PROMOTE = 0, 1, 2
-ABI_VERSION = 5
+PF8_BF16, PF8_F32 = 0, 1
+PF8_NORM_MAX_COLS = 32768
+ABI_VERSION = 6
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _vp = ctypes.c_void_p
+_f32 = ctypes.c_float
 
 # name -> (restype, argtypes); mirrors include/pf8.h
 SIGNATURES = {
@@ -46,6 +49,18 @@ SIGNATURES = {
     "pf8_abi_version": (_int, []),
 }
 
+# the inputs that both directions of the block norm take: h .. eps
+_NORM_IN = [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _int, _f32, _f32, _f32, _f32]
+
+# name -> (restype, argtypes); mirrors include/pf8_train.h
+TRAIN_SIGNATURES = {
+    "pf8_block_norm": (_int, [_i64, _i64, *_NORM_IN, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "pf8_block_norm_bwd": (
+        _int, [_i64, _i64, _vp, _i64, _vp, _i64, *_NORM_IN, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _int, _vp, _i64,
+               _vp]),
+    "pf8_block_norm_bwd_workspace": (_i64, [_i64, _i64]),
+}
+
 
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
@@ -53,7 +68,7 @@ def _load() -> ctypes.CDLL:
             f"libpf8.so is not built ({LIB_PATH}); run `python fp8_block_scaled_pf8_amd/build.py` "
             "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **TRAIN_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
@@ -105,6 +120,24 @@ def pf8_block_gemm_f32(layout, m, n, k, a, lda, a_dscale, ld_as, b, ldb, b_dscal
 
 def pf8_gemm_bf16(m, n, k, a, lda, b, ldb, d, ldd, hip_stream=0) -> int:
     return LIB.pf8_gemm_bf16(m, n, k, a, lda, b, ldb, d, ldd, hip_stream)
+
+
+def pf8_block_norm(rows, cols, h, ldh, y, ldy, w_post, gate, ld_gate, w_pre, wtype, residual_scale, branch_scale,
+                   weight_offset, eps, r, ldr, x, ldx, q, ldq, dscale, ld_s, hip_stream=0) -> int:
+    return LIB.pf8_block_norm(rows, cols, h, ldh, y, ldy, w_post, gate, ld_gate, w_pre, wtype, residual_scale,
+                              branch_scale, weight_offset, eps, r, ldr, x, ldx, q, ldq, dscale, ld_s, hip_stream)
+
+
+def pf8_block_norm_bwd(rows, cols, dr, lddr, dx, lddx, h, ldh, y, ldy, w_post, gate, ld_gate, w_pre, wtype,
+                       residual_scale, branch_scale, weight_offset, eps, dh, lddh, dy, lddy, dgate, ld_dgate, dw_pre,
+                       dw_post, accumulate, workspace, workspace_bytes, hip_stream=0) -> int:
+    return LIB.pf8_block_norm_bwd(rows, cols, dr, lddr, dx, lddx, h, ldh, y, ldy, w_post, gate, ld_gate, w_pre, wtype,
+                                  residual_scale, branch_scale, weight_offset, eps, dh, lddh, dy, lddy, dgate,
+                                  ld_dgate, dw_pre, dw_post, accumulate, workspace, workspace_bytes, hip_stream)
+
+
+def pf8_block_norm_bwd_workspace(rows, cols) -> int:
+    return LIB.pf8_block_norm_bwd_workspace(rows, cols)
 
 
 def pf8_strerror(status: int) -> str:

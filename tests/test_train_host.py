@@ -1,0 +1,105 @@
+"""The training operators' C ABI and wrappers on the host (no GPU needed): declared symbols, statuses
+of bad arguments, workspace sizes."""
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "pf8_train.h")
+
+L = pytest.importorskip("fp8_block_scaled_pf8_amd._lib", reason="libpf8.so not built (run __graft_entry__.build())")
+
+P = [0x10000 * i for i in range(1, 16)]  # fake, aligned device addresses: validation never dereferences them
+
+
+def test_every_declared_symbol_is_exported():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"^\s*(?:int64_t|pf8_status)\s+(pf8_\w+)\s*\(", text, flags=re.M))
+    assert names == set(L.TRAIN_SIGNATURES)
+    lib = ctypes.CDLL(L.LIB_PATH)
+    assert all(hasattr(lib, n) for n in names)
+    defs = dict(re.findall(r"#define\s+(PF8_\w+)\s+(\d+)", text))
+    for name in ("PF8_BF16", "PF8_F32", "PF8_NORM_MAX_COLS"):
+        assert int(defs[name]) == getattr(L, name)
+
+
+_IN = dict(h=P[0], ldh=512, y=P[1], ldy=512, w_post=P[2], gate=P[3], ld_gate=0, w_pre=P[4], wtype=0,
+           residual_scale=1.0, branch_scale=1.0, weight_offset=0.0, eps=1e-6)
+
+
+def _fwd(**kw):
+    a = dict(rows=4, cols=512, **_IN, r=P[5], ldr=512, x=P[6], ldx=512, q=P[7], ldq=512, dscale=P[8], ld_s=4)
+    a.update(kw)
+    return L.pf8_block_norm(*a.values(), 0)
+
+
+def _bwd(**kw):
+    a = dict(rows=4, cols=512, dr=P[9], lddr=512, dx=P[10], lddx=512, **_IN, dh=P[5], lddh=512, dy=P[6], lddy=512,
+             dgate=P[7], ld_dgate=0, dw_pre=P[11], dw_post=P[12], accumulate=0, workspace=P[13],
+             workspace_bytes=L.pf8_block_norm_bwd_workspace(4, 512))
+    a.update(kw)
+    return L.pf8_block_norm_bwd(*a.values(), 0)
+
+
+# argument sets that both directions refuse
+SHARED = [
+    (dict(h=0), "EINVAL"), (dict(rows=0), "EINVAL"), (dict(rows=-1), "EINVAL"), (dict(cols=0), "EINVAL"),
+    (dict(ldh=511), "EINVAL"), (dict(ldy=511), "EINVAL"), (dict(ld_gate=511), "EINVAL"), (dict(ld_gate=-1), "EINVAL"),
+    (dict(wtype=2), "EINVAL"), (dict(wtype=-1), "EINVAL"), (dict(eps=-1e-6), "EINVAL"),
+    (dict(eps=float("nan")), "EINVAL"), (dict(eps=float("inf")), "EINVAL"), (dict(branch_scale=float("nan")), "EINVAL"),
+    (dict(residual_scale=float("inf")), "EINVAL"), (dict(weight_offset=float("nan")), "EINVAL"),
+    (dict(rows=1 << 31, ld_s=1 << 31), "ESHAPE"), (dict(ldh=1 << 31), "ESHAPE"), (dict(ldy=1 << 31), "ESHAPE"),
+    (dict(ld_gate=1 << 31), "ESHAPE"),
+    (dict(h=P[0] + 1), "EALIGN"), (dict(y=P[1] + 1), "EALIGN"), (dict(gate=P[3] + 1), "EALIGN"),
+    (dict(gate=P[3] + 2, wtype=1), "EALIGN"), (dict(w_pre=P[4] + 2, wtype=1), "EALIGN"), (dict(w_post=P[2] + 1), "EALIGN"),
+]
+
+
+@pytest.mark.parametrize("kw,status", SHARED)
+def test_block_norm_inputs_are_checked(kw, status):
+    want = getattr(L, "PF8_" + status)
+    assert _fwd(**kw) == want
+    kw = {k: v for k, v in kw.items() if k != "ld_s"}
+    if "rows" in kw and kw["rows"] == 1 << 31:
+        kw["workspace_bytes"] = 1 << 40
+    if "ld_gate" in kw:
+        kw["ld_dgate"] = 512
+    assert _bwd(**kw) == want
+
+
+WIDE = {k: 40000 for k in ("cols", "ldh", "ldy", "ldr", "ldx")}
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(r=0, x=0, q=0, dscale=0), "EINVAL"), (dict(y=0, w_post=0, gate=0), "EINVAL"), (dict(w_pre=0), "EINVAL"),
+    (dict(y=0, r=0), "EINVAL"), (dict(y=0, r=0, w_post=0, gate=0, residual_scale=0.5), "EINVAL"),
+    (dict(q=0), "EINVAL"), (dict(dscale=0), "EINVAL"), (dict(ldr=511), "EINVAL"), (dict(ldx=511), "EINVAL"),
+    (dict(ldq=511), "EINVAL"), (dict(ld_s=3), "EINVAL"), (dict(cols=500), "ESHAPE"),
+    (dict(WIDE, q=0, dscale=0), "ESHAPE"), (dict(ldr=1 << 31), "ESHAPE"), (dict(ldq=1 << 31), "ESHAPE"),
+    (dict(r=P[5] + 1), "EALIGN"), (dict(q=P[7] + 8), "EALIGN"), (dict(ldq=520), "EALIGN"), (dict(dscale=P[8] + 2), "EALIGN"),
+])
+def test_block_norm_outputs_are_checked(kw, status):
+    assert _fwd(**kw) == getattr(L, "PF8_" + status)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dr=0, dx=0), "EINVAL"), (dict(w_pre=0), "EINVAL"), (dict(accumulate=2), "EINVAL"),
+    (dict(dh=0, dy=0, dgate=0, dw_pre=0, dw_post=0), "EINVAL"), (dict(gate=0), "EINVAL"), (dict(w_post=0), "EINVAL"),
+    (dict(dx=0), "EINVAL"), (dict(lddr=511), "EINVAL"), (dict(lddx=511), "EINVAL"), (dict(lddh=511), "EINVAL"),
+    (dict(lddy=511), "EINVAL"), (dict(ld_dgate=512), "EINVAL"), (dict(ld_gate=512, ld_dgate=511), "EINVAL"),
+    (dict(y=0, w_post=0, gate=0, dgate=0, dw_post=0), "EINVAL"),
+    (dict(workspace=0), "EINVAL"), (dict(workspace_bytes=4 * 3 * 512 * 4 - 1), "EINVAL"), (dict(workspace=P[13] + 8), "EALIGN"),
+    (dict(dw_pre=P[11] + 2), "EALIGN"), (dict(dgate=P[7] + 2), "EALIGN"), (dict(dx=P[10] + 1), "EALIGN"),
+    (dict(lddy=1 << 31), "ESHAPE"),
+])
+def test_block_norm_backward_is_checked(kw, status):
+    assert _bwd(**kw) == getattr(L, "PF8_" + status)
+
+
+def test_block_norm_workspace():
+    size = L.pf8_block_norm_bwd_workspace
+    assert size(0, 512) == size(4, 0) == size(4, 40000) == size(1 << 31, 512) == size(-1, 5) == 0
+    assert size(1, 1) >= 12 and size(8192, 2048) >= 3 * 2048 * 4
+    assert size((1 << 31) - 1, 32768) < 1 << 30
