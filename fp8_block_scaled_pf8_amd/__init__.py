@@ -24,6 +24,8 @@ from ._lib import (
     pf8_block_norm_bwd,
     pf8_block_norm_bwd_workspace,
     pf8_gemm_bf16,
+    pf8_newton_schulz,
+    pf8_newton_schulz_workspace,
     pf8_quant_act_1x128,
     pf8_quant_act_dual,
     pf8_quant_fwd,
@@ -33,6 +35,7 @@ from ._lib import (
 from .linear import Fp8Linear, Fp8LinearFunction, fp8_linear
 from .norm import (BlockNorm, BlockNormFunction, BlockNormGrads, block_norm, block_norm_backward, block_norm_quant,
                    fp8_block_norm)
+from .orthogonal import newton_schulz
 from .ops import (LinearStep, block_gemm, block_gemm_f32, dgrad, fprop, gemm_bf16, quant_act_1x128, quant_act_dual,
                   quant_w_128x128, wgrad, wgrad_f32)
 
@@ -45,5 +48,5 @@ __all__ = [
     "quant_w_128x128", "wgrad", "wgrad_f32", "Fp8Linear", "Fp8LinearFunction", "fp8_linear",
     "PF8_BF16", "PF8_F32", "pf8_block_norm", "pf8_block_norm_bwd", "pf8_block_norm_bwd_workspace",
     "BlockNorm", "BlockNormFunction", "BlockNormGrads", "block_norm", "block_norm_backward", "block_norm_quant",
-    "fp8_block_norm",
+    "fp8_block_norm", "pf8_newton_schulz", "pf8_newton_schulz_workspace", "newton_schulz",
 ]

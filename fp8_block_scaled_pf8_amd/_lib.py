@@ -25,6 +25,7 @@ PF8_FPROP, PF8_DGRAD, PF8_WGRAD = 0, 1, 2
 PF8_GEMM_AUTO, PF8_GEMM_MX_SCALED, PF8_GEMM_PROMOTE = 0, 1, 2
 PF8_BF16, PF8_F32 = 0, 1
 PF8_NORM_MAX_COLS = 32768
+PF8_NS_MAX_SHORT, PF8_NS_MAX_LONG, PF8_NS_MAX_BATCH, PF8_NS_MAX_STEPS = 32768, 1048576, 65535, 64
 ABI_VERSION = 6
 
 _i64 = ctypes.c_int64
@@ -59,6 +60,9 @@ TRAIN_SIGNATURES = {
         _int, [_i64, _i64, _vp, _i64, _vp, _i64, *_NORM_IN, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _int, _vp, _i64,
                _vp]),
     "pf8_block_norm_bwd_workspace": (_i64, [_i64, _i64]),
+    "pf8_newton_schulz": (
+        _int, [_i64, _i64, _i64, _vp, _i64, _i64, _int, _int, _vp, _f32, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "pf8_newton_schulz_workspace": (_i64, [_i64, _i64, _i64]),
 }
 
 
@@ -138,6 +142,17 @@ def pf8_block_norm_bwd(rows, cols, dr, lddr, dx, lddx, h, ldh, y, ldy, w_post, g
 
 def pf8_block_norm_bwd_workspace(rows, cols) -> int:
     return LIB.pf8_block_norm_bwd_workspace(rows, cols)
+
+
+def pf8_newton_schulz(batch, m, n, g, ldg, stride_g, gtype, steps, coefficients, eps, out, ldo, stride_o, workspace,
+                      workspace_bytes, hip_stream=0) -> int:
+    """``coefficients``: a ctypes array (or the host address) of steps x 3 floats."""
+    return LIB.pf8_newton_schulz(batch, m, n, g, ldg, stride_g, gtype, steps, coefficients, eps, out, ldo, stride_o,
+                                 workspace, workspace_bytes, hip_stream)
+
+
+def pf8_newton_schulz_workspace(batch, m, n) -> int:
+    return LIB.pf8_newton_schulz_workspace(batch, m, n)
 
 
 def pf8_strerror(status: int) -> str:

@@ -16,7 +16,7 @@ import sys
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
-SOURCES = ["quant.hip", "gemm.hip", "norm.hip", "abi.hip", "abi_train.hip"]
+SOURCES = ["quant.hip", "gemm.hip", "norm.hip", "newton_schulz.hip", "abi.hip", "abi_train.hip"]
 LIB_NAME = "libpf8.so"
 ARCH = "gfx950"
 

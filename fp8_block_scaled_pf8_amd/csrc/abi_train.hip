@@ -3,6 +3,7 @@
 // need no GPU.
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/pf8_train.h"
@@ -122,6 +123,37 @@ pf8_status pf8_block_norm_bwd(int64_t rows, int64_t cols, const void* dr, int64_
                      {dw_pre, dw_post, full ? nullptr : static_cast<float*>(dgate)}, accumulate,
                      static_cast<float*>(workspace)};
   return launch_status(pf8::launch_norm_bwd(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+int64_t pf8_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n) {
+  if (batch <= 0 || m <= 0 || n <= 0 || batch > PF8_NS_MAX_BATCH || std::min(m, n) > PF8_NS_MAX_SHORT ||
+      std::max(m, n) > PF8_NS_MAX_LONG)
+    return 0;
+  return pf8::ns_workspace(batch, m, n);
+}
+
+pf8_status pf8_newton_schulz(int64_t batch, int64_t m, int64_t n, const void* g, int64_t ldg, int64_t stride_g,
+                             pf8_dtype gtype, int steps, const float* coefficients, float eps, void* out, int64_t ldo,
+                             int64_t stride_o, void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (!g || !out || !coefficients || !workspace || batch <= 0 || m <= 0 || n <= 0) return PF8_EINVAL;
+  if ((gtype != PF8_BF16 && gtype != PF8_F32) || steps <= 0 || steps > PF8_NS_MAX_STEPS) return PF8_EINVAL;
+  if (!std::isfinite(eps) || eps < 0.0f || ldg < n || ldo < n) return PF8_EINVAL;
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!(std::fabs(coefficients[i]) <= 64.0f)) return PF8_EINVAL;
+  if (batch > PF8_NS_MAX_BATCH || std::min(m, n) > PF8_NS_MAX_SHORT || std::max(m, n) > PF8_NS_MAX_LONG ||
+      any_too_big(ldg, ldo))
+    return PF8_ESHAPE;
+  // a matrix spans less than 2^51 elements here, and strides up to 2^46 times the batch stay in range
+  if (batch > 1 && (stride_g < (m - 1) * ldg + n || stride_o < (m - 1) * ldo + n)) return PF8_EINVAL;
+  if (batch > 1 && (stride_g > (int64_t{1} << 46) || stride_o > (int64_t{1} << 46))) return PF8_ESHAPE;
+  if (workspace_bytes < pf8_newton_schulz_workspace(batch, m, n)) return PF8_EINVAL;
+  if (!aligned(g, gtype == PF8_F32 ? 4 : 2) || !aligned(out, 2) || !aligned(workspace, 256)) return PF8_EALIGN;
+  if (int e = device_status()) return e;
+  pf8::NsArgs a{};
+  a.m = m, a.n = n, a.g = g, a.ldg = ldg, a.stride_g = batch > 1 ? stride_g : 0, a.gf32 = gtype == PF8_F32, a.eps = eps;
+  a.out = static_cast<uint16_t*>(out), a.ldo = ldo, a.stride_o = batch > 1 ? stride_o : 0;
+  return launch_status(pf8::launch_newton_schulz(a, batch, steps, coefficients, workspace,
+                                                 static_cast<hipStream_t>(hip_stream)));
 }
 
 }  // extern "C"

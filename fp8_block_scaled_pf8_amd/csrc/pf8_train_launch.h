@@ -59,4 +59,26 @@ hipError_t launch_norm_bwd(const NormBwdArgs& args, hipStream_t stream);
 // Workgroups of the backward pass, each with one row of partial column sums.
 int64_t norm_bwd_groups(int64_t rows, int64_t cols);
 
+// Newton-Schulz orthogonalisation; the launcher fills in what lies in the workspace.
+struct NsArgs {
+  int64_t m, n;  // of G
+  const void* g;
+  int64_t ldg, stride_g;
+  int gf32;  // G is FP32, else BF16
+  float eps;
+  uint16_t* out;
+  int64_t ldo, stride_o;
+  int64_t pp, qp;   // padded min(m, n) and max(m, n)
+  int64_t x_elems;  // pp * qp
+  float* xf;
+  _Float16 *xc[2], *xr, *a16, *b16;
+  float *da, *db, *part;
+  double* norm_part;
+};
+
+int64_t ns_workspace(int64_t batch, int64_t m, int64_t n);
+// coef: steps x 3 on the host
+hipError_t launch_newton_schulz(NsArgs args, int64_t batch, int steps, const float* coef, void* workspace,
+                                hipStream_t stream);
+
 }  // namespace pf8

@@ -90,6 +90,46 @@ pf8_status pf8_block_norm_bwd(int64_t rows, int64_t cols, const void* dr, int64_
 /* Bytes of pf8_block_norm_bwd's workspace; 0 for sizes it refuses. */
 int64_t pf8_block_norm_bwd_workspace(int64_t rows, int64_t cols);
 
+/* Largest sides of a matrix that pf8_newton_schulz takes: the shorter and the longer one, and the
+   largest number of matrices and of steps. */
+#define PF8_NS_MAX_SHORT 32768
+#define PF8_NS_MAX_LONG 1048576
+#define PF8_NS_MAX_BATCH 65535
+#define PF8_NS_MAX_STEPS 64
+
+/*
+ * Newton-Schulz orthogonalisation of a stack of gradients, as orthogonalising optimisers apply it to
+ * a weight matrix's update:
+ *
+ *   X = G / (|G|_F + eps)
+ *   per step (a, b, c):  X <- a X + b (X X^T) X + c (X X^T)^2 X      (X^T X on the right of a tall X)
+ *   out = X, rounded to BF16
+ *
+ * Every singular value s of X becomes a s + b s^3 + c s^5 in each step; the singular vectors stay.
+ *
+ * g:   `batch` matrices [m, n] of gtype (BF16, or FP32 as a main gradient), row pitch ldg, stride_g
+ *      elements from one matrix to the next (not read for batch = 1).
+ * out: bf16 [m, n] each, row pitch ldo, stride stride_o; no overlap with g.
+ * coefficients: HOST pointer to steps x 3 floats (a, b, c), read before the call returns; finite and at
+ *      most 64 in magnitude. They must keep the singular values below 8 between the steps (any
+ *      orthogonalising choice keeps them near 1); beyond, FP16 operands overflow to NaN.
+ * eps: >= 0. A matrix of zeros gives zeros (NaN with eps = 0); one that holds a NaN or an infinity
+ *      gives NaN everywhere.
+ *
+ * Precision: X, the diagonals of X X^T and of the polynomial, and every sum are FP32 or FP64; the matrix
+ * products' operands are FP16, scaled by powers of two. Besides the BF16 rounding of the result
+ * (1.7e-3 of its 2-norm) the result is off by up to 1.5e-3 of its 2-norm, by up to 3e-3 where a few
+ * entries carry the norm of a large matrix. The same call gives the same bits.
+ *
+ * workspace: pf8_newton_schulz_workspace(batch, m, n) bytes, 256-byte aligned.
+ */
+pf8_status pf8_newton_schulz(int64_t batch, int64_t m, int64_t n, const void* g, int64_t ldg, int64_t stride_g,
+                             pf8_dtype gtype, int steps, const float* coefficients, float eps, void* out, int64_t ldo,
+                             int64_t stride_o, void* workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* Bytes of pf8_newton_schulz's workspace; 0 for sizes it refuses. */
+int64_t pf8_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,6 +6,7 @@ expression with every term replaced by its magnitude, which the FP32 roundings o
 relative to.
 
 newton_schulz: the odd polynomial iteration X <- a X + b (X X^T) X + c (X X^T)^2 X from G / (|G| + eps).
+newton_schulz_operands: the same, with FP16 operands in the products as the library documents them.
 """
 from __future__ import annotations
 
@@ -87,3 +88,31 @@ def newton_schulz(g, coefficients, eps=1e-7):
         gram = x @ np.swapaxes(x, -2, -1)
         x = a * x + (b * gram + c * (gram @ gram)) @ x
     return np.swapaxes(x, -2, -1) if tall else x
+
+
+def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
+    """newton_schulz with the FP16 roundings of a kernel's product operands, all else in float64.
+
+    X is kept; its rounding enters the products (with `pairs`, as value plus remainder). The
+    diagonals of A = X X^T and of B = b A + c A A are kept, their other elements rounded. The
+    diagonal of B multiplies X where its element is over 2/3 |a - 1| (with `pairs`, everywhere),
+    X's rounding elsewhere.
+    """
+    f16 = lambda a, s: (a * s).astype(np.float16).astype(np.float64) / s  # noqa: E731
+    x = np.asarray(g, dtype=np.float64)
+    x = x / (np.sqrt(np.sum(x * x)) + eps)
+    tall = x.shape[0] > x.shape[1]
+    x = x.T if tall else x
+    off = 1.0 - np.eye(x.shape[0])
+    for a, b, c in coefficients:
+        xh = f16(x, 2.0 ** 12)
+        xp = xh + (f16(x - xh, 2.0 ** 12) if pairs else 0.0)
+        gram = xp @ xp.T
+        d = np.diag(gram).copy()
+        gram = f16(gram * off, 2.0 ** 10)
+        square = gram @ gram
+        poly = b * gram + c * (square + (d[:, None] + d[None, :]) * gram)
+        diag = (b * d + c * (np.diag(square) + d * d))[:, None]
+        own = x if pairs else np.where(np.abs(diag) > 2.0 / 3.0 * abs(a - 1.0), x, xh)
+        x = a * x + diag * own + f16(poly * off, 2.0 ** 9) @ xp
+    return x.T if tall else x

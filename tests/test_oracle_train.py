@@ -62,3 +62,15 @@ def test_newton_schulz_acts_on_the_singular_values():
             s = a * s + b * s ** 3 + c * s ** 5
         np.testing.assert_allclose(train.newton_schulz(g, coef), (u * s) @ vt, atol=1e-12)
     assert not train.newton_schulz(np.zeros((3, 4)), coef).any()
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_newton_schulz_operands_are_close_to_exact(pairs):
+    rng = np.random.default_rng(2)
+    coef = [(3.4445, -4.7750, 2.0315)] * 5
+    for m, n in ((40, 60), (90, 70), (150, 200)):
+        for g in (rng.standard_normal((m, n)), rng.standard_normal((m, 2)) @ rng.standard_normal((2, n))):
+            ref = train.newton_schulz(g, coef)
+            got = train.newton_schulz_operands(g, coef, pairs=pairs)
+            off = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+            assert 1e-5 < off < 2.5e-3  # FP16's half step is 4.9e-4, over five steps

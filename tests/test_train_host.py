@@ -21,7 +21,8 @@ def test_every_declared_symbol_is_exported():
     lib = ctypes.CDLL(L.LIB_PATH)
     assert all(hasattr(lib, n) for n in names)
     defs = dict(re.findall(r"#define\s+(PF8_\w+)\s+(\d+)", text))
-    for name in ("PF8_BF16", "PF8_F32", "PF8_NORM_MAX_COLS"):
+    for name in ("PF8_BF16", "PF8_F32", "PF8_NORM_MAX_COLS", "PF8_NS_MAX_SHORT", "PF8_NS_MAX_LONG", "PF8_NS_MAX_BATCH",
+                 "PF8_NS_MAX_STEPS"):
         assert int(defs[name]) == getattr(L, name)
 
 
@@ -103,3 +104,35 @@ def test_block_norm_workspace():
     assert size(0, 512) == size(4, 0) == size(4, 40000) == size(1 << 31, 512) == size(-1, 5) == 0
     assert size(1, 1) >= 12 and size(8192, 2048) >= 3 * 2048 * 4
     assert size((1 << 31) - 1, 32768) < 1 << 30
+
+
+def _ns(**kw):
+    a = dict(batch=2, m=100, n=200, g=P[0], ldg=200, stride_g=20000, gtype=1, steps=1,
+             coefficients=(ctypes.c_float * 3)(1.5, -0.5, 0.0), eps=1e-7, out=P[1], ldo=200, stride_o=20000,
+             workspace=P[2], workspace_bytes=L.pf8_newton_schulz_workspace(2, 100, 200))
+    a.update(kw)
+    return L.pf8_newton_schulz(*a.values(), 0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(g=0), "EINVAL"), (dict(out=0), "EINVAL"), (dict(workspace=0), "EINVAL"), (dict(coefficients=None), "EINVAL"),
+    (dict(batch=0), "EINVAL"), (dict(m=0), "EINVAL"), (dict(n=-1), "EINVAL"), (dict(gtype=2), "EINVAL"),
+    (dict(steps=0), "EINVAL"), (dict(steps=65), "EINVAL"), (dict(eps=-1.0), "EINVAL"), (dict(eps=float("nan")), "EINVAL"),
+    (dict(ldg=199), "EINVAL"), (dict(ldo=199), "EINVAL"), (dict(stride_g=19999), "EINVAL"), (dict(stride_o=0), "EINVAL"),
+    (dict(coefficients=(ctypes.c_float * 3)(64.5, 0.0, 0.0)), "EINVAL"),
+    (dict(coefficients=(ctypes.c_float * 3)(1.0, float("nan"), 0.0)), "EINVAL"),
+    (dict(batch=65536), "ESHAPE"), (dict(m=32769, n=32769, ldg=32769, ldo=32769), "ESHAPE"),
+    (dict(n=1048577, ldg=1048577, ldo=1048577), "ESHAPE"), (dict(ldg=1 << 31), "ESHAPE"),
+    (dict(stride_g=(1 << 46) + 1), "ESHAPE"),
+    (dict(workspace_bytes=L.pf8_newton_schulz_workspace(2, 100, 200) - 1), "EINVAL"),
+    (dict(g=P[0] + 2), "EALIGN"), (dict(out=P[1] + 1), "EALIGN"), (dict(workspace=P[2] + 128), "EALIGN"),
+])
+def test_newton_schulz_is_checked(kw, status):
+    assert _ns(**kw) == getattr(L, "PF8_" + status)
+
+
+def test_newton_schulz_workspace():
+    size = L.pf8_newton_schulz_workspace
+    assert size(0, 5, 5) == size(1, 0, 5) == size(1, 5, -1) == size(1, 32769, 32769) == size(1, 5, 1048577) == 0
+    assert size(65536, 5, 5) == 0 and size(1, 1, 1) > 0
+    assert size(1, 2048, 512) == size(1, 512, 2048) >= 2048 * 512 * 10
