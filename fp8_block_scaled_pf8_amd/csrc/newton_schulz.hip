@@ -30,11 +30,14 @@
 // Layout. X lives in the workspace, padded to multiples of 128 with zeros that stay zero, so the
 // products have no edges: Xr [p][q] (A's operand), Xc [q][p] (the update's operand, two buffers in
 // turn) and FP32 in 64x64 regions in the order the update's lanes hold them, so that each lane
-// reads and writes 16 consecutive bytes.
+// reads and writes 16 consecutive bytes. FP16 rows are 128 bytes longer than that: a tile's loads read
+// the same columns of many rows, and with a pitch of 4 KiB or a multiple they crowd a few channels.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
+#include <utility>
 
 #include "pf8_train_launch.h"
 
@@ -53,8 +56,8 @@ struct NsCoef {
 };
 
 constexpr float kSX = 4096.0f, kSA = 1024.0f, kSB = 512.0f;  // powers of two that FP16 operands carry
-constexpr int kBK = 64;                                      // K values of one stage (128-byte LDS rows)
 constexpr int kRegion = 64 * 64;
+constexpr int64_t kPad = 64;  // values that FP16 rows are longer than padded: see "Layout"
 // a diagonal element of B over this part of |a - 1| (which a matrix of full rank with singular values
 // near one has) multiplies X in FP32
 constexpr float kOwnRow = 2.0f / 3.0f;
@@ -65,19 +68,44 @@ __device__ __forceinline__ int region_offset(int bi, int bj, int g, int lane) {
   return ((bi * 2 + bj) * 4 + g) * 256 + lane * 4;
 }
 
-// D[m, n] = sum_k P[m, k] Q[n, k] over `steps` stages of 64: a BM x BN tile by (BM/WM)(BN/WN) waves.
-// Stages go straight to LDS (16 bytes a lane), NST - 1 ahead of use. In a 128-byte LDS row, chunk c
-// of row r sits at c ^ ((r >> 1) & 7): 16 consecutive rows' reads of one chunk fall into the 16
-// different 16-byte slots of the 64 banks. One barrier a stage: behind it every wave's loads of the
-// stage have landed and the buffer of the stage before is free to be filled again.
-template <int BM, int BN, int WM, int WN, int NST>
+// Up to four stage buffers.
+struct Buffers {
+  uint8_t *b0, *b1, *b2, *b3;
+  template <int I>
+  __device__ __forceinline__ uint8_t* at() const {
+    if constexpr (I == 0) return b0;
+    else if constexpr (I == 1) return b1;
+    else if constexpr (I == 2) return b2;
+    else return b3;
+  }
+};
+
+// D[m, n] = sum_k P[m, k] Q[n, k] over `steps` stages of BK (a multiple of 128 values in all): a BM x BN tile by (BM/WM)(BN/WN) waves.
+// Stages go straight to LDS (16 bytes a lane) into NST buffers, NST - 1 to NST ahead of use. In an LDS row of
+// BK values, chunk c (16 bytes) of row r sits at c ^ ((r >> 1) & 7) (128-byte rows) or c ^ ((r >> 2) & 3)
+// (64-byte rows): 16 consecutive rows' reads of one chunk fall into the 16 different 16-byte slots of the
+// 64 banks. One barrier a stage, in its middle, while the matrix cores still have the stage's second half
+// to do: behind it every wave's loads of the next stage have landed, and the stage's own buffer, whose
+// operands are all in registers, is free to be filled again. The buffers are LDS objects of their own, so that the
+// compiler sees that a read of one does not wait for loads into another.
+template <int BM, int BN, int WM, int WN, int BK, int NST>
 struct Tile {
   static constexpr int kWavesN = BN / WN, kWaves = (BM / WM) * kWavesN, kThreads = 64 * kWaves;
   static constexpr int TM = WM / 32, TN = WN / 32;
-  static constexpr int kStage = (BM + BN) * 128;
-  static constexpr int kLoads = (BM + BN) / 8 / kWaves;  // 1 KiB loads per wave and stage
-  static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0 && (NST == 2 || NST == 3), "even loads, two or three buffers");
+  static constexpr int kRow = BK * 2, kStage = (BM + BN) * kRow;
+  static constexpr int kSlab = 1024 / kRow;  // rows of one load (64 lanes x 16 bytes)
+  static constexpr int kLoadsP = BM / kSlab / kWaves, kLoads = kLoadsP + BN / kSlab / kWaves;
+  static_assert(BM / kSlab % kWaves == 0 && BN / kSlab % kWaves == 0 && (BK == 32 || BK == 64), "even loads");
+  static_assert(NST >= 2 && NST <= 4, "up to four buffers");
   typedef f16v Acc[TM][TN];
+
+  static __device__ __forceinline__ int swizzle(int row) { return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+
+  // f(0), f(1), ... with compile-time arguments
+  template <typename F, int... V>
+  static __device__ __forceinline__ void each(F f, std::integer_sequence<int, V...>) {
+    (f(std::integral_constant<int, V>{}), ...);
+  }
 
   static __device__ __forceinline__ void zero(Acc& acc) {
 #pragma unroll
@@ -89,118 +117,269 @@ struct Tile {
   }
 
   static __device__ __forceinline__ void run(const _Float16* P, int64_t ldp, const _Float16* Q, int64_t ldq, int k0,
-                                             int steps, uint8_t* b0, uint8_t* b1, uint8_t* b2, Acc& acc) {
+                                             int steps, const Buffers& bufs, Acc& acc) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kWavesN, wn = wave % kWavesN;
     const int ldpb = static_cast<int>(ldp) * 2, ldqb = static_cast<int>(ldq) * 2;
     const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(P), 0, BM * ldpb, 0x00020000);
     const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(Q), 0, BN * ldqb, 0x00020000);
-    // lane's part of a load: row lane / 8 of 8, and the chunk that belongs at LDS chunk lane % 8.
-    // The slab's first row is a multiple of 8, so its part of the swizzle is its bit 3.
-    const int lrow = lane >> 3;
-    auto issue = [&](uint8_t* buf, int s) {
-      const int kofs = (k0 + s * kBK) * 2;
+    constexpr int kChunks = kRow / 16;
+    const int lrow = lane / kChunks;  // the lane's row in a load, and below the chunk that belongs at its place
+    // part 0: P's loads of a stage, 1: Q's
+    auto issue = [&](auto part, uint8_t* buf, int s) {
+      const int kofs = (k0 + s * BK) * 2;
+      constexpr int from = decltype(part)::value ? kLoadsP : 0, to = decltype(part)::value ? kLoads : kLoadsP;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
+      for (int i = from; i < to; ++i) {
         const int slab = wave + i * kWaves;
-        const int row = slab * 8 + lrow;
-        const int chunk = (lane & 7) ^ ((row >> 1) & 7);
+        const int chunk = (lane % kChunks) ^ swizzle(slab * kSlab + lrow);
         auto* dst = (__attribute__((address_space(3))) void*)(buf + slab * 1024);
-        if (i < BM / 8 / kWaves) __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, dst, 16, lrow * ldpb + chunk * 16, slab * 8 * ldpb + kofs, 0, 0);
-        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, dst, 16, lrow * ldqb + chunk * 16, (slab - BM / 8) * 8 * ldqb + kofs, 0, 0);
+        if (i < kLoadsP) __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, dst, 16, lrow * ldpb + chunk * 16, slab * kSlab * ldpb + kofs, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, dst, 16, lrow * ldqb + chunk * 16, (slab * kSlab - BM) * ldqb + kofs, 0, 0);
       }
     };
     const int l32 = lane & 31, half = lane >> 5;
-    auto compute = [&](const uint8_t* buf) {
+    auto frag = [&](const uint8_t* buf, int row, int k) {
+      return *reinterpret_cast<const h8*>(buf + row * kRow + (((2 * k + half) ^ swizzle(row)) << 4));
+    };
+    // operands of the first (0) or second (1) half of a stage's k-steps
+    constexpr int kHalf = BK / 32;
+    h8 fp[2][kHalf][TM], fq[2][kHalf][TN];
+    auto read = [&](auto h_c, const uint8_t* buf) {
+      constexpr int h = decltype(h_c)::value;
 #pragma unroll
-      for (int k = 0; k < kBK / 16; ++k) {
-        h8 fp[TM], fq[TN];
+      for (int k = 0; k < kHalf; ++k) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const int row = wm * WM + 32 * i + l32;
-          fp[i] = *reinterpret_cast<const h8*>(buf + row * 128 + (((2 * k + half) ^ ((row >> 1) & 7)) << 4));
-        }
+        for (int i = 0; i < TM; ++i) fp[h][k][i] = frag(buf, wm * WM + 32 * i + l32, h * kHalf + k);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int row = BM + wn * WN + 32 * j + l32;
-          fq[j] = *reinterpret_cast<const h8*>(buf + row * 128 + (((2 * k + half) ^ ((row >> 1) & 7)) << 4));
-        }
+        for (int j = 0; j < TN; ++j) fq[h][k][j] = frag(buf, BM + wn * WN + 32 * j + l32, h * kHalf + k);
+      }
+    };
+    auto multiply = [&](auto h_c) {
+      constexpr int h = decltype(h_c)::value;
+#pragma unroll
+      for (int k = 0; k < kHalf; ++k)
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[j], fp[i], acc[i][j], 0, 0, 0);
-      }
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[h][k][j], fp[h][k][i], acc[i][j], 0, 0, 0);
     };
-    auto sync_stage = [&](bool more) {
+    using H0 = std::integral_constant<int, 0>;
+    using H1 = std::integral_constant<int, 1>;
+    // Every wave's loads of a stage have landed and its operand reads are done; `behind` loads after them
+    // may still be in flight (loads complete in order).
+    auto sync_stage = [&](auto behind) {
+      constexpr int fly = decltype(behind)::value;
+      static_assert(fly < 64, "the counter's range");
+      __builtin_amdgcn_sched_barrier(0);
       asm volatile("" ::: "memory");
-      // vmcnt(loads of the stages behind this one that may still fly) lgkmcnt(0)
-      constexpr int fly = (NST - 2) * kLoads;
-      if (more) __builtin_amdgcn_s_waitcnt((fly & 0xF) | ((fly >> 4) << 14) | (0x7 << 4));
-      else __builtin_amdgcn_s_waitcnt(0x7 << 4);
+      __builtin_amdgcn_s_waitcnt((fly & 0xF) | ((fly >> 4) << 14) | (0x7 << 4));
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
     };
-    issue(b0, 0);
-    if (NST == 3 && steps > 1) issue(b1, 1);
-    auto step = [&](uint8_t* use, uint8_t* fill, int s) {
-      sync_stage(s + 1 < steps && NST == 3);
-      if (s + NST - 1 < steps) issue(fill, s + NST - 1);
-      compute(use);
+    // The order of a half stage: LDS reads and loads evenly behind the products. (Loads in a row fill the
+    // queues of the memory path, and a wave that waits for room there issues no products either.)
+    auto spread = [&](auto loads) {
+      constexpr int products = kHalf * TM * TN, reads = kHalf * (TM + TN), vm = decltype(loads)::value;
+      each(
+          [&](auto x_c) {
+            constexpr int x = decltype(x_c)::value;
+            constexpr int r = reads * (x + 1) / products - reads * x / products, v = vm * (x + 1) / products - vm * x / products;
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(0x100, r, 0);
+            if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x020, v, 0);
+          },
+          std::make_integer_sequence<int, products>{});
     };
-    if constexpr (NST == 3) {
-      for (int s = 0; s < steps; s += 3) {
-        step(b0, b2, s);
-        if (s + 1 < steps) step(b1, b0, s + 1);
-        if (s + 2 < steps) step(b2, b1, s + 2);
+    using Loads0 = std::integral_constant<int, kLoadsP>;
+    using Loads1 = std::integral_constant<int, kLoads - kLoadsP>;
+    using None = std::integral_constant<int, 0>;
+    // One stage, in buffer U. First half: the second half's operands are read, and the refill of the buffer
+    // before (stage s - 1 + NST) gets its second part. The waves meet; then the buffer itself gets the first
+    // part of its refill, and the next stage's first operands are read.
+    auto stage = [&](auto u_c, int s, auto before, auto refill, auto behind, auto last) {
+      constexpr int u = decltype(u_c)::value;
+      if constexpr (decltype(before)::value) issue(H1{}, bufs.template at<(u + NST - 1) % NST>(), s - 1 + NST);
+      read(H1{}, bufs.template at<u>());
+      multiply(H0{});
+      if constexpr (decltype(before)::value) spread(Loads1{});
+      else spread(None{});
+      if constexpr (!decltype(last)::value) {
+        sync_stage(behind);
+        if constexpr (decltype(refill)::value) issue(H0{}, bufs.template at<u>(), s + NST);
+        read(H0{}, bufs.template at<(u + 1) % NST>());
+        multiply(H1{});
+        if constexpr (decltype(refill)::value) spread(Loads0{});
+        else spread(None{});
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        multiply(H1{});
       }
+    };
+    // All waits are exact and known at compile time, which also keeps the compiler from waiting for loads
+    // by itself: the last REM stages are a code path of their own.
+    auto tail = [&](auto rem_c, int s) {
+      constexpr int rem = decltype(rem_c)::value;
+      each(
+          [&](auto v_c) {
+            constexpr int v = decltype(v_c)::value, left = rem - 2 - v;
+            stage(std::integral_constant<int, v % NST>{}, s + v, std::bool_constant<(v - 1 + NST < rem)>{},
+                  std::bool_constant<(v + NST < rem)>{},
+                  std::integral_constant<int, (left < 0 ? 0 : (left < NST - 2 ? left : NST - 2)) * kLoads>{},
+                  std::bool_constant<(v + 1 == rem)>{});
+          },
+          std::make_integer_sequence<int, rem>{});
+    };
+    // The first N stages go out, and one more's first part (MORE); the first of them is read.
+    auto start = [&](auto n_c, auto more) {
+      constexpr int n = decltype(n_c)::value;
+      each(
+          [&](auto u) {
+            issue(H0{}, bufs.template at<decltype(u)::value>(), u);
+            issue(H1{}, bufs.template at<decltype(u)::value>(), u);
+          },
+          std::make_integer_sequence<int, n>{});
+      if constexpr (decltype(more)::value) issue(H0{}, bufs.template at<n>(), n);
+      sync_stage(std::integral_constant<int, (n - 1) * kLoads + (decltype(more)::value ? kLoadsP : 0)>{});
+      read(H0{}, bufs.b0);
+    };
+    // `steps` is a multiple of 128 / BK; where NST is one too, so is what the main loop leaves
+    constexpr int kUnit = NST % (128 / BK) == 0 ? 128 / BK : 1;
+    if (steps < NST) {
+      each(
+          [&](auto v_c) {
+            constexpr int all = decltype(v_c)::value * kUnit;
+            if constexpr (all > 0 && all < NST)
+              if (steps == all) {
+                start(std::integral_constant<int, all>{}, std::false_type{});
+                tail(std::integral_constant<int, all>{}, 0);
+              }
+          },
+          std::make_integer_sequence<int, NST>{});
     } else {
-      for (int s = 0; s < steps; s += 2) {
-        step(b0, b1, s);
-        if (s + 1 < steps) step(b1, b0, s + 1);
-      }
+      start(std::integral_constant<int, NST - 1>{}, std::true_type{});
+      int s = 0;
+      for (; s + 2 * NST <= steps; s += NST)
+        each(
+            [&](auto u) {
+              stage(u, s + decltype(u)::value, std::true_type{}, std::true_type{}, std::integral_constant<int, (NST - 2) * kLoads>{},
+                    std::false_type{});
+            },
+            std::make_integer_sequence<int, NST>{});
+      // NST .. 2 NST - 1 stages are left
+      each(
+          [&](auto v_c) {
+            constexpr int rem = decltype(v_c)::value * kUnit;
+            if constexpr (rem >= NST && rem < 2 * NST)
+              if (steps - s == rem) tail(std::integral_constant<int, rem>{}, s);
+          },
+          std::make_integer_sequence<int, 2 * NST>{});
     }
     // the buffers may be written by the epilogue once every wave has read its last operands
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x7 << 4);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    sync_stage(std::integral_constant<int, 0>{});
   }
 };
 
-// Position t of the lower triangle (row by row, diagonal included) -> (row, column).
-__device__ __forceinline__ void triangle(int t, int& ti, int& tj) {
-  int i = static_cast<int>((__builtin_sqrtf(8.0f * static_cast<float>(t) + 1.0f) - 1.0f) * 0.5f);
-  while (i * (i + 1) / 2 > t) --i;
-  while ((i + 1) * (i + 2) / 2 <= t) ++i;
-  ti = i;
-  tj = t - i * (i + 1) / 2;
+// The stage buffers of a kernel, as LDS objects of their own.
+#define PF8_NS_BUFFERS(bufs, G, NST)                                                                            \
+  __shared__ __align__(16) uint8_t bufs##0 [G::kStage], bufs##1 [G::kStage], bufs##2 [NST > 2 ? G::kStage : 16], \
+      bufs##3 [NST > 3 ? G::kStage : 16];                                                                        \
+  const Buffers bufs = {bufs##0, bufs##1, bufs##2, bufs##3}
+
+// Tile t of those that cover the lower triangle of a square matrix: BM x BN tiles, numbered by rows (with
+// BN = 2 BM by pairs of rows); (ti, tj) in tiles.
+template <int BM, int BN>
+__device__ __forceinline__ void triangle_tile(int t, int& ti, int& tj) {
+  constexpr int kTwo = BM == BN ? 1 : 2;  // pairs of tiles make a square
+  static_assert(BM == BN || BM == 2 * BN || BN == 2 * BM, "square or two to one");
+  const int u = t / kTwo;
+  int i = static_cast<int>((__builtin_sqrtf(8.0f * static_cast<float>(u) + 1.0f) - 1.0f) * 0.5f);
+  while (i * (i + 1) / 2 > u) --i;
+  while ((i + 1) * (i + 2) / 2 <= u) ++i;
+  const int j = u - i * (i + 1) / 2, odd = t % kTwo;
+  ti = BN > BM ? 2 * i + odd : i;
+  tj = BM > BN ? 2 * j + odd : j;
 }
 
-// Writes a T x T tile from LDS (FP16, pitch T + 8) to rows r0.. and columns c0.. of a symmetric
-// matrix, and its mirror image. In a tile on the diagonal the lower triangle counts.
-template <int T, int THREADS>
-__device__ __forceinline__ void write_symmetric(const _Float16* sh, _Float16* out, int64_t ld, int64_t r0, int64_t c0) {
-  constexpr int PITCH = T + 8;
-  const bool diag = r0 == c0;
-  for (int c = threadIdx.x; c < T * T / 8; c += THREADS) {
-    const int row = c / (T / 8), col = (c % (T / 8)) * 8;
-    h8 v = *reinterpret_cast<const h8*>(sh + row * PITCH + col), w;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = sh[(col + e) * PITCH + row];
-    if (diag) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = col + e <= row ? v[e] : w[e];
-    } else {
-      *reinterpret_cast<h8*>(out + (c0 + row) * ld + r0 + col) = w;
-    }
-    *reinterpret_cast<h8*>(out + (r0 + row) * ld + c0 + col) = v;
+// A finished tile passes through LDS to leave in whole rows, as it is and transposed. Lanes hold four
+// consecutive columns of a row; `quad_transpose` exchanges them between four lanes (rows), so that lane
+// t of a quad then holds column t of the four. Both go to LDS 8 bytes at a time, 32 lanes to 32 different
+// bank pairs:
+//  * rows of C columns: 16-byte chunk c of row m sits at c ^ swizzle(m), its 8-byte halves swapped
+//    where bit 4 of m is set;
+//  * columns (rows of the transposed tile, R long): chunk c of row n sits at c ^ 4 (n & 3), or with
+//    128-byte rows (two to a sweep of the banks) at c ^ 4 (n / 2 & 1).
+template <int C>
+__device__ __forceinline__ int row_swizzle(int m) { return C == 64 ? (m >> 1) & 7 : m & 15; }
+template <int R>
+__device__ __forceinline__ int col_swizzle(int n) { return R == 64 ? ((n >> 1) & 1) << 2 : (n & 3) << 2; }
+
+template <int C>
+__device__ __forceinline__ void put_row(uint8_t* row, int m, int n, h4 v) {
+  *reinterpret_cast<h4*>(row + (((n >> 3) ^ row_swizzle<C>(m)) << 4) + ((((n >> 2) ^ (m >> 4)) & 1) << 3)) = v;
+}
+template <int C>
+__device__ __forceinline__ h8 get_row(const uint8_t* row, int m, int chunk) {
+  const h8 v = *reinterpret_cast<const h8*>(row + ((chunk ^ row_swizzle<C>(m)) << 4));
+  return m & 16 ? __builtin_shufflevector(v, v, 4, 5, 6, 7, 0, 1, 2, 3) : v;
+}
+__device__ __forceinline__ h4 quad_transpose(h4 v) {
+  const uint2 w = __builtin_bit_cast(uint2, v);
+  const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+  const uint32_t sel = odd ? 0x03020706u : 0x05040100u;
+  const int x0 = __builtin_amdgcn_update_dpp(0, static_cast<int>(w.x), 0xB1, 0xF, 0xF, true);
+  const int x1 = __builtin_amdgcn_update_dpp(0, static_cast<int>(w.y), 0xB1, 0xF, 0xF, true);
+  const uint32_t p0 = __builtin_amdgcn_perm(static_cast<uint32_t>(x0), w.x, sel);
+  const uint32_t p1 = __builtin_amdgcn_perm(static_cast<uint32_t>(x1), w.y, sel);
+  const uint32_t r = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(upper ? p0 : p1), 0x4E, 0xF, 0xF, true));
+  const uint2 o = upper ? make_uint2(r, p1) : make_uint2(p0, r);
+  return __builtin_bit_cast(h4, o);
+}
+// m: the lane's row, n: the column it holds after quad_transpose
+template <int R>
+__device__ __forceinline__ void put_col(uint8_t* row, int m, int n, h4 v) {
+  const int col = m & ~3;
+  *reinterpret_cast<h4*>(row + (((col >> 3) ^ col_swizzle<R>(n)) << 4) + ((col >> 2 & 1) << 3)) = quad_transpose(v);
+}
+template <int R>
+__device__ __forceinline__ h8 get_col(const uint8_t* row, int n, int chunk) {
+  return *reinterpret_cast<const h8*>(row + ((chunk ^ col_swizzle<R>(n)) << 4));
+}
+
+// Row m of a staged tile of R rows with C values: as many rows as fit (a power of two) in each stage buffer.
+template <int STAGE, int R, int C, int FIRST>
+__device__ __forceinline__ uint8_t* staged(const Buffers& bufs, int m) {
+  constexpr int fit = STAGE / (C * 2), per = fit >= R ? R : fit >= 128 ? 128 : fit >= 64 ? 64 : 32, used = R / per;
+  static_assert(fit >= 32 && used <= 4, "whole blocks of rows in up to four buffers");
+  uint8_t* b = bufs.template at<FIRST>();
+  if constexpr (used > 1) b = m / per == 1 ? bufs.template at<FIRST + 1>() : b;
+  if constexpr (used > 2) b = m / per == 2 ? bufs.template at<FIRST + 2>() : b;
+  if constexpr (used > 2) b = m / per == 3 ? bufs.template at<FIRST + 3>() : b;
+  return b + m % per * C * 2;
+}
+
+// Writes a staged BM x BN tile (rows from the first buffer on, transposed from buffer COLS on) to rows r0..
+// and columns c0.. of a symmetric matrix, and its mirror image: of each 64x64 region on or below the
+// diagonal, below it also the image.
+template <int STAGE, int BM, int BN, int THREADS, int COLS>
+__device__ __forceinline__ void write_symmetric(const Buffers& bufs, _Float16* out, int64_t ld, int64_t r0, int64_t c0) {
+#pragma unroll 4
+  for (int u = 0; u < BM * BN / 8 / THREADS; ++u) {
+    const int c = threadIdx.x + u * THREADS;
+    const int row = c / (BN / 8), chunk = c % (BN / 8), n = c / (BM / 8), chunk_m = c % (BM / 8);
+    if ((c0 + chunk * 8) / 64 <= (r0 + row) / 64)
+      *reinterpret_cast<h8*>(out + (r0 + row) * ld + c0 + chunk * 8) = get_row<BN>(staged<STAGE, BM, BN, 0>(bufs, row), row, chunk);
+    if ((c0 + n) / 64 < (r0 + chunk_m * 8) / 64)
+      *reinterpret_cast<h8*>(out + (c0 + n) * ld + r0 + chunk_m * 8) = get_col<BM>(staged<STAGE, BN, BM, COLS>(bufs, n), n, chunk_m);
   }
 }
 
 // ------------------------------------------------------------------------------ G to X
 // Sums of squares of a G, in FP64 (any FP32 value's square is in range): one partial per workgroup.
-constexpr int kNormBlocks = 256, kNormThreads = 512;
+constexpr int kNormBlocks = 512, kNormThreads = 512;
 
 template <typename T>
 __device__ __forceinline__ float value(T v);
@@ -219,25 +398,45 @@ __device__ __forceinline__ double block_sum(double s, double* sh) {
   return s;
 }
 
+// 8 values from p, of any alignment.
+typedef uint32_t u4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ void load_values(const float* p, float (&v)[8]) {
+  const f4_a4 x = *reinterpret_cast<const f4_a4*>(p), y = *reinterpret_cast<const f4_a4*>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = x[e], v[e + 4] = y[e];
+}
+__device__ __forceinline__ void load_values(const uint16_t* p, float (&v)[8]) {
+  const u4_a2 x = *reinterpret_cast<const u4_a2*>(p);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[2 * e] = __uint_as_float(x[e] << 16), v[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
+}
+
 template <typename T>
 __global__ __launch_bounds__(kNormThreads) void ns_norm_kernel(NsArgs a) {
   __shared__ double sh[kNormThreads / 64];
   const T* g = static_cast<const T*>(a.g) + blockIdx.y * a.stride_g;
-  // pieces of a row, `kPiece` values each, dealt over the workgroups in turn
-  constexpr int kPiece = kNormThreads * 8;
-  const int64_t per_row = (a.n + kPiece - 1) / kPiece, pieces = a.m * per_row;
-  double s = 0.0;
-  for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
-    const int64_t row = p / per_row, c0 = (p - row * per_row) * kPiece;
-    const T* src = g + row * a.ldg;
+  // groups of 8 columns, numbered along the rows, dealt to all threads in turn
+  const int64_t per_row = (a.n + 7) / 8, groups = a.m * per_row, all = static_cast<int64_t>(gridDim.x) * kNormThreads;
+  double s0 = 0.0, s1 = 0.0;
+#pragma unroll 4
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x; u < groups; u += all) {
+    const int64_t row = u / per_row, c = (u - row * per_row) * 8;
+    const T* src = g + row * a.ldg + c;
+    float v[8];
+    if (c + 8 <= a.n) {
+      load_values(src, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t c = c0 + i * kNormThreads + threadIdx.x;
-      const double v = c < a.n ? static_cast<double>(value<T>(src[c])) : 0.0;
-      s = __builtin_fma(v, v, s);
+      for (int e = 0; e < 8; ++e) v[e] = c + e < a.n ? value<T>(src[e]) : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      s0 = __builtin_fma(static_cast<double>(v[e]), static_cast<double>(v[e]), s0);
+      s1 = __builtin_fma(static_cast<double>(v[e + 1]), static_cast<double>(v[e + 1]), s1);
     }
   }
-  s = block_sum(s, sh);
+  const double s = block_sum(s0 + s1, sh);
   if (threadIdx.x == 0) a.norm_part[static_cast<int64_t>(blockIdx.y) * kNormBlocks + blockIdx.x] = s;
 }
 
@@ -272,8 +471,8 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
     else sh[r][c] = v;
   }
   __syncthreads();
-  _Float16* xr = a.xr + b * a.x_elems;
-  _Float16* xc = a.xc[0] + b * a.x_elems;
+  _Float16* xr = a.xr + b * a.pp * a.ldq;
+  _Float16* xc = a.xc[0] + b * a.qp * a.ldp;
   for (int t = threadIdx.x; t < kRegion / 8; t += 256) {
     const int r = t >> 3, c = (t & 7) * 8;
     h8 u, v;
@@ -282,8 +481,8 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
       u[e] = static_cast<_Float16>(sh[r][c + e] * kSX);
       v[e] = static_cast<_Float16>(sh[c + e][r] * kSX);
     }
-    *reinterpret_cast<h8*>(xr + (i0 + r) * a.qp + j0 + c) = u;
-    *reinterpret_cast<h8*>(xc + (j0 + r) * a.pp + i0 + c) = v;
+    *reinterpret_cast<h8*>(xr + (i0 + r) * a.ldq + j0 + c) = u;
+    *reinterpret_cast<h8*>(xc + (j0 + r) * a.ldp + i0 + c) = v;
   }
   float* xf = a.xf + b * a.x_elems + ((j0 / 64) * (a.pp / 64) + i0 / 64) * kRegion;
   for (int t = threadIdx.x; t < kRegion / 4; t += 256) {
@@ -293,120 +492,144 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
   }
 }
 
-// ------------------------------------------------------------------------------ A = X X^T
-// Lower tiles; K split over blockIdx.z, whose partial tiles go out as 64x64 regions.
-template <int T, int W, int NST>
-__global__ __launch_bounds__(256) void ns_gram_kernel(NsArgs a, int steps_per_split) {
-  using G = Tile<T, T, W, W, NST>;
-  __shared__ __align__(16) uint8_t b0[G::kStage], b1[G::kStage], b2[NST == 3 ? G::kStage : 16];
-  int ti, tj;
-  triangle(blockIdx.x, ti, tj);
-  const int b = blockIdx.y, split = blockIdx.z;
-  const _Float16* x = a.xr + b * a.x_elems;
-  const int all = static_cast<int>(a.qp / kBK), s0 = split * steps_per_split;
-  typename G::Acc acc;
-  G::zero(acc);
-  G::run(x + static_cast<int64_t>(ti) * T * a.qp, a.qp, x + static_cast<int64_t>(tj) * T * a.qp, a.qp, s0 * kBK,
-         min(steps_per_split, all - s0), b0, b1, b2, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* out = a.part + ((static_cast<int64_t>(b) * gridDim.x + blockIdx.x) * gridDim.z + split) * (T * T);
-  // a wave's W x W part: a whole region, or one block of the tile's only region
+// ------------------------------------------------------------------------------ A = X X^T, B = b A + c A A
+// Four elements (m, n..n+3) of a symmetric product's sums -> what is stored of them.
+// A: the FP32 diagonal aside, FP16 elsewhere.
+__device__ __forceinline__ h4 gram_elements(const NsArgs& a, int b, int64_t m, int64_t n, f4 s) {
+  h4 v;
 #pragma unroll
-  for (int i = 0; i < G::TM; ++i)
+  for (int e = 0; e < 4; ++e) {
+    const bool on = m == n + e;
+    if (on) a.da[b * a.pp + m] = s[e] * (1.0f / (kSX * kSX));
+    v[e] = on ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(s[e] * (kSA / (kSX * kSX)));
+  }
+  return v;
+}
+// B, from the sums of A' A' and A'.
+__device__ __forceinline__ const h4* poly_a16(const NsArgs& a, int b, int64_t m, int64_t n) {
+  return reinterpret_cast<const h4*>(a.a16 + (static_cast<int64_t>(b) * a.pp + m) * a.ldp + n);
+}
+__device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, int64_t n, f4 s, h4 av, float cb, float cc) {
+  const float* d = a.da + b * a.pp;
+  const float dm = d[m];
+  const f4 dn = *reinterpret_cast<const f4*>(d + n);
+  h4 v;
 #pragma unroll
-    for (int j = 0; j < G::TN; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = W == 64 ? wave * kRegion + region_offset(i, j, g, lane) : region_offset(wave >> 1, wave & 1, g, lane);
-        *reinterpret_cast<f4*>(out + at) = f4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-      }
+  for (int e = 0; e < 4; ++e) {
+    const float aa = s[e] * (1.0f / (kSA * kSA)), x = static_cast<float>(av[e]) * (1.0f / kSA);
+    const bool on = m == n + e;
+    if (on) a.db[b * a.pp + m] = cb * dm + cc * (aa + dm * dm);
+    v[e] = on ? static_cast<_Float16>(0.0f) : static_cast<_Float16>((cb * x + cc * (aa + (dm + dn[e]) * x)) * kSB);
+  }
+  return v;
 }
 
-// Sums the splits of one 64x64 region in order, and writes A' (both triangles) and the diagonal.
-template <int T>
-__global__ __launch_bounds__(256) void ns_gram_sum_kernel(NsArgs a, int splits) {
-  constexpr int PITCH = 72, kPer = (T / 64) * (T / 64);
-  __shared__ _Float16 sh[64 * PITCH];
+// The lower tiles of a symmetric product, K = q of X (POLY = false) or p of A' (true). SPLIT: K is cut into
+// gridDim.z parts; each part of a tile leaves as FP32 sums in 64x64 regions, for ns_finish_kernel.
+// Otherwise a workgroup makes a whole tile and finishes it.
+template <int BM, int BN, int WM, int WN, int NST, bool POLY, bool SPLIT>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, float cb, float cc) {
+  using G = Tile<BM, BN, WM, WN, 64, NST>;
+  constexpr int TM = G::TM, TN = G::TN;
+  PF8_NS_BUFFERS(bufs, G, NST);
+  const int b = blockIdx.y;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / (BN / WN), wn = wave % (BN / WN);
+  const int64_t ld = POLY ? a.ldp : a.ldq;
+  const _Float16* x = POLY ? a.a16 + b * a.pp * a.ldp : a.xr + b * a.pp * a.ldq;
+  int ti, tj;
+  triangle_tile<BM, BN>(blockIdx.x, ti, tj);
+  const int64_t r0 = static_cast<int64_t>(ti) * BM, c0 = static_cast<int64_t>(tj) * BN;
+  const int units = static_cast<int>((POLY ? a.pp : a.qp) / 128);  // of 128 values, two stages
+  const int k0 = SPLIT ? static_cast<int>(static_cast<int64_t>(units) * blockIdx.z / gridDim.z) : 0;
+  const int k1 = SPLIT ? static_cast<int>(static_cast<int64_t>(units) * (blockIdx.z + 1) / gridDim.z) : units;
+  auto at = [&](int i, int j, int g, int& m, int& n) {
+    m = wm * WM + 32 * i + (lane & 31);
+    n = wn * WN + 32 * j + 8 * g + 4 * (lane >> 5);
+  };
+  h4 av[POLY && !SPLIT ? TM : 1][TN][4];  // A', read early
+  if constexpr (POLY && !SPLIT) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          int m, n;
+          at(i, j, g, m, n);
+          av[i][j][g] = *poly_a16(a, b, r0 + m, c0 + n);
+        }
+  }
+  typename G::Acc acc;
+  G::zero(acc);
+  G::run(x + r0 * ld, ld, x + c0 * ld, ld, k0 * 128, (k1 - k0) * 2, bufs, acc);
+  float* out = a.part + ((static_cast<int64_t>(b) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) * (BM * BN);
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f4 v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        int m, n;
+        at(i, j, g, m, n);
+        if constexpr (SPLIT) {
+          const int bm = wm * (WM / 32) + i, bn = wn * (WN / 32) + j;  // the block of 32x32 in the tile
+          const int to = (bm / 2 * (BN / 64) + bn / 2) * kRegion + region_offset(bm & 1, bn & 1, g, lane);
+          *reinterpret_cast<f4*>(out + to) = v;
+        } else {
+          h4 h;
+          if constexpr (POLY) h = poly_elements(a, b, r0 + m, c0 + n, v, av[i][j][g], cb, cc);
+          else h = gram_elements(a, b, r0 + m, c0 + n, v);
+          put_row<BN>(staged<G::kStage, BM, BN, 0>(bufs, m), m, n, h);
+          put_col<BM>(staged<G::kStage, BN, BM, NST / 2>(bufs, n + (lane & 3)), m, n + (lane & 3), h);
+        }
+      }
+  if constexpr (!SPLIT) {
+    __syncthreads();
+    write_symmetric<G::kStage, BM, BN, G::kThreads, NST / 2>(bufs, (POLY ? a.b16 : a.a16) + b * a.pp * a.ldp, a.ldp, r0, c0);
+  }
+}
+
+// Adds the parts of one 64x64 region in their order, and writes what is stored of it.
+template <int BM, int BN, bool POLY>
+__global__ __launch_bounds__(256) void ns_finish_kernel(NsArgs a, int tiles, int splits, float cb, float cc) {
+  constexpr int kPer = (BM / 64) * (BN / 64);
+  __shared__ __align__(16) uint8_t rows[64 * 64 * 2], cols[64 * 64 * 2];
+  const Buffers bufs = {rows, cols, rows, rows};
   const int b = blockIdx.y, tile = blockIdx.x / kPer, reg = blockIdx.x % kPer;
   int ti, tj;
-  triangle(tile, ti, tj);
-  const int64_t r0 = ti * T + (reg / (T / 64)) * 64, c0 = tj * T + (reg % (T / 64)) * 64;
-  if (c0 > r0) return;  // in a tile on the diagonal: the mirror image of another region
-  const int tiles = gridDim.x / kPer;
-  const float* in = a.part + ((static_cast<int64_t>(b) * tiles + tile) * splits) * (T * T) + reg * kRegion;
-  float* d = a.da + b * a.pp;
+  triangle_tile<BM, BN>(tile, ti, tj);
+  const int64_t r0 = static_cast<int64_t>(ti) * BM + reg / (BN / 64) * 64, c0 = static_cast<int64_t>(tj) * BN + reg % (BN / 64) * 64;
+  if (c0 > r0) return;  // above the diagonal: the mirror image of another region
+  const int64_t step = static_cast<int64_t>(tiles) * (BM * BN);
+  const float* in = a.part + static_cast<int64_t>(b) * splits * step + static_cast<int64_t>(tile) * (BM * BN) + reg * kRegion;
+  f4 s[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) s[u] = *reinterpret_cast<const f4*>(in + (threadIdx.x + 256 * u) * 4);
+  for (int k = 1; k < splits; ++k)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s[u] += *reinterpret_cast<const f4*>(in + k * step + (threadIdx.x + 256 * u) * 4);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int t = threadIdx.x + 256 * u;
     const int lane = t & 63, g = (t >> 6) & 3, bj = (t >> 8) & 1, bi = t >> 9;
-    f4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < splits; ++k) s += *reinterpret_cast<const f4*>(in + static_cast<int64_t>(k) * (T * T) + t * 4);
     const int m = 32 * bi + (lane & 31), n = 32 * bj + 8 * g + 4 * (lane >> 5);
-    h4 v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool on = r0 + m == c0 + n + e;
-      if (on) d[r0 + m] = s[e] * (1.0f / (kSX * kSX));
-      v[e] = on ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(s[e] * (kSA / (kSX * kSX)));
-    }
-    *reinterpret_cast<h4*>(sh + m * PITCH + n) = v;
+    h4 h;
+    if constexpr (POLY) h = poly_elements(a, b, r0 + m, c0 + n, s[u], *poly_a16(a, b, r0 + m, c0 + n), cb, cc);
+    else h = gram_elements(a, b, r0 + m, c0 + n, s[u]);
+    put_row<64>(rows + m * 128, m, n, h);
+    put_col<64>(cols + (n + (lane & 3)) * 128, m, n + (lane & 3), h);
   }
   __syncthreads();
-  write_symmetric<64, 256>(sh, a.a16 + static_cast<int64_t>(b) * a.pp * a.pp, a.pp, r0, c0);
-}
-
-// ------------------------------------------------------------------------------ B = b A + c A A
-template <int T, int W, int NST>
-__global__ __launch_bounds__(256) void ns_poly_kernel(NsArgs a, float cb, float cc) {
-  using G = Tile<T, T, W, W, NST>;
-  __shared__ __align__(16) uint8_t b0[G::kStage], b1[G::kStage], b2[NST == 3 ? G::kStage : 16];
-  __shared__ _Float16 sh[T * (T + 8)];
-  int ti, tj;
-  triangle(blockIdx.x, ti, tj);
-  const int b = blockIdx.y;
-  const int64_t r0 = static_cast<int64_t>(ti) * T, c0 = static_cast<int64_t>(tj) * T;
-  const _Float16* A = a.a16 + static_cast<int64_t>(b) * a.pp * a.pp;
-  typename G::Acc acc;
-  G::zero(acc);
-  G::run(A + r0 * a.pp, a.pp, A + c0 * a.pp, a.pp, 0, static_cast<int>(a.pp / kBK), b0, b1, b2, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave / (T / W), wn = wave % (T / W);
-  const float* d = a.da + b * a.pp;
-#pragma unroll
-  for (int i = 0; i < G::TM; ++i) {
-    const int m = wm * W + 32 * i + (lane & 31);
-    const float dm = d[r0 + m];
-#pragma unroll
-    for (int j = 0; j < G::TN; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = wn * W + 32 * j + 8 * g + 4 * (lane >> 5);
-        const f4 dn = *reinterpret_cast<const f4*>(d + c0 + n);
-        const h4 av = *reinterpret_cast<const h4*>(A + (r0 + m) * a.pp + c0 + n);
-        h4 v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float aa = acc[i][j][4 * g + e] * (1.0f / (kSA * kSA));
-          const float x = static_cast<float>(av[e]) * (1.0f / kSA);
-          if (r0 + m == c0 + n + e) {
-            a.db[b * a.pp + r0 + m] = cb * dm + cc * (aa + dm * dm);
-            v[e] = static_cast<_Float16>(0.0f);
-          } else {
-            v[e] = static_cast<_Float16>((cb * x + cc * (aa + (dm + dn[e]) * x)) * kSB);
-          }
-        }
-        *reinterpret_cast<h4*>(sh + m * (T + 8) + n) = v;
-      }
-  }
-  __syncthreads();
-  write_symmetric<T, 256>(sh, a.b16 + static_cast<int64_t>(b) * a.pp * a.pp, a.pp, r0, c0);
+  write_symmetric<64 * 64 * 2, 64, 64, 256, 1>(bufs, (POLY ? a.b16 : a.a16) + b * a.pp * a.ldp, a.ldp, r0, c0);
 }
 
 // ------------------------------------------------------------------------------ X <- a X + B X
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)); }
 
 // The first n of 8 BF16 patterns (held as FP16 bits) to a row of any alignment.
-typedef uint32_t u4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void store_row(uint16_t* p, h8 v, int64_t n) {
   typedef uint16_t us8 __attribute__((ext_vector_type(8)));
   if (n >= 8) {
@@ -419,13 +642,13 @@ __device__ __forceinline__ void store_row(uint16_t* p, h8 v, int64_t n) {
     if (e < n) p[e] = w[e];
 }
 
-template <int BM, int BN, int W, int NST, bool LAST>
-__global__ __launch_bounds__(64 * (BM / W) * (BN / W)) void ns_update_kernel(NsArgs a, float ca, int turn) {
-  const float own_from = kOwnRow * __builtin_fabsf(ca - 1.0f);
-  using G = Tile<BM, BN, W, W, NST>;
-  constexpr int PITCH = BN + 8;
-  __shared__ __align__(16) uint8_t b0[G::kStage], b1[G::kStage], b2[NST == 3 ? G::kStage : 16];
-  __shared__ _Float16 sh[BM * PITCH];
+// X's FP32 values are read before the product, so that they arrive behind its first stages.
+template <int BM, int BN, int WM, int WN, int BK, int NST, bool LAST>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, int turn) {
+  using G = Tile<BM, BN, WM, WN, BK, NST>;
+  constexpr int TM = G::TM, TN = G::TN;
+  PF8_NS_BUFFERS(bufs, G, NST);
+  const bool tall = a.m > a.n;
   const int b = blockIdx.y;
   const int tiles_p = static_cast<int>(a.pp / BN);
   int bid = blockIdx.x;
@@ -435,67 +658,91 @@ __global__ __launch_bounds__(64 * (BM / W) * (BN / W)) void ns_update_kernel(NsA
     bid = xcd * q + min(xcd, rem) + (bid >> 3);
   }
   const int64_t j0 = static_cast<int64_t>(bid / tiles_p) * BM, i0 = static_cast<int64_t>(bid % tiles_p) * BN;
-  const _Float16* xc = a.xc[turn] + b * a.x_elems;
-  const _Float16* B = a.b16 + static_cast<int64_t>(b) * a.pp * a.pp;
+  const _Float16* xc = a.xc[turn] + b * a.qp * a.ldp;
+  const _Float16* B = a.b16 + b * a.pp * a.ldp;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / (BN / WN), wn = wave % (BN / WN);
+  auto x_at = [&](int i, int j, int g) {
+    const int m = wm * WM + 32 * i, n = wn * WN + 32 * j;
+    const int64_t region = ((j0 + m) / 64) * (a.pp / 64) + (i0 + n) / 64;
+    return reinterpret_cast<f4*>(a.xf + b * a.x_elems + region * kRegion + region_offset((m >> 5) & 1, (n >> 5) & 1, g, lane));
+  };
+  constexpr bool kEarly = TM * TN <= 4;  // more would not fit the registers
+  f4 x[kEarly ? TM : 1][kEarly ? TN : 1][4];
+  if constexpr (kEarly) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) x[i][j][g] = *x_at(i, j, g);
+  }
   typename G::Acc acc;
   G::zero(acc);
-  G::run(xc + j0 * a.pp, a.pp, B + i0 * a.pp, a.pp, 0, static_cast<int>(a.pp / kBK), b0, b1, b2, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave / (BN / W), wn = wave % (BN / W);
-  const float* d = a.db + b * a.pp;
+  G::run(xc + j0 * a.ldp, a.ldp, B + i0 * a.ldp, a.ldp, 0, static_cast<int>(a.pp / BK), bufs, acc);
+
+  const float own_from = kOwnRow * __builtin_fabsf(ca - 1.0f);
+  const float* d = a.db + b * a.pp + i0;
+  h4 v[TM][TN][4];
 #pragma unroll
-  for (int i = 0; i < G::TM; ++i) {
-    const int m = wm * W + 32 * i;  // j0 + m + lane % 32
+  for (int j = 0; j < TN; ++j)
 #pragma unroll
-    for (int j = 0; j < G::TN; ++j)
+    for (int g = 0; g < 4; ++g) {
+      const f4 dn = *reinterpret_cast<const f4*>(d + wn * WN + 32 * j + 8 * g + 4 * (lane >> 5));
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = wn * W + 32 * j;
-        const int64_t region = ((j0 + m) / 64) * (a.pp / 64) + (i0 + n) / 64;
-        float* xf = a.xf + b * a.x_elems + region * kRegion + region_offset((m >> 5) & 1, (n >> 5) & 1, g, lane);
-        const int nn = n + 8 * g + 4 * (lane >> 5);
-        const f4 dn = *reinterpret_cast<const f4*>(d + i0 + nn);
-        f4 x = *reinterpret_cast<const f4*>(xf);
-        h4 v;
+      for (int i = 0; i < TM; ++i) {
+        f4 y;
+        if constexpr (kEarly) y = x[i][j][g];
+        else y = *x_at(i, j, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float low = static_cast<float>(static_cast<_Float16>(x[e] * kSX)) * (1.0f / kSX);
-          const float xd = __builtin_fabsf(dn[e]) > own_from ? x[e] : low;
-          x[e] = ca * x[e] + (dn[e] * xd + acc[i][j][4 * g + e] * (1.0f / (kSX * kSB)));
-          if (LAST) v[e] = __builtin_bit_cast(_Float16, bf16_bits(x[e]));
-          else v[e] = static_cast<_Float16>(x[e] * kSX);
+          const float low = static_cast<float>(static_cast<_Float16>(y[e] * kSX)) * (1.0f / kSX);
+          const float yd = __builtin_fabsf(dn[e]) > own_from ? y[e] : low;
+          y[e] = ca * y[e] + (dn[e] * yd + acc[i][j][4 * g + e] * (1.0f / (kSX * kSB)));
+          if (LAST) v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y[e]));
+          else v[i][j][g][e] = static_cast<_Float16>(y[e] * kSX);
         }
-        if (!LAST) *reinterpret_cast<f4*>(xf) = x;
-        *reinterpret_cast<h4*>(sh + (m + (lane & 31)) * PITCH + nn) = v;
-      }
-  }
-  __syncthreads();
-  const bool tall = a.m > a.n;
-  _Float16* next = a.xc[turn ^ 1] + b * a.x_elems;
-  _Float16* xr = a.xr + b * a.x_elems;
-  uint16_t* out = a.out + b * a.stride_o;
-  if (!LAST || tall) {
-    for (int c = threadIdx.x; c < BM * BN / 8; c += G::kThreads) {
-      const int row = c / (BN / 8), col = (c % (BN / 8)) * 8;
-      const h8 v = *reinterpret_cast<const h8*>(sh + row * PITCH + col);
-      if (!LAST) {
-        *reinterpret_cast<h8*>(next + (j0 + row) * a.pp + i0 + col) = v;
-      } else if (j0 + row < a.m) {
-        store_row(out + (j0 + row) * a.ldo + i0 + col, v, a.n - (i0 + col));
+        if (!LAST) *x_at(i, j, g) = y;
       }
     }
+  // out through LDS, as rows of X^T and as rows of X
+  auto each_piece = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) f(wm * WM + 32 * i + (lane & 31), wn * WN + 32 * j + 8 * g + 4 * (lane >> 5), v[i][j][g]);
+  };
+  constexpr int kPieces = BM * BN / 8 / G::kThreads;
+  uint16_t* out = a.out + b * a.stride_o;
+  if (!LAST || tall) {
+    each_piece([&](int m, int n, h4 w) { put_row<BN>(staged<G::kStage, BM, BN, 0>(bufs, m), m, n, w); });
+    __syncthreads();
+    _Float16* next = a.xc[turn ^ 1] + b * a.qp * a.ldp;
+#pragma unroll 4
+    for (int u = 0; u < kPieces; ++u) {
+      const int c = threadIdx.x + u * G::kThreads, row = c / (BN / 8), chunk = c % (BN / 8), col = chunk * 8;
+      const h8 w = get_row<BN>(staged<G::kStage, BM, BN, 0>(bufs, row), row, chunk);
+      if (!LAST) *reinterpret_cast<h8*>(next + (j0 + row) * a.ldp + i0 + col) = w;
+      else if (j0 + row < a.m) store_row(out + (j0 + row) * a.ldo + i0 + col, w, a.n - (i0 + col));
+    }
+    if (!LAST) __syncthreads();
   }
   if (!LAST || !tall) {
-    for (int c = threadIdx.x; c < BM * BN / 8; c += G::kThreads) {
-      const int row = c / (BM / 8), col = (c % (BM / 8)) * 8;  // row of X, columns of X
-      h8 v;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = sh[(col + e) * PITCH + row];
-      if (!LAST) {
-        *reinterpret_cast<h8*>(xr + (i0 + row) * a.qp + j0 + col) = v;
-      } else if (i0 + row < a.m) {
-        store_row(out + (i0 + row) * a.ldo + j0 + col, v, a.n - (j0 + col));
-      }
+    each_piece([&](int m, int n, h4 w) {
+      const int nt = n + (lane & 3);
+      put_col<BM>(staged<G::kStage, BN, BM, 0>(bufs, nt), m, nt, w);
+    });
+    __syncthreads();
+    _Float16* xr = a.xr + b * a.pp * a.ldq;
+#pragma unroll 4
+    for (int u = 0; u < kPieces; ++u) {
+      const int c = threadIdx.x + u * G::kThreads, row = c / (BM / 8), chunk = c % (BM / 8), col = chunk * 8;  // row of X
+      const h8 w = get_col<BM>(staged<G::kStage, BN, BM, 0>(bufs, row), row, chunk);
+      if (!LAST) *reinterpret_cast<h8*>(xr + (i0 + row) * a.ldq + j0 + col) = w;
+      else if (i0 + row < a.m) store_row(out + (i0 + row) * a.ldo + j0 + col, w, a.n - (j0 + col));
     }
   }
 }
@@ -646,27 +893,60 @@ __global__ __launch_bounds__((P / 32) * (P / 32) * 64) void ns_small_kernel(NsAr
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
-// How a size is run: tile edges of the three products and the splits of A's.
+// How a size is run. Tile shapes are chosen by the time that a model of the kernels gives: a card's 256 CUs
+// take one workgroup each (two of 64x64), a stage of 64 K values costs a workgroup 0.34 us (128x128), 0.5 us
+// (128x256) or 0.3 us (64x64, two on a CU; 0.14 us alone), and a launch with its first loads and its last
+// stores the rest. Measured against it, for the lower triangle of 2048 x 2048 with K = 2048 / 12288:
+// 64x64 22.2 / 124 us, 128x128 18.9 / 73 us, 128x256 with K in two parts 21.5 / 67 us; of 1024 x 1024 with
+// K = 1664: 64x64 7.0 us, 128x128 13.9 us. Update of 2048 x 2048: 128x128 23.5 us, 128x256 29.2 us, 64x64
+// 42.4 us; of 12288 x 2048: 154, 114 and 239 us.
+enum Shape { k64x64, k128x128, k128x256 };
 struct Plan {
   int64_t pp, qp;
-  int gram_tile, gram_splits, gram_steps, poly_tile, update_tile;
-  int64_t gram_tiles() const { return tri(gram_tile); }
-  int64_t tri(int t) const { return (pp / t) * (pp / t + 1) / 2; }
+  Shape gram, poly, update;
+  int gram_splits, poly_splits;  // parts of K; more than one only with 128x256 tiles
 };
+
+// Tiles of a shape that cover the lower triangle.
+int64_t triangle_tiles(Shape s, int64_t pp) {
+  const int64_t n = pp / (s == k128x256 ? 256 : s == k64x64 ? 64 : 128);
+  return n * (n + 1) / 2 * (s == k128x256 ? 2 : 1);
+}
+
+int64_t rounds(int64_t tiles, int64_t slots) { return (tiles + slots - 1) / slots; }
+
+void plan_sym(int64_t pp, int64_t batch, int64_t k, Shape& shape, int& splits) {
+  const double stages = static_cast<double>(k / 64);
+  const int64_t t64 = batch * triangle_tiles(k64x64, pp), t128 = batch * triangle_tiles(k128x128, pp);
+  double best = t64 <= 256 ? 4.0 + 0.14 * stages : 5.0 + 0.3 * stages * static_cast<double>(rounds(t64, 512));
+  shape = k64x64;
+  splits = 1;
+  const double c128 = 8.0 + 0.34 * stages * static_cast<double>(rounds(t128, 256));
+  if (c128 < best) best = c128, shape = k128x128;
+  if (pp % 256) return;
+  for (int s = 1; s <= 8 && s <= k / 512; ++s) {
+    const int64_t parts = batch * triangle_tiles(k128x256, pp) * s;
+    // the parts are written and read again: 128 KiB each, at 4 TB/s in all
+    const double c = 12.0 + 0.5 * stages / s * static_cast<double>(rounds(parts, 256)) + 0.032 * static_cast<double>(parts);
+    if (c < best) best = c, shape = k128x256, splits = s;
+  }
+}
 
 Plan plan_of(int64_t batch, int64_t m, int64_t n) {
   Plan p;
-  p.pp = round_up(m < n ? m : n, 128);
-  p.qp = round_up(m < n ? n : m, 128);
-  p.update_tile = batch * (p.pp / 128) * (p.qp / 128) >= 256 ? 128 : 64;
-  p.poly_tile = batch * p.tri(128) >= 256 ? 128 : 64;
-  const int64_t steps = p.qp / kBK;
-  p.gram_tile = batch * p.tri(128) >= 64 ? 128 : 64;
-  int64_t splits = 512 / (batch * p.tri(p.gram_tile));
-  splits = splits < 1 ? 1 : splits;
-  if (splits > steps / 4) splits = steps / 4 < 1 ? 1 : steps / 4;
-  p.gram_steps = static_cast<int>((steps + splits - 1) / splits);
-  p.gram_splits = static_cast<int>((steps + p.gram_steps - 1) / p.gram_steps);
+  const int64_t shorter = m < n ? m : n, longer = m < n ? n : m;
+  p.pp = round_up(shorter, shorter > 1024 ? 256 : 128);
+  p.qp = round_up(longer, 128);
+  const double stages = static_cast<double>(p.pp / 64);
+  const int64_t t128 = batch * (p.pp / 128) * (p.qp / 128);
+  // the update also reads and writes X: a round of tiles has 8 (14) us of that behind its products
+  const double c64 = 5.0 + (0.3 * stages + 6.0) * static_cast<double>(rounds(4 * t128, 512));
+  const double c128 = 6.0 + (0.34 * stages + 8.0) * static_cast<double>(rounds(t128, 256));
+  const double c256 = 6.0 + (0.5 * stages + 14.0) * static_cast<double>(rounds(t128 / 2, 256));
+  p.update = c64 < c128 ? k64x64 : k128x128;
+  if (p.pp % 256 == 0 && c256 < std::min(c64, c128)) p.update = k128x256;
+  plan_sym(p.pp, batch, p.qp, p.gram, p.gram_splits);
+  plan_sym(p.pp, batch, p.pp, p.poly, p.poly_splits);
   return p;
 }
 
@@ -697,9 +977,32 @@ int64_t align256(int64_t v) { return round_up(v, 256); }
 
 }  // namespace
 
+template <bool POLY>
+static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, float cb, float cc, hipStream_t stream) {
+  const uint32_t tiles = static_cast<uint32_t>(triangle_tiles(shape, a.pp));
+  const dim3 grid(tiles, batch, static_cast<uint32_t>(splits));
+  if (shape == k64x64) {
+    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
+  } else if (shape == k128x128) {
+    hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
+  } else {
+    hipLaunchKernelGGL((ns_sym_kernel<128, 256, 64, 64, 3, POLY, true>), grid, dim3(512), 0, stream, a, cb, cc);
+    hipLaunchKernelGGL((ns_finish_kernel<128, 256, POLY>), dim3(tiles * 8, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
+  }
+}
+
+template <bool LAST>
+static void launch_update(const NsArgs& a, Shape shape, uint32_t batch, float ca, int turn, hipStream_t stream) {
+  const int64_t bm = shape == k64x64 ? 64 : 128, bn = shape == k64x64 ? 64 : shape == k128x128 ? 128 : 256;
+  const dim3 grid(static_cast<uint32_t>((a.qp / bm) * (a.pp / bn)), batch);
+  if (shape == k64x64) hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 32, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
+  else if (shape == k128x128) hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 64, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
+  else hipLaunchKernelGGL((ns_update_kernel<128, 256, 64, 64, 64, 3, LAST>), grid, dim3(512), 0, stream, a, ca, turn);
+}
+
 // Workspace parts, in order: FP32 X, two Xc, Xr, A, B, their diagonals, A's partial tiles, norms.
 static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base) {
-  const int64_t x = p.pp * p.qp, s = p.pp * p.pp;
+  const int64_t x = p.pp * p.qp, ldp = p.pp + kPad, ldq = p.qp + kPad;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     uint8_t* r = base + at;
@@ -707,17 +1010,19 @@ static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base)
     return r;
   };
   uint8_t* xf = take(batch * x * 4);
-  uint8_t* xc0 = take(batch * x * 2);
-  uint8_t* xc1 = take(batch * x * 2);
-  uint8_t* xr = take(batch * x * 2);
-  uint8_t* a16 = take(batch * s * 2);
-  uint8_t* b16 = take(batch * s * 2);
+  uint8_t* xc0 = take(batch * p.qp * ldp * 2);
+  uint8_t* xc1 = take(batch * p.qp * ldp * 2);
+  uint8_t* xr = take(batch * p.pp * ldq * 2);
+  uint8_t* a16 = take(batch * p.pp * ldp * 2);
+  uint8_t* b16 = take(batch * p.pp * ldp * 2);
   uint8_t* da = take(batch * p.pp * 4);
   uint8_t* db = take(batch * p.pp * 4);
-  uint8_t* part = take(batch * p.gram_tiles() * p.gram_splits * p.gram_tile * p.gram_tile * 4);
+  auto parts = [&](Shape shape, int splits) { return shape == k128x256 ? triangle_tiles(shape, p.pp) * splits * 128 * 256 : 0; };
+  const int64_t gram = parts(p.gram, p.gram_splits), poly = parts(p.poly, p.poly_splits);
+  uint8_t* part = take(batch * std::max(gram, poly) * 4);
   uint8_t* norm = take(batch * kNormBlocks * 8);
   if (a) {
-    a->pp = p.pp, a->qp = p.qp, a->x_elems = x;
+    a->pp = p.pp, a->qp = p.qp, a->ldp = ldp, a->ldq = ldq, a->x_elems = x;
     a->xf = reinterpret_cast<float*>(xf);
     a->xc[0] = reinterpret_cast<_Float16*>(xc0), a->xc[1] = reinterpret_cast<_Float16*>(xc1);
     a->xr = reinterpret_cast<_Float16*>(xr);
@@ -755,27 +1060,10 @@ hipError_t launch_newton_schulz(NsArgs a, int64_t batch, int steps, const float*
   if (hipError_t e = hipGetLastError()) return e;
   for (int s = 0; s < steps; ++s) {
     const float ca = coef[3 * s], cb = coef[3 * s + 1], cc = coef[3 * s + 2];
-    const dim3 gg(static_cast<uint32_t>(p.gram_tiles()), nb, static_cast<uint32_t>(p.gram_splits));
-    if (p.gram_tile == 128) {
-      hipLaunchKernelGGL((ns_gram_kernel<128, 64, 2>), gg, dim3(256), 0, stream, a, p.gram_steps);
-      hipLaunchKernelGGL((ns_gram_sum_kernel<128>), dim3(gg.x * 4, nb), dim3(256), 0, stream, a, p.gram_splits);
-    } else {
-      hipLaunchKernelGGL((ns_gram_kernel<64, 32, 3>), gg, dim3(256), 0, stream, a, p.gram_steps);
-      hipLaunchKernelGGL((ns_gram_sum_kernel<64>), dim3(gg.x, nb), dim3(256), 0, stream, a, p.gram_splits);
-    }
-    const dim3 pg(static_cast<uint32_t>(p.tri(p.poly_tile)), nb);
-    if (p.poly_tile == 128) hipLaunchKernelGGL((ns_poly_kernel<128, 64, 2>), pg, dim3(256), 0, stream, a, cb, cc);
-    else hipLaunchKernelGGL((ns_poly_kernel<64, 32, 3>), pg, dim3(256), 0, stream, a, cb, cc);
-    const int64_t t = p.update_tile;
-    const dim3 ug(static_cast<uint32_t>((p.qp / t) * (p.pp / t)), nb);
-    const int turn = s & 1;
-    if (t == 128) {
-      if (s + 1 < steps) hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 2, false>), ug, dim3(256), 0, stream, a, ca, turn);
-      else hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 2, true>), ug, dim3(256), 0, stream, a, ca, turn);
-    } else {
-      if (s + 1 < steps) hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 3, false>), ug, dim3(256), 0, stream, a, ca, turn);
-      else hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 3, true>), ug, dim3(256), 0, stream, a, ca, turn);
-    }
+    launch_sym<false>(a, p.gram, p.gram_splits, nb, cb, cc, stream);
+    launch_sym<true>(a, p.poly, p.poly_splits, nb, cb, cc, stream);
+    if (s + 1 < steps) launch_update<false>(a, p.update, nb, ca, s & 1, stream);
+    else launch_update<true>(a, p.update, nb, ca, s & 1, stream);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
