@@ -24,7 +24,7 @@ PF8_ALONG_COLS, PF8_ALONG_ROWS = 0, 1
 PF8_FPROP, PF8_DGRAD, PF8_WGRAD = 0, 1, 2
 PF8_GEMM_AUTO, PF8_GEMM_MX_SCALED, PF8_GEMM_PROMOTE = 0, 1, 2
 PF8_BF16, PF8_F32 = 0, 1
-PF8_NORM_MAX_COLS = 32768
+PF8_NORM_MAX_COLS = 16384
 PF8_NS_MAX_SHORT, PF8_NS_MAX_LONG, PF8_NS_MAX_BATCH, PF8_NS_MAX_STEPS = 32768, 1048576, 65535, 64
 ABI_VERSION = 6
 

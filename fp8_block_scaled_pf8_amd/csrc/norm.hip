@@ -84,27 +84,26 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// Sums of N values over the L threads of a row. With several waves they meet in `slot`, N floats
-// per wave; consecutive reductions take turns between two slots, so one barrier each is enough: a
-// slot is written again only after the barrier of the reduction in between, which every thread
-// reaches after it has read the slot.
-template <int L, int N>
+// Sums of N values over the threads of a row: one wave (SINGLE), or the whole workgroup. With several
+// waves they meet in `slot`, N floats per wave; consecutive reductions take turns between two slots, so
+// one barrier each is enough: a slot is written again only after the barrier of the reduction in
+// between, which every thread reaches after it has read the slot.
+template <bool SINGLE, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* slot) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (L > 64) {
-    const int wave = threadIdx.x >> 6;
+  if constexpr (!SINGLE) {
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) slot[wave * N + i] = v[i];
+      for (int i = 0; i < N; ++i) slot[(threadIdx.x >> 6) * N + i] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = 0.0f;
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+    const int waves = blockDim.x >> 6;
+    for (int w = 0; w < waves; ++w) {
 #pragma unroll
-      for (int w = 0; w < L / 64; ++w) s += slot[w * N + i];
-      v[i] = s;
+      for (int i = 0; i < N; ++i) v[i] += slot[w * N + i];
     }
   }
 }
@@ -119,119 +118,170 @@ __device__ __forceinline__ float add_sq(float v, float sq, float s) {
   return __builtin_fmaf(t, t, s);
 }
 
-// L threads per row, NV steps of 8 values per thread.
-template <int L, int NV>
-__global__ __launch_bounds__(L < 256 ? 256 : L) void norm_fwd_kernel(NormFwdArgs a) {
-  constexpr int THREADS = L < 256 ? 256 : L, RPB = THREADS / L;
-  __shared__ float slots[2][L > 64 ? L / 64 : 1];
-  const NormArgs& p = a.in;
-  const int t = threadIdx.x % L;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / L;
-  if (RPB > 1 && row >= p.rows) return;  // whole waves only (one row per wave)
-  const int cols = p.cols;
-
-  uint4 hv[NV], yv[NV], gv[NV];
-  const bool branch = p.y != nullptr, full_gate = p.gate != nullptr && p.ld_gate != 0;
+// A thread's part of a row: NV steps of 8 values, `span` threads of the row apart.
+template <int NV>
+struct Cols {
+  int c[NV], n[NV];  // first column, and how many there are from it on
+  __device__ __forceinline__ Cols(int t, int span, int cols) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = 8 * (t + i * L), n = cols - c;
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    hv[i] = yv[i] = gv[i] = z;
-    if (n > 0) {
-      hv[i] = load8(p.h + row * p.ldh + c, n);
-      if (branch) yv[i] = load8(p.y + row * p.ldy + c, n);
-      if (full_gate) gv[i] = load8(static_cast<const uint16_t*>(p.gate) + row * p.ld_gate + c, n);
+    for (int i = 0; i < NV; ++i) c[i] = 8 * (t + i * span), n[i] = cols - c[i];
+  }
+  __device__ __forceinline__ void load(const uint16_t* row, uint4 (&v)[NV]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (n[i] > 0) v[i] = load8(row + c[i], n[i]);
     }
   }
+};
 
-  float r[NV][8];
-  if (branch) {
-    float rho_y = 1.0f;
-    if (p.w_post) {
-      float s[1] = {0.0f};
+// A [cols] vector's values at a thread's columns: kept in registers over the rows where they are few.
+template <int NV, bool KEEP>
+struct Weights {
+  static constexpr bool kKeep = KEEP;
+  const void* w;
+  int wf32;
+  float offset;
+  float kept[kKeep ? NV : 1][8];
+  __device__ __forceinline__ Weights(const void* w_, int wf32_, float offset_, const Cols<NV>& at) : w(w_), wf32(wf32_), offset(offset_) {
+    if constexpr (kKeep) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float y[8];
-        unpack8(yv[i], y);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s[0] = add_sq(y[k], p.sq, s[0]);
+        for (int k = 0; k < 8; ++k) kept[i][k] = 1.0f;
+        if (w && at.n[i] > 0) load_w8(w, wf32, at.c[i], at.n[i], offset, kept[i]);
       }
-      row_sum<L, 1>(s, slots[0]);
-      rho_y = inv_rms(s[0], p);
     }
+  }
+  // (1 without a vector)
+  __device__ __forceinline__ void get(int i, const Cols<NV>& at, float (&f)[8]) const {
+    if constexpr (kKeep) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (t + i * L), n = cols - c;
-      float h[8], y[8];
-      unpack8(hv[i], h);
-      unpack8(yv[i], y);
-      if (p.w_post && n > 0) {
-        float w[8];
-        load_w8(p.w_post, p.wf32, c, n, p.offset, w);
+      for (int k = 0; k < 8; ++k) f[k] = kept[i][k];
+    } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = y[k] * rho_y * w[k];
-      }
-      if (p.gate && n > 0) {
-        float g[8];
-        if (full_gate) unpack8(gv[i], g);
-        else load_w8(p.gate, p.wf32, c, n, 0.0f, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= g[k];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r[i][k] = p.residual_scale * h[k] + p.branch_scale * y[k];
+      for (int k = 0; k < 8; ++k) f[k] = 1.0f;
+      if (w && at.n[i] > 0) load_w8(w, wf32, at.c[i], at.n[i], offset, f);
     }
-  } else {
+  }
+};
+
+// Forward. A row belongs to a wave (SINGLE: four rows a workgroup) or to the workgroup; workgroups walk
+// the rows, and (AHEAD) the next row's values are on their way while one is worked on.
+template <bool SINGLE, int NV, int THREADS, bool AHEAD>
+__global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
+  __shared__ float slots[2][SINGLE ? 1 : THREADS / 64];
+  const NormArgs& p = a.in;
+  const int span = SINGLE ? 64 : blockDim.x, t = SINGLE ? threadIdx.x & 63 : threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (SINGLE ? THREADS / 64 : 1);
+  const Cols<NV> at(t, span, p.cols);
+  const bool branch = p.y != nullptr, full_gate = p.gate != nullptr && p.ld_gate != 0, post = p.w_post != nullptr;
+  const Weights<NV, AHEAD> w_pre(p.w_pre, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
+      gate(full_gate ? nullptr : p.gate, p.wf32, 0.0f, at);
+
+  uint4 hv[NV], yv[NV], gv[NV], hn[NV], yn[NV], gn[NV];
+  auto load_row = [&](int64_t row, uint4 (&h)[NV], uint4 (&y)[NV], uint4 (&g)[NV]) {
+    at.load(p.h + row * p.ldh, h);
+    if (branch) at.load(p.y + row * p.ldy, y);
+    if (full_gate) at.load(static_cast<const uint16_t*>(p.gate) + row * p.ld_gate, g);
+  };
+  int64_t row = SINGLE ? static_cast<int64_t>(blockIdx.x) * (THREADS / 64) + (threadIdx.x >> 6) : blockIdx.x;
+  if (AHEAD && row < p.rows) load_row(row, hn, yn, gn);
+  for (; row < p.rows; row += step) {
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) hv[i] = hn[i], yv[i] = yn[i], gv[i] = gn[i];
+      if (row + step < p.rows) load_row(row + step, hn, yn, gn);
+    } else {
+      load_row(row, hv, yv, gv);
+    }
+
+    float r[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) unpack8(hv[i], r[i]);
-  }
-  if (a.r) {
+    if (branch) {
+      float rho_y = 1.0f;
+      if (post) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float y[8];
+          unpack8(yv[i], y);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s[0] = add_sq(y[k], p.sq, s[0]);
+        }
+        row_sum<SINGLE, 1>(s, slots[0]);
+        rho_y = inv_rms(s[0], p);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float y[8], w[8];
+        unpack8(yv[i], y);
+        if (post) {
+          w_post.get(i, at, w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = y[k] * rho_y * w[k];
+        }
+        if (full_gate) unpack8(gv[i], w);
+        else gate.get(i, at, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) r[i][k] = p.residual_scale * r[i][k] + p.branch_scale * (w[k] * y[k]);
+      }
+    }
+    if (a.r) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (at.n[i] > 0) store8(a.r + row * a.ldr + at.c[i], pack8(r[i]), at.n[i]);
+    }
+    if (!p.w_pre) {
+      if (!SINGLE) __syncthreads();  // slot 0 has been read
+      continue;
+    }
+
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        // the places behind the row's end hold zeros (times finite scales)
+        s[0] = add_sq(r[i][k], p.sq, s[0]);
+    row_sum<SINGLE, 1>(s, slots[1]);
+    // without a norm behind the branch, slot 1 alone is used: a barrier before it is written again
+    if (!SINGLE && !(branch && post)) __syncthreads();
+    const float rho_r = inv_rms(s[0], p);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (t + i * L), n = cols - c;
-      if (n > 0) store8(a.r + row * a.ldr + c, pack8(r[i]), n);
-    }
-  }
-  if (!p.w_pre) return;
-
-  float s[1] = {0.0f};
+      if (at.n[i] <= 0) continue;
+      float w[8];
+      w_pre.get(i, at, w);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      // the places behind the row's end hold zeros (times finite scales)
-      s[0] = add_sq(r[i][k], p.sq, s[0]);
-  row_sum<L, 1>(s, slots[1]);
-  const float rho_r = inv_rms(s[0], p);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = 8 * (t + i * L), n = cols - c;
-    if (n <= 0) continue;
-    float w[8];
-    load_w8(p.w_pre, p.wf32, c, n, p.offset, w);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = r[i][k] * rho_r * w[k];
-    const uint4 v = pack8(w);
-    if (a.x) store8(a.x + row * a.ldx + c, v, n);
-    if (a.q) {
-      // a 1x128 group is 16 consecutive threads; cols is a multiple of 128, so they are all here
-      const int e = block_exponent(row16_max(amax8_bits(v)));
-      *reinterpret_cast<uint2*>(a.q + row * a.ldq + c) = quant8_scaled(v, pow2f(e));
-      if ((t & 15) == 0) a.dscale[static_cast<int64_t>(c >> 7) * a.ld_s + row] = pow2f(e);
+      for (int k = 0; k < 8; ++k) w[k] = r[i][k] * rho_r * w[k];
+      const uint4 v = pack8(w);
+      if (a.x) store8(a.x + row * a.ldx + at.c[i], v, at.n[i]);
+      if (a.q) {
+        // a 1x128 group is 16 consecutive threads; cols is a multiple of 128, so they are all here
+        const int e = block_exponent(row16_max(amax8_bits(v)));
+        *reinterpret_cast<uint2*>(a.q + row * a.ldq + at.c[i]) = quant8_scaled(v, pow2f(e));
+        if ((t & 15) == 0) a.dscale[static_cast<int64_t>(at.c[i] >> 7) * a.ld_s + row] = pow2f(e);
+      }
     }
   }
 }
 
-// Backward: workgroup b takes rows b, b + G, ...; every thread sums its own columns' weight and
-// gate gradients over the workgroup's rows in registers and writes one row of partial sums.
-template <int L, int NV>
-__global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) {
-  __shared__ float slots[2][2 * (L / 64)];
+// Backward: workgroup b takes rows b, b + G, ... (the next row on its way as above); every thread sums its
+// own columns' weight and gate gradients over the workgroup's rows in registers and writes one row of
+// partial sums.
+template <int NV, int THREADS, bool AHEAD>
+__global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_sums) {
+  __shared__ float slots[2][2 * (THREADS / 64)];
   const NormArgs& p = a.in;
-  const int t = threadIdx.x, cols = p.cols;
+  const int cols = p.cols;
+  const Cols<NV> at(threadIdx.x, blockDim.x, cols);
   const bool branch = p.y != nullptr, full_gate = p.gate != nullptr && p.ld_gate != 0;
   const bool pre = a.dx != nullptr, post = p.w_post != nullptr;
   const float inv_n = 1.0f / static_cast<float>(cols);
+  const Weights<NV, AHEAD> w_pre(pre ? p.w_pre : nullptr, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
+      gate(full_gate ? nullptr : p.gate, p.wf32, 0.0f, at);
   float acc[3][NV][8];
 #pragma unroll
   for (int j = 0; j < 3; ++j)
@@ -240,20 +290,31 @@ __global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) 
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[j][i][k] = 0.0f;
   int turn = 0;
+  auto sum = [&](auto& s) {
+    row_sum<false>(s, slots[turn]);
+    turn ^= 1;
+  };
 
+  struct Row {
+    uint4 h[NV], y[NV], g[NV], dr[NV], dx[NV];
+  };
+  auto load_row = [&](int64_t row, Row& v) {
+    if (pre) {
+      at.load(p.h + row * p.ldh, v.h);
+      at.load(a.dx + row * a.lddx, v.dx);
+    }
+    if (branch) at.load(p.y + row * p.ldy, v.y);
+    if (full_gate) at.load(static_cast<const uint16_t*>(p.gate) + row * p.ld_gate, v.g);
+    if (a.dr) at.load(a.dr + row * a.lddr, v.dr);
+  };
+  Row cur{}, next{};
+  if (AHEAD) load_row(blockIdx.x, next);  // there are no more workgroups than rows
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    uint4 hv[NV], yv[NV], gv[NV], rv[NV], xv[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (t + i * L), n = cols - c;
-      hv[i] = yv[i] = gv[i] = rv[i] = xv[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (n > 0) {
-        if (pre) hv[i] = load8(p.h + row * p.ldh + c, n);
-        if (branch) yv[i] = load8(p.y + row * p.ldy + c, n);
-        if (full_gate) gv[i] = load8(static_cast<const uint16_t*>(p.gate) + row * p.ld_gate + c, n);
-        if (a.dr) rv[i] = load8(a.dr + row * a.lddr + c, n);
-        if (pre) xv[i] = load8(a.dx + row * a.lddx + c, n);
-      }
+    if constexpr (AHEAD) {
+      cur = next;
+      if (row + gridDim.x < p.rows) load_row(row + gridDim.x, next);
+    } else {
+      load_row(row, cur);
     }
     float rho_y = 1.0f;
     if (post) {
@@ -261,72 +322,58 @@ __global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) 
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float y[8];
-        unpack8(yv[i], y);
+        unpack8(cur.y[i], y);
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[0] = add_sq(y[k], p.sq, s[0]);
       }
-      row_sum<L, 1>(s, slots[turn]);
-      turn ^= 1;
+      sum(s);
       rho_y = inv_rms(s[0], p);
     }
     // the branch's value u at a step, and the gate's
-    auto branch_values = [&](int i, int c, int n, float (&u)[8], float (&g)[8]) {
-      unpack8(yv[i], u);
-      if (post && n > 0) {
-        float w[8];
-        load_w8(p.w_post, p.wf32, c, n, p.offset, w);
+    auto branch_values = [&](int i, float (&u)[8], float (&g)[8]) {
+      unpack8(cur.y[i], u);
+      if (post) {
+        w_post.get(i, at, g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) u[k] = u[k] * rho_y * w[k];
+        for (int k = 0; k < 8; ++k) u[k] = u[k] * rho_y * g[k];
       }
-      if (full_gate) {
-        unpack8(gv[i], g);
-      } else if (p.gate && n > 0) {
-        load_w8(p.gate, p.wf32, c, n, 0.0f, g);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = 1.0f;
-      }
+      if (full_gate) unpack8(cur.g[i], g);
+      else gate.get(i, at, g);
     };
 
     float d[NV][8];  // the gradient that reaches r
 #pragma unroll
-    for (int i = 0; i < NV; ++i) unpack8(rv[i], d[i]);
+    for (int i = 0; i < NV; ++i) unpack8(cur.dr[i], d[i]);
     if (pre) {
       float s[2] = {0.0f, 0.0f};  // sums of (r sq)^2 and t (r sq)
       float rr[NV][8];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (t + i * L), n = cols - c;
-        unpack8(hv[i], rr[i]);
+        unpack8(cur.h[i], rr[i]);
         if (branch) {
           float u[8], g[8];
-          branch_values(i, c, n, u, g);
+          branch_values(i, u, g);
 #pragma unroll
           for (int k = 0; k < 8; ++k) rr[i][k] = p.residual_scale * rr[i][k] + p.branch_scale * (u[k] * g[k]);
         }
-        if (n > 0) {
-          float x[8], w[8];
-          unpack8(xv[i], x);
-          load_w8(p.w_pre, p.wf32, c, n, p.offset, w);
+        float x[8], w[8];
+        unpack8(cur.dx[i], x);
+        w_pre.get(i, at, w);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float q = rr[i][k] * p.sq;
-            s[0] = __builtin_fmaf(q, q, s[0]);
-            s[1] = __builtin_fmaf(x[k] * w[k], q, s[1]);
-          }
+        for (int k = 0; k < 8; ++k) {
+          const float q = rr[i][k] * p.sq;
+          s[0] = __builtin_fmaf(q, q, s[0]);
+          s[1] = __builtin_fmaf(x[k] * w[k], q, s[1]);
         }
       }
-      row_sum<L, 2>(s, slots[turn]);
-      turn ^= 1;
+      sum(s);
       const float rho_r = inv_rms(s[0], p);
       const float m = s[1] * rho_r * (inv_n / p.sq);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (t + i * L), n = cols - c;
-        if (n <= 0) continue;
         float x[8], w[8];
-        unpack8(xv[i], x);
-        load_w8(p.w_pre, p.wf32, c, n, p.offset, w);
+        unpack8(cur.dx[i], x);
+        w_pre.get(i, at, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float rn = rr[i][k] * rho_r;
@@ -338,22 +385,18 @@ __global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) 
     if (a.dh) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (t + i * L), n = cols - c;
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = p.residual_scale * d[i][k];
-        if (n > 0) store8(a.dh + row * a.lddh + c, pack8(o), n);
+        if (at.n[i] > 0) store8(a.dh + row * a.lddh + at.c[i], pack8(o), at.n[i]);
       }
     }
     if (!branch) continue;
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (t + i * L), n = cols - c;
-      if (n <= 0) continue;
-      float u[8], g[8];
-      branch_values(i, c, n, u, g);
-      float o[8];
+      float u[8], g[8], o[8];
+      branch_values(i, u, g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float v = p.branch_scale * d[i][k];
@@ -361,11 +404,11 @@ __global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) 
         acc[2][i][k] += o[k];
         d[i][k] = v * g[k];
       }
-      if (a.dgate_full) store8(a.dgate_full + row * a.ld_dgate + c, pack8(o), n);
+      if (a.dgate_full && at.n[i] > 0) store8(a.dgate_full + row * a.ld_dgate + at.c[i], pack8(o), at.n[i]);
       if (post) {
         float y[8], w[8];
-        unpack8(yv[i], y);
-        load_w8(p.w_post, p.wf32, c, n, p.offset, w);
+        unpack8(cur.y[i], y);
+        w_post.get(i, at, w);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float yn = y[k] * rho_y;
@@ -377,19 +420,17 @@ __global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) 
     }
     float m2 = 0.0f;
     if (post) {
-      row_sum<L, 1>(s, slots[turn]);
-      turn ^= 1;
+      sum(s);
       m2 = s[0] * inv_n;
     }
     if (a.dy) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (t + i * L), n = cols - c;
         float o[8], y[8];
-        unpack8(yv[i], y);
+        unpack8(cur.y[i], y);
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = post ? rho_y * (d[i][k] - y[k] * rho_y * m2) : d[i][k];
-        if (n > 0) store8(a.dy + row * a.lddy + c, pack8(o), n);
+        if (at.n[i] > 0) store8(a.dy + row * a.lddy + at.c[i], pack8(o), at.n[i]);
       }
     }
   }
@@ -399,12 +440,10 @@ __global__ __launch_bounds__(L) void norm_bwd_kernel(NormBwdArgs a, int n_sums) 
   for (int j = 0; j < 3; ++j) {
     if (!a.sums[j]) continue;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (t + i * L);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k < cols) out[c + k] = acc[j][i][k];
-    }
+        if (k < at.n[i]) out[at.c[i] + k] = acc[j][i][k];
     out += cols;
   }
 }
@@ -435,29 +474,40 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void norm_colsum_kernel(cons
 
 }  // namespace
 
+// Workgroups for `units` units of work (rows, or four of them): no more than the card's 256 CUs hold at
+// once, and evenly loaded. 8192 x 2048 forward: 28.9 us with 1024 workgroups of 8 rows, 31.8 with 2048, 36.9
+// with one for each row; backward 55.9 us with 745, 61.5 with 512, 69.7 with 1024.
+static int64_t even_groups(int64_t units, int64_t per_cu) {
+  const int64_t most = 256 * (per_cu < 1 ? 1 : per_cu), each = (units + most - 1) / most;
+  return (units + each - 1) / each;
+}
+
 hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
   const int64_t rows = a.in.rows;
   const int cols = a.in.cols;
-  auto wide = [&](auto kern, int threads, int rpb) {
-    hipLaunchKernelGGL(kern, dim3(static_cast<uint32_t>((rows + rpb - 1) / rpb)), dim3(threads), 0, stream, a);
+  auto go = [&](auto kern, int64_t groups, int threads) {
+    hipLaunchKernelGGL(kern, dim3(static_cast<uint32_t>(groups)), dim3(threads), 0, stream, a);
     return hipGetLastError();
   };
-  if (rows >= 1024 && cols <= 2048) {
-    if (cols <= 512) return wide(norm_fwd_kernel<64, 1>, 256, 4);
-    if (cols <= 1024) return wide(norm_fwd_kernel<64, 2>, 256, 4);
-    return wide(norm_fwd_kernel<64, 4>, 256, 4);
-  }
-  if (cols <= 512) return wide(norm_fwd_kernel<64, 1>, 256, 4);
-  if (cols <= 2048) return wide(norm_fwd_kernel<256, 1>, 256, 1);
-  if (cols <= 4096) return wide(norm_fwd_kernel<256, 2>, 256, 1);
-  if (cols <= 8192) return wide(norm_fwd_kernel<256, 4>, 256, 1);
-  if (cols <= 16384) return wide(norm_fwd_kernel<1024, 2>, 1024, 1);
-  return wide(norm_fwd_kernel<1024, 4>, 1024, 1);
+  // A row by one wave, by up to four with the next row on its way (88 registers: 20 waves on a CU), or by up to
+  // 16 without (wide rows have enough loads in flight: 4096 x 6144 with a full gate 56.3 us, 59.5 us by half the
+  // waves with the next row on its way).
+  const int threads = (cols + 511) / 512 * 64;  // 8 values each
+  if (cols <= 512) return go(norm_fwd_kernel<true, 1, 256, true>, even_groups((rows + 3) / 4, 5), 256);
+  if (cols <= 2048) return go(norm_fwd_kernel<false, 1, 256, true>, even_groups(rows, 1280 / threads), threads);
+  if (cols <= 8192) return go(norm_fwd_kernel<false, 1, 1024, false>, even_groups(rows, 1536 / threads), threads);
+  return go(norm_fwd_kernel<false, 2, 1024, false>, even_groups(rows, 1), 1024);
 }
 
+// Threads of a row in the backward pass: whole waves, one, two or four steps of 8 values each.
+static int norm_bwd_threads(int64_t cols) {
+  const int64_t steps = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+  return static_cast<int>((cols + 512 * steps - 1) / (512 * steps) * 64);
+}
+
+// (12 waves on a CU with 158 registers each, or 8 with 256)
 int64_t norm_bwd_groups(int64_t rows, int64_t cols) {
-  (void)cols;
-  return rows < 512 ? rows : 512;
+  return even_groups(rows, (cols <= 2048 ? 768 : 512) / norm_bwd_threads(cols));
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
@@ -471,13 +521,11 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(kern, dim3(groups), dim3(threads), 0, stream, a, n_sums);
     return hipGetLastError();
   };
+  const int threads = norm_bwd_threads(cols);
   hipError_t e;
-  if (cols <= 512) e = go(norm_bwd_kernel<64, 1>, 64);
-  else if (cols <= 2048) e = go(norm_bwd_kernel<256, 1>, 256);
-  else if (cols <= 4096) e = go(norm_bwd_kernel<256, 2>, 256);
-  else if (cols <= 8192) e = go(norm_bwd_kernel<1024, 1>, 1024);
-  else if (cols <= 16384) e = go(norm_bwd_kernel<1024, 2>, 1024);
-  else e = go(norm_bwd_kernel<1024, 4>, 1024);
+  if (cols <= 2048) e = go(norm_bwd_kernel<1, 256, true>, threads);
+  else if (cols <= 8192) e = go(norm_bwd_kernel<2, 512, true>, threads);
+  else e = go(norm_bwd_kernel<4, 512, false>, threads);
   if (e != hipSuccess || n_sums == 0) return e;
   const int width = n_sums * cols;
   hipLaunchKernelGGL(norm_colsum_kernel, dim3((width + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumSlices), 0, stream,

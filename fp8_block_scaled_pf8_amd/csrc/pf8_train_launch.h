@@ -6,7 +6,7 @@
 
 namespace pf8 {
 
-constexpr int64_t kNormMaxCols = 32768;
+constexpr int64_t kNormMaxCols = 16384;
 
 // Operands and scalars that the block norm's forward and backward share.
 struct NormArgs {

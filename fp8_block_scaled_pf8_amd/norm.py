@@ -101,6 +101,14 @@ def _inputs(h: Tensor, y: Optional[Tensor], w_pre, w_post, gate, residual_scale,
     return rows, cols, full, args
 
 
+def _output(out: Optional[Tensor], name: str, like: Tensor) -> Tuple[Tensor, int, int]:
+    """A bf16 result of like's shape: the one given, after its checks, or a new one."""
+    if out is not None:
+        return (out, *_rows(out, name, like.shape, like.device))
+    out = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return out, out.data_ptr(), like.shape[1]
+
+
 def _extent(t: Tensor) -> Tuple[int, int]:
     """First byte and the byte behind the last of a 2-D tensor with at least one element."""
     n = (t.shape[0] - 1) * t.stride(0) + (t.shape[1] - 1) * t.stride(1) + 1
@@ -116,6 +124,16 @@ def _may_write(out: Tensor, name: str, others) -> None:
         c, d = _extent(o) if o.dim() == 2 else (o.data_ptr(), o.data_ptr() + o.numel() * o.element_size())
         if a < d and c < b and not (same_ok and a == c and (out.shape[0] == 1 or out.stride(0) == o.stride(0))):
             raise ValueError(f"{name} overlaps another operand")
+
+
+# The current stream's handle without the Stream object around it (which costs as much as half a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 class _on:
@@ -149,11 +167,9 @@ def _forward(h, y, w_pre, w_post, gate, residual_scale, branch_scale, eps, unit_
     r = x = q = s = None
     pr = ldr = px = ldx = pq = ldq = ps = lds = 0
     if y is not None:
-        r = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if r_out is None else r_out
-        pr, ldr = _rows(r, "r_out", h.shape, dev)
+        r, pr, ldr = _output(r_out, "r_out", h)
     if w_pre is not None and not codes:
-        x = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if x_out is None else x_out
-        px, ldx = _rows(x, "x_out", h.shape, dev)
+        x, px, ldx = _output(x_out, "x_out", h)
     if codes:
         q = code_buffer(rows, cols, dev)
         s = torch.empty((cols // GROUP, rows), dtype=torch.float32, device=dev)
@@ -167,7 +183,7 @@ def _forward(h, y, w_pre, w_post, gate, residual_scale, branch_scale, eps, unit_
     if rows:
         with _on(dev):
             L.check(L.pf8_block_norm(rows, cols, *args, pr, ldr, px, ldx, pq, ldq, ps, lds,
-                                     torch.cuda.current_stream(dev).cuda_stream), "pf8_block_norm")
+                                     _stream(dev)), "pf8_block_norm")
     return (h if r is None else r), x, q, s
 
 
@@ -239,10 +255,9 @@ def block_norm_backward(dr: Optional[Tensor], dx: Optional[Tensor], h: Tensor, y
     dgate, p_gate = column(dgate_out, "dgate_out", gate is not None and not full)
     ld_dg = 0
     if full:
-        dgate = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-        p_gate, ld_dg = dgate.data_ptr(), cols
-    dh = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
-    dy = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if y is not None else None
+        dgate, p_gate, ld_dg = _output(None, "", h)
+    dh, p_dh, _ = _output(None, "", h)
+    dy, p_dy, _ = (None, 0, 0) if y is None else _output(None, "", h)
     sums = [t for t in (dw_pre, dw_post, None if full else dgate) if t is not None]
     if accumulate or dw_pre_out is not None or dw_post_out is not None or dgate_out is not None:
         operands = [t for t in (dr, dx, h, y, w_pre, w_post, gate) if t is not None and t.numel()]
@@ -262,10 +277,9 @@ def block_norm_backward(dr: Optional[Tensor], dx: Optional[Tensor], h: Tensor, y
         nws = L.pf8_block_norm_bwd_workspace(rows, cols)
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
     with _on(dev):
-        L.check(L.pf8_block_norm_bwd(rows, cols, pdr, ldr, pdx, ldx, *args, dh.data_ptr(), cols,
-                                     0 if dy is None else dy.data_ptr(), cols, p_gate, ld_dg, p_pre, p_post,
-                                     int(accumulate), 0 if ws is None else ws.data_ptr(), nws,
-                                     torch.cuda.current_stream(dev).cuda_stream), "pf8_block_norm_bwd")
+        L.check(L.pf8_block_norm_bwd(rows, cols, pdr, ldr, pdx, ldx, *args, p_dh, cols, p_dy, cols,
+                                     p_gate, ld_dg, p_pre, p_post, int(accumulate), 0 if ws is None else ws.data_ptr(), nws,
+                                     _stream(dev)), "pf8_block_norm_bwd")
     return BlockNormGrads(dh, dy, dgate, dw_pre, dw_post)
 
 

@@ -12,7 +12,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib as L
-from .norm import _on
+from .norm import _on, _stream
 
 # Steep at zero (slope 3.4445), so that small singular values grow fast; after five steps values
 # above 1e-2 of the norm lie between 0.7 and 1.2.
@@ -68,5 +68,5 @@ def newton_schulz(g: torch.Tensor, steps: int = 5, coefficients: Sequence = QUIN
     with _on(g.device):
         L.check(L.pf8_newton_schulz(batch, m, n, g0, ldg, sg, L.PF8_F32 if g.dtype == torch.float32 else L.PF8_BF16,
                                     steps, coef, eps, o0, ldo, so, ws.data_ptr(), size,
-                                    torch.cuda.current_stream(g.device).cuda_stream), "pf8_newton_schulz")
+                                    _stream(g.device)), "pf8_newton_schulz")
     return out

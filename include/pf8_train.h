@@ -31,7 +31,7 @@ typedef int pf8_dtype;
 #define PF8_F32 1
 
 /* Largest row of the block norm. */
-#define PF8_NORM_MAX_COLS 32768
+#define PF8_NORM_MAX_COLS 16384
 
 /*
  * Block norm, forward. Per row of [rows, cols], everything in FP32, each output rounded once:

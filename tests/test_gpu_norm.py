@@ -91,7 +91,7 @@ def _check_backward(k, sc, dr, dx, g):
 
 SIZES = [(1, 1), (1, 2048), (3, 7), (5, 64), (2, 511), (4, 512), (3, 513), (1030, 520), (1025, 1000), (1100, 2048),
          (7, 1536), (6, 2047), (5, 2056), (9, 4096), (2, 4100), (3, 5407), (2, 6144), (4, 8192), (2, 8193), (3, 16384),
-         (2, 16400), (2, 32768)]
+         (2, 16383), (2, 12000)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES)
@@ -127,7 +127,7 @@ def test_without_a_branch(wdt):
     _check_backward(k, {}, None, dx, pf8.block_norm_backward(None, dx, **k))
 
 
-@pytest.mark.parametrize("rows,cols", [(1, 128), (5, 384), (1030, 512), (1100, 2048), (3, 4096), (2, 12288), (2, 32768)])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (5, 384), (1030, 512), (1100, 2048), (3, 4096), (2, 12288), (2, 16384)])
 def test_codes_are_the_quantisers_of_the_same_x(rows, cols):
     k = _case(rows, cols, gate="full", seed=9)
     k["h"][0, :min(cols, 256)] = 0

@@ -103,7 +103,7 @@ def test_block_norm_workspace():
     size = L.pf8_block_norm_bwd_workspace
     assert size(0, 512) == size(4, 0) == size(4, 40000) == size(1 << 31, 512) == size(-1, 5) == 0
     assert size(1, 1) >= 12 and size(8192, 2048) >= 3 * 2048 * 4
-    assert size((1 << 31) - 1, 32768) < 1 << 30
+    assert size((1 << 31) - 1, 16384) < 1 << 30
 
 
 def _ns(**kw):
