@@ -9,6 +9,8 @@
 #include "pf8_device.h"
 #include "pf8_train_launch.h"
 
+#include <type_traits>
+
 namespace pf8 {
 
 namespace {
@@ -16,6 +18,8 @@ namespace {
 // 16 bytes at 2-byte alignment: global accesses of any alignment are one instruction on gfx950, so
 // odd row pitches take the same path as aligned ones.
 typedef uint32_t u128_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u64_a2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
 typedef float f128_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -35,76 +39,81 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
 }
 
-// 8 bf16 from p; only the first n are read (n >= 8 except in a row's last step), the rest are zero.
-__device__ __forceinline__ uint4 load8(const uint16_t* p, int n) {
-  if (n >= 8) {
-    const u128_a2 v = *reinterpret_cast<const u128_a2*>(p);
-    return make_uint4(v[0], v[1], v[2], v[3]);
-  }
+__device__ __forceinline__ uint4 load8(const uint16_t* p) {
+  const u128_a2 v = *reinterpret_cast<const u128_a2*>(p);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+// The first n < 8, zeros behind.
+__device__ __forceinline__ uint4 load_few(const uint16_t* p, int n) {
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 7; ++i)
     if (i < n) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
-__device__ __forceinline__ void store8(uint16_t* p, uint4 v, int n) {
-  if (n >= 8) {
-    *reinterpret_cast<u128_a2*>(p) = u128_a2{v.x, v.y, v.z, v.w};
-    return;
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (i < n) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+// The last n < 8 of 8 values whose first belongs at p, in pieces of 1, 2 and 4.
+__device__ __forceinline__ void store_last(uint16_t* p, uint4 v, int n) {
+  if (n & 1) p[8 - n] = static_cast<uint16_t>((n & 4 ? (n & 2 ? v.x : v.y) : (n & 2 ? v.z : v.w)) >> 16);
+  if (n & 2) *reinterpret_cast<u32_a2*>(p + (n & 4 ? 2 : 6)) = n & 4 ? v.y : v.w;
+  if (n & 4) *reinterpret_cast<u64_a2*>(p + 4) = u64_a2{v.z, v.w};
 }
 
-// 8 weights (FP32 or BF16) from index c on, plus the offset.
-__device__ __forceinline__ void load_w8(const void* w, int wf32, int c, int n, float offset, float (&f)[8]) {
-  if (wf32) {
-    const float* p = static_cast<const float*>(w) + c;
-    if (n >= 8) {
-      const f128_a4 a = *reinterpret_cast<const f128_a4*>(p), b = *reinterpret_cast<const f128_a4*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] = a[i], f[i + 4] = b[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = i < n ? p[i] : 0.0f;
-    }
-  } else {
-    unpack8(load8(static_cast<const uint16_t*>(w) + c, n), f);
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] += offset;
-}
-
+// Sum over a wave, the same in every lane: four DPP steps within rows of 16 lanes, then the four rows'
+// sums by lane reads. (Shuffles through LDS cost some hundred cycles for the six steps, and a row has up to
+// three sums that wait for one another.)
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-  return v;
+  auto step = [&](auto ctrl) {
+    v += __uint_as_float(static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), decltype(ctrl)::value, 0xF, 0xF, true)));
+  };
+  // quad_perm [1,0,3,2], quad_perm [2,3,0,1], row_half_mirror, row_mirror
+  step(std::integral_constant<int, 0xB1>{});
+  step(std::integral_constant<int, 0x4E>{});
+  step(std::integral_constant<int, 0x141>{});
+  step(std::integral_constant<int, 0x140>{});
+  const int x = static_cast<int>(__float_as_uint(v));
+  auto lane = [&](int l) { return __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(x, l))); };
+  return (lane(0) + lane(16)) + (lane(32) + lane(48));
 }
 
-// Sums of N values over the threads of a row: one wave (SINGLE), or the whole workgroup. With several
-// waves they meet in `slot`, N floats per wave; consecutive reductions take turns between two slots, so
-// one barrier each is enough: a slot is written again only after the barrier of the reduction in
-// between, which every thread reaches after it has read the slot.
-template <bool SINGLE, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* slot) {
+// Sums of N values over the threads of a row: one wave (WAVES = 1), or the whole workgroup of up to WAVES
+// waves. With several waves they meet in `slot` (N rows of WAVES values, zero where there is no wave);
+// consecutive reductions take turns between two slots, so one barrier each is enough: a slot is written
+// again only after the barrier of the reduction in between, which every thread reaches after it has read
+// the slot.
+template <int WAVES, int N>
+struct __align__(16) Slot {
+  float v[N][WAVES];
+};
+template <int WAVES, int N, int M>
+__device__ __forceinline__ void row_sum(float (&v)[N], Slot<WAVES, M>& slot) {
+  static_assert(N <= M, "room for the values");
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-  if constexpr (!SINGLE) {
+  if constexpr (WAVES > 1) {
+    static_assert(WAVES % 4 == 0, "four at a time");
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) slot[(threadIdx.x >> 6) * N + i] = v[i];
+      for (int i = 0; i < N; ++i) slot.v[i][threadIdx.x >> 6] = v[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    const int waves = blockDim.x >> 6;
-    for (int w = 0; w < waves; ++w) {
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += slot[w * N + i];
+      for (int w = 0; w < WAVES; w += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&slot.v[i][w]);
+        v[i] += (f.x + f.y) + (f.z + f.w);
+      }
     }
+  }
+}
+// Zeros for the waves that a workgroup does not have.
+template <int WAVES, int N>
+__device__ __forceinline__ void clear(Slot<WAVES, N> (&slots)[2]) {
+  if constexpr (WAVES > 1) {
+    for (int i = threadIdx.x; i < 2 * N * WAVES; i += blockDim.x) (&slots[0].v[0][0])[i] = 0.0f;
+    __syncthreads();
   }
 }
 
@@ -118,65 +127,127 @@ __device__ __forceinline__ float add_sq(float v, float sq, float s) {
   return __builtin_fmaf(t, t, s);
 }
 
-// A thread's part of a row: NV steps of 8 values, `span` threads of the row apart.
-template <int NV>
+// A thread's part of a row: NV steps of 8 columns, `span` threads apart. In the row's last step, where
+// fewer than 8 columns are left, the thread takes the row's last 8 all the same, so that they come by one
+// load, and masks those that belong to the thread before it: they count as zeros, and are not stored.
+// (Loads put together from pieces would be waited for where they are made, and no longer travel during the
+// row before: 8192 x 2047 backward took 143 us, 2048 columns 51 us.) kEven: there is
+// no such step. kTiny: rows of under 8 columns, loaded value by value, zeros behind.
+enum Tail { kEven, kOdd, kTiny };
+template <int NV, Tail TAIL>
 struct Cols {
-  int c[NV], n[NV];  // first column, and how many there are from it on
-  __device__ __forceinline__ Cols(int t, int span, int cols) {
+  static constexpr bool TINY = TAIL == kTiny;
+  int cols;
+  int c[NV];      // the first column
+  int first[NV];  // the first of the 8 that is the thread's own; 8: none is
+  __device__ __forceinline__ Cols(int t, int span, int cols_) : cols(cols_) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) c[i] = 8 * (t + i * span), n[i] = cols - c[i];
+    for (int i = 0; i < NV; ++i) {
+      c[i] = 8 * (t + i * span);
+      const int n = cols - c[i];
+      first[i] = n >= 8 || (TINY && n > 0) ? 0 : n <= 0 ? 8 : 8 - n;
+      if (TAIL == kOdd && n < 8) c[i] = cols - 8;
+    }
   }
+  __device__ __forceinline__ bool any(int i) const { return first[i] < 8; }
   __device__ __forceinline__ void load(const uint16_t* row, uint4 (&v)[NV]) const {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (n[i] > 0) v[i] = load8(row + c[i], n[i]);
+      if (any(i)) v[i] = TINY ? load_few(row, cols) : load8(row + c[i]);
     }
+  }
+  // zeros for the columns that are another thread's
+  __device__ __forceinline__ void mask(uint4 (&v)[NV]) const {
+    if constexpr (TAIL != kOdd) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (first[i]) {
+        auto keep = [&](int w) { return first[i] <= 2 * w ? 0xFFFFFFFFu : first[i] == 2 * w + 1 ? 0xFFFF0000u : 0u; };
+        v[i].x &= keep(0), v[i].y &= keep(1), v[i].z &= keep(2), v[i].w &= keep(3);
+      }
+  }
+  __device__ __forceinline__ void store(uint16_t* row, int i, const float (&f)[8]) const { store(row, i, pack8(f)); }
+  __device__ __forceinline__ void store(uint16_t* row, int i, uint4 v) const {
+    if (!any(i)) return;
+    uint16_t* p = row + c[i];
+    if constexpr (TINY) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (k < cols) p[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    } else if (TAIL == kEven || first[i] == 0) {
+      *reinterpret_cast<u128_a2*>(p) = u128_a2{v.x, v.y, v.z, v.w};
+    } else {
+      store_last(p, v, 8 - first[i]);
+    }
+  }
+  // the 8 values of a vector of FP32 or BF16, plus the offset
+  __device__ __forceinline__ void vector(const void* w, int wf32, int i, float offset, float (&f)[8]) const {
+    if (!any(i)) return;
+    if constexpr (TINY) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        f[k] = k >= cols ? 0.0f
+               : wf32    ? static_cast<const float*>(w)[k]
+                         : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(w)[k]) << 16);
+    } else if (wf32) {
+      const float* p = static_cast<const float*>(w) + c[i];
+      const f128_a4 a = *reinterpret_cast<const f128_a4*>(p), b = *reinterpret_cast<const f128_a4*>(p + 4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = a[k], f[k + 4] = b[k];
+    } else {
+      unpack8(load8(static_cast<const uint16_t*>(w) + c[i]), f);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] += offset;
   }
 };
 
 // A [cols] vector's values at a thread's columns: kept in registers over the rows where they are few.
-template <int NV, bool KEEP>
+template <int NV, Tail TAIL, bool KEEP>
 struct Weights {
   static constexpr bool kKeep = KEEP;
   const void* w;
   int wf32;
   float offset;
   float kept[kKeep ? NV : 1][8];
-  __device__ __forceinline__ Weights(const void* w_, int wf32_, float offset_, const Cols<NV>& at) : w(w_), wf32(wf32_), offset(offset_) {
+  __device__ __forceinline__ Weights(const void* w_, int wf32_, float offset_, const Cols<NV, TAIL>& at) : w(w_), wf32(wf32_), offset(offset_) {
     if constexpr (kKeep) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) kept[i][k] = 1.0f;
-        if (w && at.n[i] > 0) load_w8(w, wf32, at.c[i], at.n[i], offset, kept[i]);
+        if (w) at.vector(w, wf32, i, offset, kept[i]);
       }
     }
   }
   // (1 without a vector)
-  __device__ __forceinline__ void get(int i, const Cols<NV>& at, float (&f)[8]) const {
+  __device__ __forceinline__ void get(int i, const Cols<NV, TAIL>& at, float (&f)[8]) const {
     if constexpr (kKeep) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = kept[i][k];
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) f[k] = 1.0f;
-      if (w && at.n[i] > 0) load_w8(w, wf32, at.c[i], at.n[i], offset, f);
+      if (w) at.vector(w, wf32, i, offset, f);
     }
   }
 };
 
 // Forward. A row belongs to a wave (SINGLE: four rows a workgroup) or to the workgroup; workgroups walk
 // the rows, and (AHEAD) the next row's values are on their way while one is worked on.
-template <bool SINGLE, int NV, int THREADS, bool AHEAD>
+template <bool SINGLE, int NV, int THREADS, bool AHEAD, Tail TAIL>
 __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
-  __shared__ float slots[2][SINGLE ? 1 : THREADS / 64];
+  constexpr int kWaves = SINGLE ? 1 : THREADS / 64;
+  __shared__ Slot<kWaves, 1> slots[2];
+  clear(slots);
   const NormArgs& p = a.in;
   const int span = SINGLE ? 64 : blockDim.x, t = SINGLE ? threadIdx.x & 63 : threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (SINGLE ? THREADS / 64 : 1);
-  const Cols<NV> at(t, span, p.cols);
+  const Cols<NV, TAIL> at(t, span, p.cols);
   const bool branch = p.y != nullptr, full_gate = p.gate != nullptr && p.ld_gate != 0, post = p.w_post != nullptr;
-  const Weights<NV, AHEAD> w_pre(p.w_pre, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
+  const Weights<NV, TAIL, AHEAD> w_pre(p.w_pre, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
       gate(full_gate ? nullptr : p.gate, p.wf32, 0.0f, at);
 
   uint4 hv[NV], yv[NV], gv[NV], hn[NV], yn[NV], gn[NV];
@@ -195,6 +266,8 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
     } else {
       load_row(row, hv, yv, gv);
     }
+    at.mask(hv);
+    at.mask(yv);
 
     float r[NV][8];
 #pragma unroll
@@ -210,7 +283,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) s[0] = add_sq(y[k], p.sq, s[0]);
         }
-        row_sum<SINGLE, 1>(s, slots[0]);
+        row_sum<kWaves>(s, slots[0]);
         rho_y = inv_rms(s[0], p);
       }
 #pragma unroll
@@ -230,8 +303,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
     }
     if (a.r) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (at.n[i] > 0) store8(a.r + row * a.ldr + at.c[i], pack8(r[i]), at.n[i]);
+      for (int i = 0; i < NV; ++i) at.store(a.r + row * a.ldr, i, r[i]);
     }
     if (!p.w_pre) {
       if (!SINGLE) __syncthreads();  // slot 0 has been read
@@ -243,21 +315,21 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        // the places behind the row's end hold zeros (times finite scales)
+        // places that are not the thread's own hold zeros
         s[0] = add_sq(r[i][k], p.sq, s[0]);
-    row_sum<SINGLE, 1>(s, slots[1]);
+    row_sum<kWaves>(s, slots[1]);
     // without a norm behind the branch, slot 1 alone is used: a barrier before it is written again
     if (!SINGLE && !(branch && post)) __syncthreads();
     const float rho_r = inv_rms(s[0], p);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (at.n[i] <= 0) continue;
+      if (!at.any(i)) continue;
       float w[8];
       w_pre.get(i, at, w);
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = r[i][k] * rho_r * w[k];
       const uint4 v = pack8(w);
-      if (a.x) store8(a.x + row * a.ldx + at.c[i], v, at.n[i]);
+      if (a.x) at.store(a.x + row * a.ldx, i, v);
       if (a.q) {
         // a 1x128 group is 16 consecutive threads; cols is a multiple of 128, so they are all here
         const int e = block_exponent(row16_max(amax8_bits(v)));
@@ -271,16 +343,17 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
 // Backward: workgroup b takes rows b, b + G, ... (the next row on its way as above); every thread sums its
 // own columns' weight and gate gradients over the workgroup's rows in registers and writes one row of
 // partial sums.
-template <int NV, int THREADS, bool AHEAD>
+template <int NV, int THREADS, bool AHEAD, Tail TAIL>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_sums) {
-  __shared__ float slots[2][2 * (THREADS / 64)];
+  __shared__ Slot<THREADS / 64, 2> slots[2];
+  clear(slots);
   const NormArgs& p = a.in;
   const int cols = p.cols;
-  const Cols<NV> at(threadIdx.x, blockDim.x, cols);
+  const Cols<NV, TAIL> at(threadIdx.x, blockDim.x, cols);
   const bool branch = p.y != nullptr, full_gate = p.gate != nullptr && p.ld_gate != 0;
   const bool pre = a.dx != nullptr, post = p.w_post != nullptr;
   const float inv_n = 1.0f / static_cast<float>(cols);
-  const Weights<NV, AHEAD> w_pre(pre ? p.w_pre : nullptr, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
+  const Weights<NV, TAIL, AHEAD> w_pre(pre ? p.w_pre : nullptr, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
       gate(full_gate ? nullptr : p.gate, p.wf32, 0.0f, at);
   float acc[3][NV][8];
 #pragma unroll
@@ -291,7 +364,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
       for (int k = 0; k < 8; ++k) acc[j][i][k] = 0.0f;
   int turn = 0;
   auto sum = [&](auto& s) {
-    row_sum<false>(s, slots[turn]);
+    row_sum<THREADS / 64>(s, slots[turn]);
     turn ^= 1;
   };
 
@@ -316,6 +389,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
     } else {
       load_row(row, cur);
     }
+    at.mask(cur.y);
     float rho_y = 1.0f;
     if (post) {
       float s[1] = {0.0f};
@@ -341,10 +415,13 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
       else gate.get(i, at, g);
     };
 
+    at.mask(cur.dr);
     float d[NV][8];  // the gradient that reaches r
 #pragma unroll
     for (int i = 0; i < NV; ++i) unpack8(cur.dr[i], d[i]);
     if (pre) {
+      at.mask(cur.h);
+      at.mask(cur.dx);
       float s[2] = {0.0f, 0.0f};  // sums of (r sq)^2 and t (r sq)
       float rr[NV][8];
 #pragma unroll
@@ -388,7 +465,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = p.residual_scale * d[i][k];
-        if (at.n[i] > 0) store8(a.dh + row * a.lddh + at.c[i], pack8(o), at.n[i]);
+        at.store(a.dh + row * a.lddh, i, o);
       }
     }
     if (!branch) continue;
@@ -404,7 +481,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
         acc[2][i][k] += o[k];
         d[i][k] = v * g[k];
       }
-      if (a.dgate_full && at.n[i] > 0) store8(a.dgate_full + row * a.ld_dgate + at.c[i], pack8(o), at.n[i]);
+      if (a.dgate_full) at.store(a.dgate_full + row * a.ld_dgate, i, o);
       if (post) {
         float y[8], w[8];
         unpack8(cur.y[i], y);
@@ -430,7 +507,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
         unpack8(cur.y[i], y);
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[k] = post ? rho_y * (d[i][k] - y[k] * rho_y * m2) : d[i][k];
-        if (at.n[i] > 0) store8(a.dy + row * a.lddy + at.c[i], pack8(o), at.n[i]);
+        at.store(a.dy + row * a.lddy, i, o);
       }
     }
   }
@@ -443,7 +520,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < at.n[i]) out[at.c[i] + k] = acc[j][i][k];
+        if (k >= at.first[i] && at.c[i] + k < cols) out[at.c[i] + k] = acc[j][i][k];
     out += cols;
   }
 }
@@ -493,10 +570,15 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
   // 16 without (wide rows have enough loads in flight: 4096 x 6144 with a full gate 56.3 us, 59.5 us by half the
   // waves with the next row on its way).
   const int threads = (cols + 511) / 512 * 64;  // 8 values each
-  if (cols <= 512) return go(norm_fwd_kernel<true, 1, 256, true>, even_groups((rows + 3) / 4, 5), 256);
-  if (cols <= 2048) return go(norm_fwd_kernel<false, 1, 256, true>, even_groups(rows, 1280 / threads), threads);
-  if (cols <= 8192) return go(norm_fwd_kernel<false, 1, 1024, false>, even_groups(rows, 1536 / threads), threads);
-  return go(norm_fwd_kernel<false, 2, 1024, false>, even_groups(rows, 1), 1024);
+  if (cols < 8) return go(norm_fwd_kernel<true, 1, 256, true, kTiny>, even_groups((rows + 3) / 4, 5), 256);
+  auto by_width = [&](auto tail) {
+    constexpr Tail T = decltype(tail)::value;
+    if (cols <= 512) return go(norm_fwd_kernel<true, 1, 256, true, T>, even_groups((rows + 3) / 4, 5), 256);
+    if (cols <= 2048) return go(norm_fwd_kernel<false, 1, 256, true, T>, even_groups(rows, 1280 / threads), threads);
+    if (cols <= 8192) return go(norm_fwd_kernel<false, 1, 1024, false, T>, even_groups(rows, 1536 / threads), threads);
+    return go(norm_fwd_kernel<false, 2, 1024, false, T>, even_groups(rows, 1), 1024);
+  };
+  return cols % 8 ? by_width(std::integral_constant<Tail, kOdd>{}) : by_width(std::integral_constant<Tail, kEven>{});
 }
 
 // Threads of a row in the backward pass: whole waves, one, two or four steps of 8 values each.
@@ -507,7 +589,7 @@ static int norm_bwd_threads(int64_t cols) {
 
 // (12 waves on a CU with 158 registers each, or 8 with 256)
 int64_t norm_bwd_groups(int64_t rows, int64_t cols) {
-  return even_groups(rows, (cols <= 2048 ? 768 : 512) / norm_bwd_threads(cols));
+  return even_groups(rows, 512 / norm_bwd_threads(cols));
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
@@ -522,10 +604,15 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     return hipGetLastError();
   };
   const int threads = norm_bwd_threads(cols);
-  hipError_t e;
-  if (cols <= 2048) e = go(norm_bwd_kernel<1, 256, true>, threads);
-  else if (cols <= 8192) e = go(norm_bwd_kernel<2, 512, true>, threads);
-  else e = go(norm_bwd_kernel<4, 512, false>, threads);
+  auto by_width = [&](auto tail) {
+    constexpr Tail T = decltype(tail)::value;
+    if (cols <= 2048) return go(norm_bwd_kernel<1, 256, true, T>, threads);
+    if (cols <= 8192) return go(norm_bwd_kernel<2, 512, true, T>, threads);
+    return go(norm_bwd_kernel<4, 512, false, T>, threads);
+  };
+  const hipError_t e = cols < 8   ? go(norm_bwd_kernel<1, 256, true, kTiny>, threads)
+                       : cols % 8 ? by_width(std::integral_constant<Tail, kOdd>{})
+                                  : by_width(std::integral_constant<Tail, kEven>{});
   if (e != hipSuccess || n_sums == 0) return e;
   const int width = n_sums * cols;
   hipLaunchKernelGGL(norm_colsum_kernel, dim3((width + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumSlices), 0, stream,

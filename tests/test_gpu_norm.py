@@ -90,7 +90,7 @@ def _check_backward(k, sc, dr, dx, g):
 
 
 SIZES = [(1, 1), (1, 2048), (3, 7), (5, 64), (2, 511), (4, 512), (3, 513), (1030, 520), (1025, 1000), (1100, 2048),
-         (7, 1536), (6, 2047), (5, 2056), (9, 4096), (2, 4100), (3, 5407), (2, 6144), (4, 8192), (2, 8193), (3, 16384),
+         (7, 1536), (6, 2047), (2600, 2047), (1300, 4099), (600, 9001), (9000, 5), (8000, 13), (3000, 8), (2500, 999), (5, 2056), (9, 4096), (2, 4100), (3, 5407), (2, 6144), (4, 8192), (2, 8193), (3, 16384),
          (2, 16383), (2, 12000)]
 
 
