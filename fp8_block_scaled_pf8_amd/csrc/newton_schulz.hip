@@ -21,8 +21,8 @@
 //    1 - a, and there the rounding of X would enter 2.4-fold. In a matrix of low rank the diagonal
 //    is small, and B' times the rounding alone, without the diagonal's part, would be noise outside
 //    of the matrix's column space, which grows by a in every step.
-//  * A matrix of at most 64 x 512 or 128 x 256 stays in one workgroup, and its X enters the products as a sum of
-//    two FP16 values (22 bits): few entries average out little of the rounding noise.
+//  * A matrix of at most 64 x 512 or 128 x 256 stays in one workgroup, and its X enters the update as a sum of
+//    two FP16 values (22 bits), diagonal or not: few entries average out little of the rounding noise.
 // Against float64, besides the BF16 rounding of the result (1.7e-3 of its 2-norm), the result is off
 // by up to 1.3e-3 of its 2-norm (2.8e-3 where a few entries carry the norm of a larger matrix); BF16
 // operands would give 1.4e-2.
@@ -748,134 +748,186 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
 }
 
 // ------------------------------------------------------------------------------ small matrices
-// One matrix of at most P x (NS P) per workgroup, all steps in one launch: (P/32)^2 waves hold one
-// 32x32 block of every P x P slab of X^T in registers (FP32); the products' operands go through LDS.
-// The slabs enter X X^T and B X as FP16 pairs (value and remainder), A' and B' as FP16.
-template <int P, int NS, typename T>
-__global__ __launch_bounds__((P / 32) * (P / 32) * 64) void ns_small_kernel(NsArgs a, NsCoef coef, int steps) {
-  constexpr int NB = P / 32, PITCH = P + 8;  // 16 rows' 16-byte reads of one column fall into different banks
+// One matrix of at most P x (NS P) per workgroup, all steps in one launch: the waves hold a WM x 32 part of every
+// P x P slab of X^T in registers (FP32); the products' operands go through LDS as FP16, X in the update as value
+// and remainder. 16 matrices of 128 x 128, five steps: 40 us with 16 waves of 32 x 32, 48 with 8 of 64 x 32.
+template <int P, int WM, int NS, typename T>
+__global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsArgs a, NsCoef coef, int steps) {
+  constexpr int TM = WM / 32, TN = 1, kWaves = (P / WM) * (P / 32), PITCH = P + 8;  // 16 rows' 16-byte reads of one column fall into different banks
   __shared__ __align__(16) _Float16 zh[P * PITCH], zl[P * PITCH], ab[P * PITCH];
   __shared__ float da[P], db[P];
-  __shared__ double red[NB * NB];
+  __shared__ double red[kWaves];
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int bi = wave / NB, bj = wave % NB;
+  const int r0 = wave / (P / 32) * WM, c0 = wave % (P / 32) * 32;
   const bool tall = a.m > a.n;
   const int p = static_cast<int>(tall ? a.n : a.m), q = static_cast<int>(tall ? a.m : a.n);
   const T* g = static_cast<const T*>(a.g) + blockIdx.x * a.stride_g;
-  const int m = 32 * bi + l32, n0 = 32 * bj + 4 * half;  // register 4 g + e: X^T[m][n0 + 8 g + e] of a slab
+  // register r = 4 g + e of block (bi, bj) is element (row(bi), col(bj, r)) of a slab of X^T, of A or of B
+  auto row = [&](int bi) { return r0 + 32 * bi + l32; };
+  auto col = [&](int bj, int r) { return c0 + 32 * bj + 4 * half + 8 * (r >> 2) + (r & 3); };
+  auto blocks = [&](auto f) {
+#pragma unroll
+    for (int bi = 0; bi < TM; ++bi)
+#pragma unroll
+      for (int bj = 0; bj < TN; ++bj) f(bi, bj);
+  };
 
-  float z[NS][16];
+  float z[NS][TM][TN][16];
   double sum = 0.0;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
+    blocks([&](int bi, int bj) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = n0 + 8 * (r >> 2) + (r & 3), j = s * P + m;
-      float v = 0.0f;
-      if (i < p && j < q) v = value<T>(tall ? g[j * a.ldg + i] : g[i * a.ldg + j]);
-      z[s][r] = v;
-      sum = __builtin_fma(static_cast<double>(v), static_cast<double>(v), sum);
-    }
-  sum = block_sum(sum, red);
-  const double scale = sum <= 1e300 ? 1.0 / (__builtin_sqrt(sum) + static_cast<double>(a.eps)) : __builtin_nan("");
+      for (int r = 0; r < 16; ++r) {
+        // (always a load, of the matrix's last row or column if need be: behind a branch each would be waited for)
+        const int i = min(col(bj, r), p - 1), j = min(s * P + row(bi), q - 1);
+        z[s][bi][bj][r] = value<T>(g[tall ? j * a.ldg + i : i * a.ldg + j]);
+      }
+    });
 #pragma unroll
   for (int s = 0; s < NS; ++s)
+    blocks([&](int bi, int bj) {
 #pragma unroll
-    // zeros outside the matrix stay zero, or turn NaN with every element inside it
-    for (int r = 0; r < 16; ++r) z[s][r] = static_cast<float>(static_cast<double>(z[s][r]) * scale);
+      for (int r = 0; r < 16; ++r) {
+        float& v = z[s][bi][bj][r];
+        v = col(bj, r) < p && s * P + row(bi) < q ? v : 0.0f;
+        sum = __builtin_fma(static_cast<double>(v), static_cast<double>(v), sum);
+      }
+    });
+  sum = block_sum(sum, red);
+  const double scale = sum <= 1e300 ? 1.0 / (__builtin_sqrt(sum) + static_cast<double>(a.eps)) : __builtin_nan("");
+  // zeros outside the matrix stay zero, or turn NaN with every element inside it
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    blocks([&](int bi, int bj) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) z[s][bi][bj][r] = static_cast<float>(static_cast<double>(z[s][bi][bj][r]) * scale);
+    });
 
-  auto frag = [&](const _Float16* mat, int row0, int k) {
-    return *reinterpret_cast<const h8*>(mat + (row0 + l32) * PITCH + 16 * k + 8 * half);
+  auto frag = [&](const _Float16* mat, int first, int k) {
+    return *reinterpret_cast<const h8*>(mat + (first + l32) * PITCH + 16 * k + 8 * half);
+  };
+  // four values as FP16 and what that leaves
+  auto split = [&](const float (&v)[16], int u, h4& h, h4& l) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[4 * u + e] * kSX;
+      h[e] = static_cast<_Float16>(x);
+      l[e] = static_cast<_Float16>(x - static_cast<float>(h[e]));
+    }
+  };
+  f16v acc[TM][TN];
+  auto clear = [&] {
+    blocks([&](int bi, int bj) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[bi][bj][r] = 0.0f;
+    });
   };
   for (int step = 0; step < steps; ++step) {
     const float ca = coef.v[step][0], cb = coef.v[step][1], cc = coef.v[step][2];
-    f16v acc;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+    clear();
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       if (s * P >= q) continue;  // uniform
       if (s) __syncthreads();
+      blocks([&](int bi, int bj) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int i = n0 + 8 * (r >> 2) + (r & 3);
-        const float v = z[s][r] * kSX;
-        const _Float16 h = static_cast<_Float16>(v);
-        zh[i * PITCH + m] = h;
-        zl[i * PITCH + m] = static_cast<_Float16>(v - static_cast<float>(h));
-      }
+        for (int u = 0; u < 4; ++u) {
+          h4 h, l;
+          split(z[s][bi][bj], u, h, l);
+          *reinterpret_cast<h4*>(zh + (col(bj, 4 * u) + (lane & 3)) * PITCH + (row(bi) & ~3)) = quad_transpose(h);
+        }
+      });
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < P / 16; ++k) {
-        const h8 ih = frag(zh, 32 * bi, k), il = frag(zl, 32 * bi, k), jh = frag(zh, 32 * bj, k), jl = frag(zl, 32 * bj, k);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(jl, ih, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(jh, il, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(jh, ih, acc, 0, 0, 0);
+        h8 fi[TM], fj[TN];
+#pragma unroll
+        for (int t = 0; t < TM; ++t) fi[t] = frag(zh, r0 + 32 * t, k);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) fj[t] = frag(zh, c0 + 32 * t, k);
+        blocks([&](int bi, int bj) { acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fj[bj], fi[bi], acc[bi][bj], 0, 0, 0); });
       }
     }
-    float x[16];  // A' as its FP16 values
+    h4 x[TM][TN][4];  // A'
+    blocks([&](int bi, int bj) {
+      const int m = row(bi);
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      h4 v;
+      for (int u = 0; u < 4; ++u) {
+        const int n = col(bj, 4 * u);
+        h4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool on = m == n0 + 2 * r + e;
-        if (on) da[m] = acc[r + e] * (1.0f / (kSX * kSX));
-        v[e] = on ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(acc[r + e] * (kSA / (kSX * kSX)));
-        x[r + e] = static_cast<float>(v[e]) * (1.0f / kSA);
+        for (int e = 0; e < 4; ++e) {
+          const float w = acc[bi][bj][4 * u + e];
+          if (m == n + e) da[m] = w * (1.0f / (kSX * kSX));
+          v[e] = m == n + e ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(w * (kSA / (kSX * kSX)));
+        }
+        x[bi][bj][u] = v;
+        *reinterpret_cast<h4*>(ab + m * PITCH + n) = v;
       }
-      *reinterpret_cast<h4*>(ab + m * PITCH + n0 + 2 * r) = v;
-    }
+    });
     __syncthreads();
+    clear();
 #pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+    for (int k = 0; k < P / 16; ++k) {
+      h8 fi[TM], fj[TN];
 #pragma unroll
-    for (int k = 0; k < P / 16; ++k)
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(frag(ab, 32 * bj, k), frag(ab, 32 * bi, k), acc, 0, 0, 0);
-    __syncthreads();  // A' has been read: B' takes its place
-    const float dm = da[m];
+      for (int t = 0; t < TM; ++t) fi[t] = frag(ab, r0 + 32 * t, k);
 #pragma unroll
-    for (int r = 0; r < 16; r += 4) {
-      h4 v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int n = n0 + 2 * r + e;
-        const float aa = acc[r + e] * (1.0f / (kSA * kSA));
-        const float b = m == n ? 0.0f : cb * x[r + e] + cc * (aa + (dm + da[n]) * x[r + e]);
-        if (m == n) db[m] = cb * dm + cc * (aa + dm * dm);
-        v[e] = static_cast<_Float16>(b * kSB);
-      }
-      *reinterpret_cast<h4*>(ab + m * PITCH + n0 + 2 * r) = v;
+      for (int t = 0; t < TN; ++t) fj[t] = frag(ab, c0 + 32 * t, k);
+      blocks([&](int bi, int bj) { acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fj[bj], fi[bi], acc[bi][bj], 0, 0, 0); });
     }
+    __syncthreads();  // A' has been read: B' takes its place
+    blocks([&](int bi, int bj) {
+      const int m = row(bi);
+      const float dm = da[m];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int n = col(bj, 4 * u);
+        h4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float aa = acc[bi][bj][4 * u + e] * (1.0f / (kSA * kSA)), w = static_cast<float>(x[bi][bj][u][e]) * (1.0f / kSA);
+          if (m == n + e) db[m] = cb * dm + cc * (aa + dm * dm);
+          v[e] = m == n + e ? static_cast<_Float16>(0.0f)
+                            : static_cast<_Float16>((cb * w + cc * (aa + (dm + da[n + e]) * w)) * kSB);
+        }
+        *reinterpret_cast<h4*>(ab + m * PITCH + n) = v;
+      }
+    });
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       if (s * P >= q) continue;
       if (s) __syncthreads();
+      blocks([&](int bi, int bj) {
 #pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        h4 h, l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = z[s][r + e] * kSX;
-          h[e] = static_cast<_Float16>(v);
-          l[e] = static_cast<_Float16>(v - static_cast<float>(h[e]));
+        for (int u = 0; u < 4; ++u) {
+          h4 h, l;
+          split(z[s][bi][bj], u, h, l);
+          *reinterpret_cast<h4*>(zh + row(bi) * PITCH + col(bj, 4 * u)) = h;
+          *reinterpret_cast<h4*>(zl + row(bi) * PITCH + col(bj, 4 * u)) = l;
         }
-        *reinterpret_cast<h4*>(zh + m * PITCH + n0 + 2 * r) = h;
-        *reinterpret_cast<h4*>(zl + m * PITCH + n0 + 2 * r) = l;
-      }
+      });
       __syncthreads();
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+      clear();
 #pragma unroll
       for (int k = 0; k < P / 16; ++k) {
-        const h8 b = frag(ab, 32 * bj, k);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, frag(zl, 32 * bi, k), acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, frag(zh, 32 * bi, k), acc, 0, 0, 0);
-      }
+        h8 fh[TM], fl[TM], fb[TN];
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        z[s][r] = (ca + db[n0 + 8 * (r >> 2) + (r & 3)]) * z[s][r] + acc[r] * (1.0f / (kSX * kSB));
+        for (int t = 0; t < TM; ++t) fh[t] = frag(zh, r0 + 32 * t, k), fl[t] = frag(zl, r0 + 32 * t, k);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) fb[t] = frag(ab, c0 + 32 * t, k);
+        blocks([&](int bi, int bj) {
+          acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[bj], fl[bi], acc[bi][bj], 0, 0, 0);
+          acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fb[bj], fh[bi], acc[bi][bj], 0, 0, 0);
+        });
+      }
+      blocks([&](int bi, int bj) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          z[s][bi][bj][r] = (ca + db[col(bj, r)]) * z[s][bi][bj][r] + acc[bi][bj][r] * (1.0f / (kSX * kSB));
+      });
     }
     __syncthreads();  // the last slab and B' have been read
   }
@@ -884,11 +936,13 @@ __global__ __launch_bounds__((P / 32) * (P / 32) * 64) void ns_small_kernel(NsAr
   asm volatile("" : "+s"(pe), "+s"(qe));  // the comparisons are made again, not kept from the loads
 #pragma unroll
   for (int s = 0; s < NS; ++s)
+    blocks([&](int bi, int bj) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int i = n0 + 8 * (r >> 2) + (r & 3), j = s * P + m;
-      if (i < pe && j < qe) out[tall ? j * a.ldo + i : i * a.ldo + j] = bf16_bits(z[s][r]);
-    }
+      for (int r = 0; r < 16; ++r) {
+        const int i = col(bj, r), j = s * P + row(bi);
+        if (i < pe && j < qe) out[tall ? j * a.ldo + i : i * a.ldo + j] = bf16_bits(z[s][bi][bj][r]);
+      }
+    });
 }
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -904,7 +958,7 @@ enum Shape { k64x64, k128x128, k128x256 };
 struct Plan {
   int64_t pp, qp;
   Shape gram, poly, update;
-  int gram_splits, poly_splits;  // parts of K; more than one only with 128x256 tiles
+  int gram_splits, poly_splits;  // parts of K: with 128x256 tiles, and where 64x64 tiles are few
 };
 
 // Tiles of a shape that cover the lower triangle.
@@ -918,11 +972,18 @@ int64_t rounds(int64_t tiles, int64_t slots) { return (tiles + slots - 1) / slot
 void plan_sym(int64_t pp, int64_t batch, int64_t k, Shape& shape, int& splits) {
   const double stages = static_cast<double>(k / 64);
   const int64_t t64 = batch * triangle_tiles(k64x64, pp), t128 = batch * triangle_tiles(k128x128, pp);
-  double best = t64 <= 256 ? 4.0 + 0.14 * stages : 5.0 + 0.3 * stages * static_cast<double>(rounds(t64, 512));
+  auto c64 = [&](int64_t parts, double n) {
+    return parts <= 256 ? 4.0 + 0.14 * n : 5.0 + 0.3 * n * static_cast<double>(rounds(parts, 512));
+  };
+  double best = c64(t64, stages);
   shape = k64x64;
   splits = 1;
+  for (int s = 2; s <= 32 && s <= k / 256; s *= 2) {
+    const double c = 4.0 + c64(t64 * s, stages / s) + 0.004 * static_cast<double>(t64 * s);
+    if (c < best) best = c, splits = s;
+  }
   const double c128 = 8.0 + 0.34 * stages * static_cast<double>(rounds(t128, 256));
-  if (c128 < best) best = c128, shape = k128x128;
+  if (c128 < best) best = c128, shape = k128x128, splits = 1;
   if (pp % 256) return;
   for (int s = 1; s <= 8 && s <= k / 512; ++s) {
     const int64_t parts = batch * triangle_tiles(k128x256, pp) * s;
@@ -930,6 +991,12 @@ void plan_sym(int64_t pp, int64_t batch, int64_t k, Shape& shape, int& splits) {
     const double c = 12.0 + 0.5 * stages / s * static_cast<double>(rounds(parts, 256)) + 0.032 * static_cast<double>(parts);
     if (c < best) best = c, shape = k128x256, splits = s;
   }
+}
+
+// Values of the split products' partial sums.
+int64_t part_elems(Shape shape, int splits, int64_t pp) {
+  const int64_t tile = shape == k128x256 ? 128 * 256 : shape == k64x64 && splits > 1 ? 64 * 64 : 0;
+  return triangle_tiles(shape, pp) * splits * tile;
 }
 
 Plan plan_of(int64_t batch, int64_t m, int64_t n) {
@@ -964,13 +1031,13 @@ hipError_t launch_small(const NsArgs& a, const NsCoef& coef, int steps, uint32_t
     return hipGetLastError();
   };
   if (p <= 64) {
-    if (q <= 64) return go(ns_small_kernel<64, 1, T>, 256);
-    if (q <= 128) return go(ns_small_kernel<64, 2, T>, 256);
-    if (q <= 256) return go(ns_small_kernel<64, 4, T>, 256);
-    return go(ns_small_kernel<64, 8, T>, 256);
+    if (q <= 64) return go(ns_small_kernel<64, 32, 1, T>, 256);
+    if (q <= 128) return go(ns_small_kernel<64, 32, 2, T>, 256);
+    if (q <= 256) return go(ns_small_kernel<64, 32, 4, T>, 256);
+    return go(ns_small_kernel<64, 32, 8, T>, 256);
   }
-  if (q <= 128) return go(ns_small_kernel<128, 1, T>, 1024);
-  return go(ns_small_kernel<128, 2, T>, 1024);
+  if (q <= 128) return go(ns_small_kernel<128, 32, 1, T>, 1024);
+  return go(ns_small_kernel<128, 32, 2, T>, 1024);
 }
 
 int64_t align256(int64_t v) { return round_up(v, 256); }
@@ -981,7 +1048,10 @@ template <bool POLY>
 static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, float cb, float cc, hipStream_t stream) {
   const uint32_t tiles = static_cast<uint32_t>(triangle_tiles(shape, a.pp));
   const dim3 grid(tiles, batch, static_cast<uint32_t>(splits));
-  if (shape == k64x64) {
+  if (shape == k64x64 && splits > 1) {
+    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, true>), grid, dim3(256), 0, stream, a, cb, cc);
+    hipLaunchKernelGGL((ns_finish_kernel<64, 64, POLY>), dim3(tiles, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
+  } else if (shape == k64x64) {
     hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
   } else if (shape == k128x128) {
     hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
@@ -1017,8 +1087,7 @@ static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base)
   uint8_t* b16 = take(batch * p.pp * ldp * 2);
   uint8_t* da = take(batch * p.pp * 4);
   uint8_t* db = take(batch * p.pp * 4);
-  auto parts = [&](Shape shape, int splits) { return shape == k128x256 ? triangle_tiles(shape, p.pp) * splits * 128 * 256 : 0; };
-  const int64_t gram = parts(p.gram, p.gram_splits), poly = parts(p.poly, p.poly_splits);
+  const int64_t gram = part_elems(p.gram, p.gram_splits, p.pp), poly = part_elems(p.poly, p.poly_splits, p.pp);
   uint8_t* part = take(batch * std::max(gram, poly) * 4);
   uint8_t* norm = take(batch * kNormBlocks * 8);
   if (a) {

@@ -93,7 +93,7 @@ def newton_schulz(g, coefficients, eps=1e-7):
 def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
     """newton_schulz with the FP16 roundings of a kernel's product operands, all else in float64.
 
-    X is kept; its rounding enters the products (with `pairs`, as value plus remainder). The
+    X is kept; its rounding enters the products (with `pairs`, in B X as value plus remainder). The
     diagonals of A = X X^T and of B = b A + c A A are kept, their other elements rounded. The
     diagonal of B multiplies X where its element is over 2/3 |a - 1| (with `pairs`, everywhere),
     X's rounding elsewhere.
@@ -107,7 +107,7 @@ def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
     for a, b, c in coefficients:
         xh = f16(x, 2.0 ** 12)
         xp = xh + (f16(x - xh, 2.0 ** 12) if pairs else 0.0)
-        gram = xp @ xp.T
+        gram = xh @ xh.T
         d = np.diag(gram).copy()
         gram = f16(gram * off, 2.0 ** 10)
         square = gram @ gram

@@ -69,8 +69,8 @@ def _check(out, g, coef=(COEF,) * 5, eps=1e-7, what=""):
         assert (np.abs(x - y) <= 2.0 ** -8 * np.abs(y) + most).all(), what
 
 
-SIZES = [(1, 1), (1, 512), (513, 2), (64, 65), (60, 250), (64, 512), (500, 40), (100, 256), (250, 128), (1, 300), (300, 1), (2, 3), (5, 64), (33, 33), (64, 64), (65, 127), (128, 128), (129, 128), (128, 130),
-         (200, 100), (127, 1000), (256, 640), (1000, 500), (513, 513), (16, 4099), (4100, 24), (384, 1537)]
+SIZES = [(1, 1), (1, 512), (513, 2), (64, 65), (60, 250), (64, 512), (500, 40), (100, 256), (250, 128), (128, 512), (400, 120), (512, 65), (1, 300), (300, 1), (2, 3), (5, 64), (33, 33), (64, 64), (65, 127), (128, 128), (129, 128), (128, 130),
+         (200, 100), (127, 1000), (256, 640), (1000, 500), (513, 513), (16, 4099), (4100, 24), (384, 1537), (40, 5000), (260, 6100), (9000, 130)]
 
 
 @pytest.mark.parametrize("m,n", SIZES)
