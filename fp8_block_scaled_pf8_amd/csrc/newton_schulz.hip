@@ -14,7 +14,7 @@
 //  * A and B = b A + c A A are split into their diagonals, kept in FP32, and the rest in FP16:
 //    near the end A is close to a multiple of the identity and the diagonal carries nearly all.
 //    (A A)_ij = sum A'_ik A'_kj + (d_i + d_j) A'_ij off the diagonal.
-//  * FP16 operands are scaled by powers of two (X 2^12, A 2^10, B 2^9), so that entries down to
+//  * FP16 operands (and X in FP32) are scaled by powers of two (X 2^12, A 2^10, B 2^9), so that entries down to
 //    2^-26 of the norm keep all their bits and singular values up to 8 stay in range.
 //  * The diagonal's part of B X takes a row of X in FP32 where the diagonal's element is large, and
 //    the row's FP16 rounding elsewhere (kOwnRow). A matrix of full rank ends with diagonals near
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
   const int b = blockIdx.y;
   const int tiles_q = static_cast<int>(a.qp / 64);
   const int64_t i0 = (blockIdx.x / tiles_q) * 64, j0 = (blockIdx.x % tiles_q) * 64;
-  const double s = inv_norm(a, b, red);
+  const double s = inv_norm(a, b, red) * static_cast<double>(kSX);
   const T* g = static_cast<const T*>(a.g) + b * a.stride_g;
   const bool tall = a.m > a.n;
   // read along G's rows: G[row][col] is X[row][col], or X[col][row] of a tall G
@@ -478,8 +478,8 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
     h8 u, v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      u[e] = static_cast<_Float16>(sh[r][c + e] * kSX);
-      v[e] = static_cast<_Float16>(sh[c + e][r] * kSX);
+      u[e] = static_cast<_Float16>(sh[r][c + e]);
+      v[e] = static_cast<_Float16>(sh[c + e][r]);
     }
     *reinterpret_cast<h8*>(xr + (i0 + r) * a.ldq + j0 + c) = u;
     *reinterpret_cast<h8*>(xc + (j0 + r) * a.ldp + i0 + c) = v;
@@ -498,10 +498,14 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
 __device__ __forceinline__ h4 gram_elements(const NsArgs& a, int b, int64_t m, int64_t n, f4 s) {
   h4 v;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const bool on = m == n + e;
-    if (on) a.da[b * a.pp + m] = s[e] * (1.0f / (kSX * kSX));
-    v[e] = on ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(s[e] * (kSA / (kSX * kSX)));
+  for (int e = 0; e < 4; ++e) v[e] = static_cast<_Float16>(s[e] * (kSA / (kSX * kSX)));
+  if (m >= n && m < n + 4) {  // the diagonal
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (m == n + e) {
+        a.da[b * a.pp + m] = s[e] * (1.0f / (kSX * kSX));
+        v[e] = static_cast<_Float16>(0.0f);
+      }
   }
   return v;
 }
@@ -513,13 +517,18 @@ __device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, i
   const float* d = a.da + b * a.pp;
   const float dm = d[m];
   const f4 dn = *reinterpret_cast<const f4*>(d + n);
+  const float from = (cb + cc * dm) * (kSB / kSA), by = cc * (kSB / kSA), squares = cc * (kSB / (kSA * kSA));
   h4 v;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float aa = s[e] * (1.0f / (kSA * kSA)), x = static_cast<float>(av[e]) * (1.0f / kSA);
-    const bool on = m == n + e;
-    if (on) a.db[b * a.pp + m] = cb * dm + cc * (aa + dm * dm);
-    v[e] = on ? static_cast<_Float16>(0.0f) : static_cast<_Float16>((cb * x + cc * (aa + (dm + dn[e]) * x)) * kSB);
+  for (int e = 0; e < 4; ++e)
+    v[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(av[e]), __builtin_fmaf(by, dn[e], from), squares * s[e]));
+  if (m >= n && m < n + 4) {  // the diagonal
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (m == n + e) {
+        a.db[b * a.pp + m] = cb * dm + cc * (s[e] * (1.0f / (kSA * kSA)) + dm * dm);
+        v[e] = static_cast<_Float16>(0.0f);
+      }
   }
   return v;
 }
@@ -690,6 +699,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const f4 dn = *reinterpret_cast<const f4*>(d + wn * WN + 32 * j + 8 * g + 4 * (lane >> 5));
+      bool own[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) own[e] = __builtin_fabsf(dn[e]) > own_from;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         f4 y;
@@ -697,11 +709,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
         else y = *x_at(i, j, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float low = static_cast<float>(static_cast<_Float16>(y[e] * kSX)) * (1.0f / kSX);
-          const float yd = __builtin_fabsf(dn[e]) > own_from ? y[e] : low;
-          y[e] = ca * y[e] + (dn[e] * yd + acc[i][j][4 * g + e] * (1.0f / (kSX * kSB)));
-          if (LAST) v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y[e]));
-          else v[i][j][g][e] = static_cast<_Float16>(y[e] * kSX);
+          const float yd = own[e] ? y[e] : static_cast<float>(static_cast<_Float16>(y[e]));
+          y[e] = __builtin_fmaf(ca, y[e], __builtin_fmaf(dn[e], yd, acc[i][j][4 * g + e] * (1.0f / kSB)));
+          if (LAST) v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y[e] * (1.0f / kSX)));
+          else v[i][j][g][e] = static_cast<_Float16>(y[e]);
         }
         if (!LAST) *x_at(i, j, g) = y;
       }
@@ -755,7 +766,7 @@ template <int P, int WM, int NS, typename T>
 __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsArgs a, NsCoef coef, int steps) {
   constexpr int TM = WM / 32, TN = 1, kWaves = (P / WM) * (P / 32), PITCH = P + 8;  // 16 rows' 16-byte reads of one column fall into different banks
   __shared__ __align__(16) _Float16 zh[P * PITCH], zl[P * PITCH], ab[P * PITCH];
-  __shared__ float da[P], db[P];
+  __shared__ __align__(16) float da[P], db[P];  // the diagonals of A, and of B plus a
   __shared__ double red[kWaves];
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -796,7 +807,8 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
       }
     });
   sum = block_sum(sum, red);
-  const double scale = sum <= 1e300 ? 1.0 / (__builtin_sqrt(sum) + static_cast<double>(a.eps)) : __builtin_nan("");
+  const double scale =
+      sum <= 1e300 ? static_cast<double>(kSX) / (__builtin_sqrt(sum) + static_cast<double>(a.eps)) : __builtin_nan("");
   // zeros outside the matrix stay zero, or turn NaN with every element inside it
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -812,7 +824,7 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
   auto split = [&](const float (&v)[16], int u, h4& h, h4& l) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = v[4 * u + e] * kSX;
+      const float x = v[4 * u + e];
       h[e] = static_cast<_Float16>(x);
       l[e] = static_cast<_Float16>(x - static_cast<float>(h[e]));
     }
@@ -850,20 +862,24 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
         blocks([&](int bi, int bj) { acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fj[bj], fi[bi], acc[bi][bj], 0, 0, 0); });
       }
     }
+    // (only the blocks on the diagonal look for it)
+    auto diagonal = [&](int bi, int bj) { return r0 + 32 * bi == c0 + 32 * bj; };
     h4 x[TM][TN][4];  // A'
     blocks([&](int bi, int bj) {
       const int m = row(bi);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int n = col(bj, 4 * u);
-        h4 v;
+        h4& v = x[bi][bj][u];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = acc[bi][bj][4 * u + e];
-          if (m == n + e) da[m] = w * (1.0f / (kSX * kSX));
-          v[e] = m == n + e ? static_cast<_Float16>(0.0f) : static_cast<_Float16>(w * (kSA / (kSX * kSX)));
+        for (int e = 0; e < 4; ++e) v[e] = static_cast<_Float16>(acc[bi][bj][4 * u + e] * (kSA / (kSX * kSX)));
+        if (diagonal(bi, bj)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (m == n + e) da[m] = acc[bi][bj][4 * u + e] * (1.0f / (kSX * kSX));
+            v[e] = m == n + e ? static_cast<_Float16>(0.0f) : v[e];
+          }
         }
-        x[bi][bj][u] = v;
         *reinterpret_cast<h4*>(ab + m * PITCH + n) = v;
       }
     });
@@ -882,16 +898,22 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
     blocks([&](int bi, int bj) {
       const int m = row(bi);
       const float dm = da[m];
+      const float from = (cb + cc * dm) * (kSB / kSA), by = cc * (kSB / kSA), squares = cc * (kSB / (kSA * kSA));
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int n = col(bj, 4 * u);
+        const f4 dn = *reinterpret_cast<const f4*>(da + n);
         h4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float aa = acc[bi][bj][4 * u + e] * (1.0f / (kSA * kSA)), w = static_cast<float>(x[bi][bj][u][e]) * (1.0f / kSA);
-          if (m == n + e) db[m] = cb * dm + cc * (aa + dm * dm);
-          v[e] = m == n + e ? static_cast<_Float16>(0.0f)
-                            : static_cast<_Float16>((cb * w + cc * (aa + (dm + da[n + e]) * w)) * kSB);
+        for (int e = 0; e < 4; ++e)
+          v[e] = static_cast<_Float16>(__builtin_fmaf(static_cast<float>(x[bi][bj][u][e]), __builtin_fmaf(by, dn[e], from),
+                                                      squares * acc[bi][bj][4 * u + e]));
+        if (diagonal(bi, bj)) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (m == n + e) db[m] = ca + cb * dm + cc * (acc[bi][bj][4 * u + e] * (1.0f / (kSA * kSA)) + dm * dm);
+            v[e] = m == n + e ? static_cast<_Float16>(0.0f) : v[e];
+          }
         }
         *reinterpret_cast<h4*>(ab + m * PITCH + n) = v;
       }
@@ -926,7 +948,7 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
       blocks([&](int bi, int bj) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          z[s][bi][bj][r] = (ca + db[col(bj, r)]) * z[s][bi][bj][r] + acc[bi][bj][r] * (1.0f / (kSX * kSB));
+          z[s][bi][bj][r] = __builtin_fmaf(db[col(bj, r)], z[s][bi][bj][r], acc[bi][bj][r] * (1.0f / kSB));
       });
     }
     __syncthreads();  // the last slab and B' have been read
@@ -940,7 +962,7 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
         const int i = col(bj, r), j = s * P + row(bi);
-        if (i < pe && j < qe) out[tall ? j * a.ldo + i : i * a.ldo + j] = bf16_bits(z[s][bi][bj][r]);
+        if (i < pe && j < qe) out[tall ? j * a.ldo + i : i * a.ldo + j] = bf16_bits(z[s][bi][bj][r] * (1.0f / kSX));
       }
     });
 }
