@@ -5,18 +5,19 @@
 // p^2 q multiply-adds for A and p^3 / 2 for A A, both symmetric and formed for their lower tiles
 // only, and p^2 q for the update.
 //
-// Number formats. The products run on FP16 operands with FP32 accumulation; everything that adds
-// up over the steps is FP32:
-//  * X itself is kept in FP32. The update adds a X from it; only the small product B X is formed
-//    from X's FP16 rounding. (Rounding X itself would put noise into directions whose singular
+// Number formats. The products run on FP16 operands with FP32 accumulation; what adds up over the
+// steps has more bits:
+//  * X itself is kept as the sum of two FP16 values, the operand and its remainder (22 bits, 8 bytes
+//    an element and step less to move than FP32 beside the operand: 12288 x 2048 in 1221 us, 1268). The
+//    update adds a X from both; only the small product B X is formed from X's FP16 rounding. (Rounding X itself would put noise into directions whose singular
 //    value is nearly zero, which the iteration multiplies by a in every step: a rank-one G came
 //    out 15 % off.)
 //  * A and B = b A + c A A are split into their diagonals, kept in FP32, and the rest in FP16:
 //    near the end A is close to a multiple of the identity and the diagonal carries nearly all.
 //    (A A)_ij = sum A'_ik A'_kj + (d_i + d_j) A'_ij off the diagonal.
-//  * FP16 operands (and X in FP32) are scaled by powers of two (X 2^12, A 2^10, B 2^9), so that entries down to
-//    2^-26 of the norm keep all their bits and singular values up to 8 stay in range.
-//  * The diagonal's part of B X takes a row of X in FP32 where the diagonal's element is large, and
+//  * FP16 values are scaled by powers of two (X 2^12, A 2^10, B 2^9), so that entries down to 2^-26 of
+//    the norm keep all an operand's bits and singular values up to 8 stay in range.
+//  * The diagonal's part of B X takes a row of X whole where the diagonal's element is large, and
 //    the row's FP16 rounding elsewhere (kOwnRow). A matrix of full rank ends with diagonals near
 //    1 - a, and there the rounding of X would enter 2.4-fold. In a matrix of low rank the diagonal
 //    is small, and B' times the rounding alone, without the diagonal's part, would be noise outside
@@ -29,8 +30,8 @@
 //
 // Layout. X lives in the workspace, padded to multiples of 128 with zeros that stay zero, so the
 // products have no edges: Xr [p][q] (A's operand), Xc [q][p] (the update's operand, two buffers in
-// turn) and FP32 in 64x64 regions in the order the update's lanes hold them, so that each lane
-// reads and writes 16 consecutive bytes. FP16 rows are 128 bytes longer than that: a tile's loads read
+// turn) and the remainders in 64x64 regions in the order the update's lanes hold them, so that each
+// lane reads and writes 16 consecutive bytes. FP16 rows are 128 bytes longer than that: a tile's loads read
 // the same columns of many rows, and with a pitch of 4 KiB or a multiple they crowd a few channels.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -59,13 +60,17 @@ constexpr float kSX = 4096.0f, kSA = 1024.0f, kSB = 512.0f;  // powers of two th
 constexpr int kRegion = 64 * 64;
 constexpr int64_t kPad = 64;  // values that FP16 rows are longer than padded: see "Layout"
 // a diagonal element of B over this part of |a - 1| (which a matrix of full rank with singular values
-// near one has) multiplies X in FP32
+// near one has) multiplies X whole
 constexpr float kOwnRow = 2.0f / 3.0f;
 
 // In a 64x64 region of a product, block (bi, bj) of 32x32 and register 4 g + e of lane l hold the
-// element (32 bi + l % 32, 32 bj + 8 g + 4 (l / 32) + e).
+// element (32 bi + l % 32, 32 bj + 8 g + 4 (l / 32) + e). FP32 sums lie there four registers a lane, the
+// remainders of X (FP16) eight, those of two g.
 __device__ __forceinline__ int region_offset(int bi, int bj, int g, int lane) {
   return ((bi * 2 + bj) * 4 + g) * 256 + lane * 4;
+}
+__device__ __forceinline__ int rest_offset(int bi, int bj, int pair, int lane) {
+  return ((bi * 2 + bj) * 2 + pair) * 512 + lane * 8;
 }
 
 // Up to four stage buffers.
@@ -80,26 +85,26 @@ struct Buffers {
   }
 };
 
-// D[m, n] = sum_k P[m, k] Q[n, k] over `steps` stages of BK (a multiple of 128 values in all): a BM x BN tile by (BM/WM)(BN/WN) waves.
-// Stages go straight to LDS (16 bytes a lane) into NST buffers, NST - 1 to NST ahead of use. In an LDS row of
-// BK values, chunk c (16 bytes) of row r sits at c ^ ((r >> 1) & 7) (128-byte rows) or c ^ ((r >> 2) & 3)
-// (64-byte rows): 16 consecutive rows' reads of one chunk fall into the 16 different 16-byte slots of the
-// 64 banks. One barrier a stage, in its middle, while the matrix cores still have the stage's second half
+// D[m, n] = sum_k P[m, k] Q[n, k] over an even number of stages of 64 values each: a BM x BN tile by
+// (BM/WM)(BN/WN) waves. Stages go straight to LDS (16 bytes a lane) into NST buffers, NST - 1 to NST ahead of
+// use, in rows of 128 bytes (of 64 bytes, such loads come at half the rate). Chunk c (16 bytes) of row r sits
+// at c ^ ((r >> 1) & 7): 16 consecutive rows' reads of one chunk fall into the 16 different 16-byte slots of
+// the 64 banks. One barrier a stage, in its middle, while the matrix cores still have the stage's second half
 // to do: behind it every wave's loads of the next stage have landed, and the stage's own buffer, whose
 // operands are all in registers, is free to be filled again. The buffers are LDS objects of their own, so that the
 // compiler sees that a read of one does not wait for loads into another.
-template <int BM, int BN, int WM, int WN, int BK, int NST>
+template <int BM, int BN, int WM, int WN, int NST>
 struct Tile {
   static constexpr int kWavesN = BN / WN, kWaves = (BM / WM) * kWavesN, kThreads = 64 * kWaves;
   static constexpr int TM = WM / 32, TN = WN / 32;
-  static constexpr int kRow = BK * 2, kStage = (BM + BN) * kRow;
+  static constexpr int BK = 64, kRow = BK * 2, kStage = (BM + BN) * kRow;
   static constexpr int kSlab = 1024 / kRow;  // rows of one load (64 lanes x 16 bytes)
   static constexpr int kLoadsP = BM / kSlab / kWaves, kLoads = kLoadsP + BN / kSlab / kWaves;
-  static_assert(BM / kSlab % kWaves == 0 && BN / kSlab % kWaves == 0 && (BK == 32 || BK == 64), "even loads");
+  static_assert(BM / kSlab % kWaves == 0 && BN / kSlab % kWaves == 0, "even loads");
   static_assert(NST >= 2 && NST <= 4, "up to four buffers");
   typedef f16v Acc[TM][TN];
 
-  static __device__ __forceinline__ int swizzle(int row) { return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+  static __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 
   // f(0), f(1), ... with compile-time arguments
   template <typename F, int... V>
@@ -246,8 +251,8 @@ struct Tile {
       sync_stage(std::integral_constant<int, (n - 1) * kLoads + (decltype(more)::value ? kLoadsP : 0)>{});
       read(H0{}, bufs.b0);
     };
-    // `steps` is a multiple of 128 / BK; where NST is one too, so is what the main loop leaves
-    constexpr int kUnit = NST % (128 / BK) == 0 ? 128 / BK : 1;
+    // `steps` is even; where NST is too, so is what the main loop leaves
+    constexpr int kUnit = NST % 2 == 0 ? 2 : 1;
     if (steps < NST) {
       each(
           [&](auto v_c) {
@@ -449,7 +454,12 @@ __device__ __forceinline__ double inv_norm(const NsArgs& a, int batch, double* s
   return 1.0 / (__builtin_sqrt(s) + static_cast<double>(a.eps));
 }
 
-// One 64x64 block of X: FP32 regions, Xr and Xc from G, zeros outside.
+// What FP16 leaves of a value.
+__device__ __forceinline__ _Float16 remainder16(float x) {
+  return static_cast<_Float16>(x - static_cast<float>(static_cast<_Float16>(x)));
+}
+
+// One 64x64 block of X: Xr, Xc and the remainders from G, zeros outside.
 template <typename T>
 __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
   __shared__ double red[4];
@@ -484,11 +494,14 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
     *reinterpret_cast<h8*>(xr + (i0 + r) * a.ldq + j0 + c) = u;
     *reinterpret_cast<h8*>(xc + (j0 + r) * a.ldp + i0 + c) = v;
   }
-  float* xf = a.xf + b * a.x_elems + ((j0 / 64) * (a.pp / 64) + i0 / 64) * kRegion;
-  for (int t = threadIdx.x; t < kRegion / 4; t += 256) {
-    const int lane = t & 63, gq = (t >> 6) & 3, bj = (t >> 8) & 1, bi = t >> 9;
-    const int m = 32 * bi + (lane & 31), n = 32 * bj + 8 * gq + 4 * (lane >> 5);
-    *reinterpret_cast<f4*>(xf + region_offset(bi, bj, gq, lane)) = f4{sh[n][m], sh[n + 1][m], sh[n + 2][m], sh[n + 3][m]};
+  _Float16* rest = a.rest + b * a.x_elems + ((j0 / 64) * (a.pp / 64) + i0 / 64) * kRegion;
+  for (int t = threadIdx.x; t < kRegion / 8; t += 256) {
+    const int lane = t & 63, pair = (t >> 6) & 1, bj = (t >> 7) & 1, bi = t >> 8;
+    const int m = 32 * bi + (lane & 31), n = 32 * bj + 16 * pair + 4 * (lane >> 5);
+    h8 v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = remainder16(sh[n + (e & 3) + 2 * (e & 4)][m]);
+    *reinterpret_cast<h8*>(rest + rest_offset(bi, bj, pair, lane)) = v;
   }
 }
 
@@ -538,7 +551,7 @@ __device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, i
 // Otherwise a workgroup makes a whole tile and finishes it.
 template <int BM, int BN, int WM, int WN, int NST, bool POLY, bool SPLIT>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, float cb, float cc) {
-  using G = Tile<BM, BN, WM, WN, 64, NST>;
+  using G = Tile<BM, BN, WM, WN, NST>;
   constexpr int TM = G::TM, TN = G::TN;
   PF8_NS_BUFFERS(bufs, G, NST);
   const int b = blockIdx.y;
@@ -651,10 +664,20 @@ __device__ __forceinline__ void store_row(uint16_t* p, h8 v, int64_t n) {
     if (e < n) p[e] = w[e];
 }
 
-// X's FP32 values are read before the product, so that they arrive behind its first stages.
-template <int BM, int BN, int WM, int WN, int BK, int NST, bool LAST>
+// Lanes l and l + 32 hold 8 columns each, 8 c .. and 8 (c + 1) ..; afterwards l has the first four of both,
+// l + 32 the last four.
+__device__ __forceinline__ h8 swap_halves(h8 v) {
+  uint4 w = __builtin_bit_cast(uint4, v);
+  const auto p = __builtin_amdgcn_permlane32_swap(w.x, w.z, false, false);
+  const auto q = __builtin_amdgcn_permlane32_swap(w.y, w.w, false, false);
+  w.x = p[0], w.z = p[1], w.y = q[0], w.w = q[1];
+  return __builtin_bit_cast(h8, w);
+}
+
+// X is read before the product, so that it arrives behind its first stages.
+template <int BM, int BN, int WM, int WN, int NST, bool LAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, int turn) {
-  using G = Tile<BM, BN, WM, WN, BK, NST>;
+  using G = Tile<BM, BN, WM, WN, NST>;
   constexpr int TM = G::TM, TN = G::TN;
   PF8_NS_BUFFERS(bufs, G, NST);
   const bool tall = a.m > a.n;
@@ -672,24 +695,26 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / (BN / WN), wn = wave % (BN / WN);
-  auto x_at = [&](int i, int j, int g) {
+  // X as it was: a lane reads 8 consecutive columns of X^T, those of its half of the wave's lanes (pair of g) ..
+  auto rest_at = [&](int i, int j, int pair) {
     const int m = wm * WM + 32 * i, n = wn * WN + 32 * j;
     const int64_t region = ((j0 + m) / 64) * (a.pp / 64) + (i0 + n) / 64;
-    return reinterpret_cast<f4*>(a.xf + b * a.x_elems + region * kRegion + region_offset((m >> 5) & 1, (n >> 5) & 1, g, lane));
+    return reinterpret_cast<h8*>(a.rest + b * a.x_elems + region * kRegion + rest_offset((m >> 5) & 1, (n >> 5) & 1, pair, lane));
   };
-  constexpr bool kEarly = TM * TN <= 4;  // more would not fit the registers
-  f4 x[kEarly ? TM : 1][kEarly ? TN : 1][4];
-  if constexpr (kEarly) {
+  h8 xh[TM][TN][2], xl[TM][TN][2];
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) x[i][j][g] = *x_at(i, j, g);
-  }
+      for (int pair = 0; pair < 2; ++pair) {
+        const int m = wm * WM + 32 * i + (lane & 31), n = wn * WN + 32 * j + 16 * pair + 8 * (lane >> 5);
+        xh[i][j][pair] = *reinterpret_cast<const h8*>(xc + (j0 + m) * a.ldp + i0 + n);
+        xl[i][j][pair] = *rest_at(i, j, pair);
+      }
   typename G::Acc acc;
   G::zero(acc);
-  G::run(xc + j0 * a.ldp, a.ldp, B + i0 * a.ldp, a.ldp, 0, static_cast<int>(a.pp / BK), bufs, acc);
+  G::run(xc + j0 * a.ldp, a.ldp, B + i0 * a.ldp, a.ldp, 0, static_cast<int>(a.pp / G::BK), bufs, acc);
 
   const float own_from = kOwnRow * __builtin_fabsf(ca - 1.0f);
   const float* d = a.db + b * a.pp + i0;
@@ -697,24 +722,33 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
 #pragma unroll
   for (int j = 0; j < TN; ++j)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const f4 dn = *reinterpret_cast<const f4*>(d + wn * WN + 32 * j + 8 * g + 4 * (lane >> 5));
-      bool own[4];
+    for (int pair = 0; pair < 2; ++pair) {
+      f4 dn[2];
+      bool own[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) own[e] = __builtin_fabsf(dn[e]) > own_from;
+      for (int h = 0; h < 2; ++h) {
+        dn[h] = *reinterpret_cast<const f4*>(d + wn * WN + 32 * j + 8 * (2 * pair + h) + 4 * (lane >> 5));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own[4 * h + e] = __builtin_fabsf(dn[h][e]) > own_from;
+      }
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        f4 y;
-        if constexpr (kEarly) y = x[i][j][g];
-        else y = *x_at(i, j, g);
+        // .. and the halves exchange, so that it has the four columns of each g that its sums belong to
+        const h8 hi = swap_halves(xh[i][j][pair]);
+        h8 lo = xl[i][j][pair];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float yd = own[e] ? y[e] : static_cast<float>(static_cast<_Float16>(y[e]));
-          y[e] = __builtin_fmaf(ca, y[e], __builtin_fmaf(dn[e], yd, acc[i][j][4 * g + e] * (1.0f / kSB)));
-          if (LAST) v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y[e] * (1.0f / kSX)));
-          else v[i][j][g][e] = static_cast<_Float16>(y[e]);
+        for (int k = 0; k < 8; ++k) {
+          const int h = k >> 2, e = k & 3, g = 2 * pair + h;
+          const float yh = static_cast<float>(hi[k]), x = yh + static_cast<float>(lo[k]);
+          const float y = __builtin_fmaf(ca, x, __builtin_fmaf(dn[h][e], own[k] ? x : yh, acc[i][j][4 * g + e] * (1.0f / kSB)));
+          if (LAST) {
+            v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y * (1.0f / kSX)));
+          } else {
+            v[i][j][g][e] = static_cast<_Float16>(y);
+            lo[k] = remainder16(y);
+          }
         }
-        if (!LAST) *x_at(i, j, g) = y;
+        if (!LAST) *rest_at(i, j, pair) = lo;
       }
     }
   // out through LDS, as rows of X^T and as rows of X
@@ -1000,7 +1034,8 @@ void plan_sym(int64_t pp, int64_t batch, int64_t k, Shape& shape, int& splits) {
   double best = c64(t64, stages);
   shape = k64x64;
   splits = 1;
-  for (int s = 2; s <= 32 && s <= k / 256; s *= 2) {
+  // (with no more than pp values along K the parts never come out cheaper)
+  for (int s = 2; k > pp && s <= 32 && s <= k / 256; s *= 2) {
     const double c = 4.0 + c64(t64 * s, stages / s) + 0.004 * static_cast<double>(t64 * s);
     if (c < best) best = c, splits = s;
   }
@@ -1070,10 +1105,14 @@ template <bool POLY>
 static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, float cb, float cc, hipStream_t stream) {
   const uint32_t tiles = static_cast<uint32_t>(triangle_tiles(shape, a.pp));
   const dim3 grid(tiles, batch, static_cast<uint32_t>(splits));
-  if (shape == k64x64 && splits > 1) {
-    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, true>), grid, dim3(256), 0, stream, a, cb, cc);
-    hipLaunchKernelGGL((ns_finish_kernel<64, 64, POLY>), dim3(tiles, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
-  } else if (shape == k64x64) {
+  if constexpr (!POLY) {
+    if (shape == k64x64 && splits > 1) {
+      hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, false, true>), grid, dim3(256), 0, stream, a, cb, cc);
+      hipLaunchKernelGGL((ns_finish_kernel<64, 64, false>), dim3(tiles, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
+      return;
+    }
+  }
+  if (shape == k64x64) {
     hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
   } else if (shape == k128x128) {
     hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
@@ -1087,12 +1126,12 @@ template <bool LAST>
 static void launch_update(const NsArgs& a, Shape shape, uint32_t batch, float ca, int turn, hipStream_t stream) {
   const int64_t bm = shape == k64x64 ? 64 : 128, bn = shape == k64x64 ? 64 : shape == k128x128 ? 128 : 256;
   const dim3 grid(static_cast<uint32_t>((a.qp / bm) * (a.pp / bn)), batch);
-  if (shape == k64x64) hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 32, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
-  else if (shape == k128x128) hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 64, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
-  else hipLaunchKernelGGL((ns_update_kernel<128, 256, 64, 64, 64, 3, LAST>), grid, dim3(512), 0, stream, a, ca, turn);
+  if (shape == k64x64) hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 32, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
+  else if (shape == k128x128) hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
+  else hipLaunchKernelGGL((ns_update_kernel<128, 256, 64, 64, 3, LAST>), grid, dim3(512), 0, stream, a, ca, turn);
 }
 
-// Workspace parts, in order: FP32 X, two Xc, Xr, A, B, their diagonals, A's partial tiles, norms.
+// Workspace parts, in order: X's remainders, two Xc, Xr, A, B, their diagonals, A's partial tiles, norms.
 static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base) {
   const int64_t x = p.pp * p.qp, ldp = p.pp + kPad, ldq = p.qp + kPad;
   int64_t at = 0;
@@ -1101,7 +1140,7 @@ static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base)
     at += align256(bytes);
     return r;
   };
-  uint8_t* xf = take(batch * x * 4);
+  uint8_t* rest = take(batch * x * 2);
   uint8_t* xc0 = take(batch * p.qp * ldp * 2);
   uint8_t* xc1 = take(batch * p.qp * ldp * 2);
   uint8_t* xr = take(batch * p.pp * ldq * 2);
@@ -1114,7 +1153,7 @@ static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base)
   uint8_t* norm = take(batch * kNormBlocks * 8);
   if (a) {
     a->pp = p.pp, a->qp = p.qp, a->ldp = ldp, a->ldq = ldq, a->x_elems = x;
-    a->xf = reinterpret_cast<float*>(xf);
+    a->rest = reinterpret_cast<_Float16*>(rest);
     a->xc[0] = reinterpret_cast<_Float16*>(xc0), a->xc[1] = reinterpret_cast<_Float16*>(xc1);
     a->xr = reinterpret_cast<_Float16*>(xr);
     a->a16 = reinterpret_cast<_Float16*>(a16), a->b16 = reinterpret_cast<_Float16*>(b16);

@@ -71,8 +71,7 @@ struct NsArgs {
   int64_t pp, qp;   // padded min(m, n) and max(m, n)
   int64_t ldp, ldq;  // pitches of FP16 rows of pp and of qp values
   int64_t x_elems;   // pp * qp
-  float* xf;
-  _Float16 *xc[2], *xr, *a16, *b16;
+  _Float16 *rest, *xc[2], *xr, *a16, *b16;
   float *da, *db, *part;
   double* norm_part;
 };
