@@ -7,7 +7,7 @@
 //
 // Number formats. The products run on FP16 operands with FP32 accumulation; what adds up over the
 // steps has more bits:
-//  * X itself is kept as the sum of two FP16 values, the operand and its remainder (22 bits, 8 bytes
+//  * X itself is kept as the sum of two FP16 values, the operand and its remainder (22 bits, 4 bytes
 //    an element and step less to move than FP32 beside the operand: 12288 x 2048 in 1221 us, 1268). The
 //    update adds a X from both; only the small product B X is formed from X's FP16 rounding. (Rounding X itself would put noise into directions whose singular
 //    value is nearly zero, which the iteration multiplies by a in every step: a rank-one G came
@@ -29,9 +29,10 @@
 // operands would give 1.4e-2.
 //
 // Layout. X lives in the workspace, padded to multiples of 128 with zeros that stay zero, so the
-// products have no edges: Xr [p][q] (A's operand), Xc [q][p] (the update's operand, two buffers in
-// turn) and the remainders in 64x64 regions in the order the update's lanes hold them, so that each
-// lane reads and writes 16 consecutive bytes. FP16 rows are 128 bytes longer than that: a tile's loads read
+// products have no edges: Xc [q][p] (two buffers in turn; the update's operand, and A's by transposing
+// reads of LDS: a copy [p][q] for A cost 12288 x 2048 another 49 us of 1144) and the remainders in
+// 64x64 regions in the order the update's lanes hold them, so that each lane reads and writes 16
+// consecutive bytes. FP16 rows are 128 bytes longer than that: a tile's loads read
 // the same columns of many rows, and with a pitch of 4 KiB or a multiple they crowd a few channels.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -48,6 +49,7 @@ namespace {
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 
@@ -86,25 +88,33 @@ struct Buffers {
 };
 
 // D[m, n] = sum_k P[m, k] Q[n, k] over an even number of stages of 64 values each: a BM x BN tile by
-// (BM/WM)(BN/WN) waves. Stages go straight to LDS (16 bytes a lane) into NST buffers, NST - 1 to NST ahead of
-// use, in rows of 128 bytes (of 64 bytes, such loads come at half the rate). Chunk c (16 bytes) of row r sits
-// at c ^ ((r >> 1) & 7): 16 consecutive rows' reads of one chunk fall into the 16 different 16-byte slots of
-// the 64 banks. One barrier a stage, in its middle, while the matrix cores still have the stage's second half
+// (BM/WM)(BN/WN) waves. The operands lie in memory with m and n as rows, or with k as rows (KROWS). Stages
+// go straight to LDS (16 bytes a lane) into NST buffers, NST - 1 to NST ahead of use, in rows of 128 bytes or
+// more (of 64 bytes, such loads come at half the rate). Their 16-byte chunks change places:
+//  * rows of m or n: chunk c of row r sits at c ^ ((r >> 1) & 7), and 16 consecutive rows' reads of one
+//    chunk fall into the 16 different 16-byte slots of the 64 banks;
+//  * rows of k: transposing reads of 4 rows x 64 bytes by 32 lanes; c ^ 4 (r & 3), with 128-byte rows
+//    c ^ 4 (r / 2 & 1), spreads them over all banks.
+// One barrier a stage, in its middle, while the matrix cores still have the stage's second half
 // to do: behind it every wave's loads of the next stage have landed, and the stage's own buffer, whose
-// operands are all in registers, is free to be filled again. The buffers are LDS objects of their own, so that the
-// compiler sees that a read of one does not wait for loads into another.
-template <int BM, int BN, int WM, int WN, int NST>
+// operands are all in registers, is free to be filled again. The buffers are LDS objects of their own, so that
+// the compiler sees that a read of one does not wait for loads into another.
+template <int BM, int BN, int WM, int WN, int NST, bool KROWS>
 struct Tile {
   static constexpr int kWavesN = BN / WN, kWaves = (BM / WM) * kWavesN, kThreads = 64 * kWaves;
   static constexpr int TM = WM / 32, TN = WN / 32;
   static constexpr int BK = 64, kRow = BK * 2, kStage = (BM + BN) * kRow;
-  static constexpr int kSlab = 1024 / kRow;  // rows of one load (64 lanes x 16 bytes)
-  static constexpr int kLoadsP = BM / kSlab / kWaves, kLoads = kLoadsP + BN / kSlab / kWaves;
-  static_assert(BM / kSlab % kWaves == 0 && BN / kSlab % kWaves == 0, "even loads");
+  static constexpr int kLoadsP = BM * kRow / 1024 / kWaves, kLoads = kStage / 1024 / kWaves;  // of 64 lanes x 16 bytes
+  static_assert(BM * kRow / 1024 % kWaves == 0 && BN * kRow / 1024 % kWaves == 0, "even loads");
   static_assert(NST >= 2 && NST <= 4, "up to four buffers");
   typedef f16v Acc[TM][TN];
 
-  static __device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
+  // what the chunks of an LDS row change places by; ROW: its bytes
+  template <int ROW>
+  static __device__ __forceinline__ int swizzle(int row) {
+    if constexpr (!KROWS) return (row >> 1) & 7;
+    else return ROW == 128 ? (row >> 1 & 1) << 2 : (row & 3) << 2;
+  }
 
   // f(0), f(1), ... with compile-time arguments
   template <typename F, int... V>
@@ -121,32 +131,59 @@ struct Tile {
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   }
 
-  static __device__ __forceinline__ void run(const _Float16* P, int64_t ldp, const _Float16* Q, int64_t ldq, int k0,
+  static __device__ __forceinline__ void run(const _Float16* P, int64_t ldp, const _Float16* Q, int64_t ldq, int64_t k0,
                                              int steps, const Buffers& bufs, Acc& acc) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kWavesN, wn = wave % kWavesN;
-    const int ldpb = static_cast<int>(ldp) * 2, ldqb = static_cast<int>(ldq) * 2;
-    const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(P), 0, BM * ldpb, 0x00020000);
-    const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(Q), 0, BN * ldqb, 0x00020000);
-    constexpr int kChunks = kRow / 16;
-    const int lrow = lane / kChunks;  // the lane's row in a load, and below the chunk that belongs at its place
-    // part 0: P's loads of a stage, 1: Q's
-    auto issue = [&](auto part, uint8_t* buf, int s) {
-      const int kofs = (k0 + s * BK) * 2;
-      constexpr int from = decltype(part)::value ? kLoadsP : 0, to = decltype(part)::value ? kLoads : kLoadsP;
+    // a wave's loads `from` to `to` of one operand's part of a stage, W values wide (of rows or of columns)
+    auto issue_part = [&](auto w_c, const _Float16* X, int64_t ld, uint8_t* buf, int s, auto from, auto to) {
+      constexpr int W = decltype(w_c)::value;
+      constexpr int kLine = KROWS ? W * 2 : kRow, kLines = KROWS ? BK : W, kChunks = kLine / 16, kSlab = 1024 / kLine;
+      const int64_t k = k0 + static_cast<int64_t>(s) * BK;
+      const int pitch = static_cast<int>(ld) * 2;
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16*>(X + (KROWS ? k * ld : k)), 0,
+                                                                        (kLines - 1) * pitch + kLine, 0x00020000);
+      const int line = lane / kChunks;
 #pragma unroll
-      for (int i = from; i < to; ++i) {
+      for (int i = decltype(from)::value; i < decltype(to)::value; ++i) {
         const int slab = wave + i * kWaves;
-        const int chunk = (lane % kChunks) ^ swizzle(slab * kSlab + lrow);
+        const int chunk = (lane % kChunks) ^ swizzle<kLine>(slab * kSlab + line);
         auto* dst = (__attribute__((address_space(3))) void*)(buf + slab * 1024);
-        if (i < kLoadsP) __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, dst, 16, lrow * ldpb + chunk * 16, slab * kSlab * ldpb + kofs, 0, 0);
-        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, dst, 16, lrow * ldqb + chunk * 16, (slab * kSlab - BM) * ldqb + kofs, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, line * pitch + chunk * 16, slab * kSlab * pitch, 0, 0);
       }
     };
+    // part 0: P's loads of a stage, 1: Q's
+    auto issue = [&](auto part, uint8_t* buf, int s) {
+      using Zero = std::integral_constant<int, 0>;
+      if constexpr (decltype(part)::value == 0)
+        issue_part(std::integral_constant<int, BM>{}, P, ldp, buf, s, Zero{}, std::integral_constant<int, kLoadsP>{});
+      else
+        issue_part(std::integral_constant<int, BN>{}, Q, ldq, buf + BM * kRow, s, Zero{}, std::integral_constant<int, kLoads - kLoadsP>{});
+    };
+    using H0 = std::integral_constant<int, 0>;
+    using H1 = std::integral_constant<int, 1>;
     const int l32 = lane & 31, half = lane >> 5;
-    auto frag = [&](const uint8_t* buf, int row, int k) {
-      return *reinterpret_cast<const h8*>(buf + row * kRow + (((2 * k + half) ^ swizzle(row)) << 4));
+    // 8 values along K of each lane's row of P (Q 0) or Q (1). (All that is added to the buffer is added up first:
+    // the compiler loses sight of whose LDS a read is in after a few steps of pointer arithmetic.)
+    auto frag = [&](auto q_c, const uint8_t* buf, int first, int k) {
+      constexpr int W = decltype(q_c)::value ? BN : BM, from = decltype(q_c)::value ? BM * kRow : 0;
+      if constexpr (!KROWS) {
+        const int row = first + l32;
+        return *reinterpret_cast<const h8*>(buf + (from + row * kRow + (((2 * k + half) ^ swizzle<kRow>(row)) << 4)));
+      } else {
+        // 16 lanes read 4 rows of 16 values and hold their columns
+        constexpr int kLine = W * 2;
+        const int col = first + (lane & 16) + (lane & 3) * 4;
+        h4 v[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row = 16 * k + 8 * half + 4 * t + (lane >> 2 & 3);
+          const uint8_t* p = buf + (from + row * kLine + (((col >> 3) ^ swizzle<kLine>(row)) << 4) + (col & 4) * 2);
+          v[t] = __builtin_bit_cast(h4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4*)(p)));
+        }
+        return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      }
     };
     // operands of the first (0) or second (1) half of a stage's k-steps
     constexpr int kHalf = BK / 32;
@@ -156,9 +193,9 @@ struct Tile {
 #pragma unroll
       for (int k = 0; k < kHalf; ++k) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fp[h][k][i] = frag(buf, wm * WM + 32 * i + l32, h * kHalf + k);
+        for (int i = 0; i < TM; ++i) fp[h][k][i] = frag(H0{}, buf, wm * WM + 32 * i, h * kHalf + k);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) fq[h][k][j] = frag(buf, BM + wn * WN + 32 * j + l32, h * kHalf + k);
+        for (int j = 0; j < TN; ++j) fq[h][k][j] = frag(H1{}, buf, wn * WN + 32 * j, h * kHalf + k);
       }
     };
     auto multiply = [&](auto h_c) {
@@ -171,8 +208,6 @@ struct Tile {
           for (int j = 0; j < TN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fq[h][k][j], fp[h][k][i], acc[i][j], 0, 0, 0);
     };
-    using H0 = std::integral_constant<int, 0>;
-    using H1 = std::integral_constant<int, 1>;
     // Every wave's loads of a stage have landed and its operand reads are done; `behind` loads after them
     // may still be in flight (loads complete in order).
     auto sync_stage = [&](auto behind) {
@@ -188,7 +223,7 @@ struct Tile {
     // The order of a half stage: LDS reads and loads evenly behind the products. (Loads in a row fill the
     // queues of the memory path, and a wave that waits for room there issues no products either.)
     auto spread = [&](auto loads) {
-      constexpr int products = kHalf * TM * TN, reads = kHalf * (TM + TN), vm = decltype(loads)::value;
+      constexpr int products = kHalf * TM * TN, reads = (KROWS ? 2 : 1) * kHalf * (TM + TN), vm = decltype(loads)::value;
       each(
           [&](auto x_c) {
             constexpr int x = decltype(x_c)::value;
@@ -459,7 +494,7 @@ __device__ __forceinline__ _Float16 remainder16(float x) {
   return static_cast<_Float16>(x - static_cast<float>(static_cast<_Float16>(x)));
 }
 
-// One 64x64 block of X: Xr, Xc and the remainders from G, zeros outside.
+// One 64x64 block of X: Xc and the remainders from G, zeros outside.
 template <typename T>
 __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
   __shared__ double red[4];
@@ -481,17 +516,12 @@ __global__ __launch_bounds__(256) void ns_init_kernel(NsArgs a) {
     else sh[r][c] = v;
   }
   __syncthreads();
-  _Float16* xr = a.xr + b * a.pp * a.ldq;
   _Float16* xc = a.xc[0] + b * a.qp * a.ldp;
   for (int t = threadIdx.x; t < kRegion / 8; t += 256) {
     const int r = t >> 3, c = (t & 7) * 8;
-    h8 u, v;
+    h8 v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      u[e] = static_cast<_Float16>(sh[r][c + e]);
-      v[e] = static_cast<_Float16>(sh[c + e][r]);
-    }
-    *reinterpret_cast<h8*>(xr + (i0 + r) * a.ldq + j0 + c) = u;
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<_Float16>(sh[c + e][r]);
     *reinterpret_cast<h8*>(xc + (j0 + r) * a.ldp + i0 + c) = v;
   }
   _Float16* rest = a.rest + b * a.x_elems + ((j0 / 64) * (a.pp / 64) + i0 / 64) * kRegion;
@@ -550,16 +580,16 @@ __device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, i
 // gridDim.z parts; each part of a tile leaves as FP32 sums in 64x64 regions, for ns_finish_kernel.
 // Otherwise a workgroup makes a whole tile and finishes it.
 template <int BM, int BN, int WM, int WN, int NST, bool POLY, bool SPLIT>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, float cb, float cc) {
-  using G = Tile<BM, BN, WM, WN, NST>;
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, int turn, float cb, float cc) {
+  using G = Tile<BM, BN, WM, WN, NST, !POLY>;
   constexpr int TM = G::TM, TN = G::TN;
   PF8_NS_BUFFERS(bufs, G, NST);
   const int b = blockIdx.y;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / (BN / WN), wn = wave % (BN / WN);
-  const int64_t ld = POLY ? a.ldp : a.ldq;
-  const _Float16* x = POLY ? a.a16 + b * a.pp * a.ldp : a.xr + b * a.pp * a.ldq;
+  const int64_t ld = a.ldp;
+  const _Float16* x = POLY ? a.a16 + b * a.pp * ld : a.xc[turn] + b * a.qp * ld;
   int ti, tj;
   triangle_tile<BM, BN>(blockIdx.x, ti, tj);
   const int64_t r0 = static_cast<int64_t>(ti) * BM, c0 = static_cast<int64_t>(tj) * BN;
@@ -585,7 +615,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsAr
   }
   typename G::Acc acc;
   G::zero(acc);
-  G::run(x + r0 * ld, ld, x + c0 * ld, ld, k0 * 128, (k1 - k0) * 2, bufs, acc);
+  G::run(x + (POLY ? r0 * ld : r0), ld, x + (POLY ? c0 * ld : c0), ld, k0 * 128, (k1 - k0) * 2, bufs, acc);
   float* out = a.part + ((static_cast<int64_t>(b) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x) * (BM * BN);
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -677,7 +707,7 @@ __device__ __forceinline__ h8 swap_halves(h8 v) {
 // X is read before the product, so that it arrives behind its first stages.
 template <int BM, int BN, int WM, int WN, int NST, bool LAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, int turn) {
-  using G = Tile<BM, BN, WM, WN, NST>;
+  using G = Tile<BM, BN, WM, WN, NST, false>;
   constexpr int TM = G::TM, TN = G::TN;
   PF8_NS_BUFFERS(bufs, G, NST);
   const bool tall = a.m > a.n;
@@ -751,7 +781,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
         if (!LAST) *rest_at(i, j, pair) = lo;
       }
     }
-  // out through LDS, as rows of X^T and as rows of X
+  // out through LDS: as rows of X^T, the last step's as rows of G
   auto each_piece = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -773,21 +803,17 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
       if (!LAST) *reinterpret_cast<h8*>(next + (j0 + row) * a.ldp + i0 + col) = w;
       else if (j0 + row < a.m) store_row(out + (j0 + row) * a.ldo + i0 + col, w, a.n - (i0 + col));
     }
-    if (!LAST) __syncthreads();
-  }
-  if (!LAST || !tall) {
+  } else {
     each_piece([&](int m, int n, h4 w) {
       const int nt = n + (lane & 3);
       put_col<BM>(staged<G::kStage, BN, BM, 0>(bufs, nt), m, nt, w);
     });
     __syncthreads();
-    _Float16* xr = a.xr + b * a.pp * a.ldq;
 #pragma unroll 4
     for (int u = 0; u < kPieces; ++u) {
       const int c = threadIdx.x + u * G::kThreads, row = c / (BM / 8), chunk = c % (BM / 8), col = chunk * 8;  // row of X
       const h8 w = get_col<BM>(staged<G::kStage, BN, BM, 0>(bufs, row), row, chunk);
-      if (!LAST) *reinterpret_cast<h8*>(xr + (i0 + row) * a.ldq + j0 + col) = w;
-      else if (i0 + row < a.m) store_row(out + (i0 + row) * a.ldo + j0 + col, w, a.n - (j0 + col));
+      if (i0 + row < a.m) store_row(out + (i0 + row) * a.ldo + j0 + col, w, a.n - (j0 + col));
     }
   }
 }
@@ -1102,22 +1128,22 @@ int64_t align256(int64_t v) { return round_up(v, 256); }
 }  // namespace
 
 template <bool POLY>
-static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, float cb, float cc, hipStream_t stream) {
+static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, int turn, float cb, float cc, hipStream_t stream) {
   const uint32_t tiles = static_cast<uint32_t>(triangle_tiles(shape, a.pp));
   const dim3 grid(tiles, batch, static_cast<uint32_t>(splits));
   if constexpr (!POLY) {
     if (shape == k64x64 && splits > 1) {
-      hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, false, true>), grid, dim3(256), 0, stream, a, cb, cc);
+      hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, false, true>), grid, dim3(256), 0, stream, a, turn, cb, cc);
       hipLaunchKernelGGL((ns_finish_kernel<64, 64, false>), dim3(tiles, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
       return;
     }
   }
   if (shape == k64x64) {
-    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
+    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, turn, cb, cc);
   } else if (shape == k128x128) {
-    hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, cb, cc);
+    hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, turn, cb, cc);
   } else {
-    hipLaunchKernelGGL((ns_sym_kernel<128, 256, 64, 64, 3, POLY, true>), grid, dim3(512), 0, stream, a, cb, cc);
+    hipLaunchKernelGGL((ns_sym_kernel<128, 256, 64, 64, 3, POLY, true>), grid, dim3(512), 0, stream, a, turn, cb, cc);
     hipLaunchKernelGGL((ns_finish_kernel<128, 256, POLY>), dim3(tiles * 8, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
   }
 }
@@ -1131,9 +1157,9 @@ static void launch_update(const NsArgs& a, Shape shape, uint32_t batch, float ca
   else hipLaunchKernelGGL((ns_update_kernel<128, 256, 64, 64, 3, LAST>), grid, dim3(512), 0, stream, a, ca, turn);
 }
 
-// Workspace parts, in order: X's remainders, two Xc, Xr, A, B, their diagonals, A's partial tiles, norms.
+// Workspace parts, in order: X's remainders, two Xc, A, B, their diagonals, A's partial tiles, norms.
 static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base) {
-  const int64_t x = p.pp * p.qp, ldp = p.pp + kPad, ldq = p.qp + kPad;
+  const int64_t x = p.pp * p.qp, ldp = p.pp + kPad;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     uint8_t* r = base + at;
@@ -1143,7 +1169,6 @@ static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base)
   uint8_t* rest = take(batch * x * 2);
   uint8_t* xc0 = take(batch * p.qp * ldp * 2);
   uint8_t* xc1 = take(batch * p.qp * ldp * 2);
-  uint8_t* xr = take(batch * p.pp * ldq * 2);
   uint8_t* a16 = take(batch * p.pp * ldp * 2);
   uint8_t* b16 = take(batch * p.pp * ldp * 2);
   uint8_t* da = take(batch * p.pp * 4);
@@ -1152,10 +1177,9 @@ static int64_t ns_layout(int64_t batch, const Plan& p, NsArgs* a, uint8_t* base)
   uint8_t* part = take(batch * std::max(gram, poly) * 4);
   uint8_t* norm = take(batch * kNormBlocks * 8);
   if (a) {
-    a->pp = p.pp, a->qp = p.qp, a->ldp = ldp, a->ldq = ldq, a->x_elems = x;
+    a->pp = p.pp, a->qp = p.qp, a->ldp = ldp, a->x_elems = x;
     a->rest = reinterpret_cast<_Float16*>(rest);
     a->xc[0] = reinterpret_cast<_Float16*>(xc0), a->xc[1] = reinterpret_cast<_Float16*>(xc1);
-    a->xr = reinterpret_cast<_Float16*>(xr);
     a->a16 = reinterpret_cast<_Float16*>(a16), a->b16 = reinterpret_cast<_Float16*>(b16);
     a->da = reinterpret_cast<float*>(da), a->db = reinterpret_cast<float*>(db);
     a->part = reinterpret_cast<float*>(part), a->norm_part = reinterpret_cast<double*>(norm);
@@ -1190,8 +1214,8 @@ hipError_t launch_newton_schulz(NsArgs a, int64_t batch, int steps, const float*
   if (hipError_t e = hipGetLastError()) return e;
   for (int s = 0; s < steps; ++s) {
     const float ca = coef[3 * s], cb = coef[3 * s + 1], cc = coef[3 * s + 2];
-    launch_sym<false>(a, p.gram, p.gram_splits, nb, cb, cc, stream);
-    launch_sym<true>(a, p.poly, p.poly_splits, nb, cb, cc, stream);
+    launch_sym<false>(a, p.gram, p.gram_splits, nb, s & 1, cb, cc, stream);
+    launch_sym<true>(a, p.poly, p.poly_splits, nb, s & 1, cb, cc, stream);
     if (s + 1 < steps) launch_update<false>(a, p.update, nb, ca, s & 1, stream);
     else launch_update<true>(a, p.update, nb, ca, s & 1, stream);
     if (hipError_t e = hipGetLastError()) return e;

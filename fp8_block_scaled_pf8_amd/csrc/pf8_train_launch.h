@@ -69,9 +69,9 @@ struct NsArgs {
   uint16_t* out;
   int64_t ldo, stride_o;
   int64_t pp, qp;   // padded min(m, n) and max(m, n)
-  int64_t ldp, ldq;  // pitches of FP16 rows of pp and of qp values
+  int64_t ldp;       // pitch of FP16 rows of pp values
   int64_t x_elems;   // pp * qp
-  _Float16 *rest, *xc[2], *xr, *a16, *b16;
+  _Float16 *rest, *xc[2], *a16, *b16;
   float *da, *db, *part;
   double* norm_part;
 };
