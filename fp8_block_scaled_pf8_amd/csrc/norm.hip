@@ -201,6 +201,11 @@ struct Cols {
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] += offset;
+    // (a zero times another thread's infinity would be a NaN in the row's sums)
+    if (TAIL == kOdd && first[i]) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = k < first[i] ? 0.0f : f[k];
+    }
   }
 };
 
@@ -268,6 +273,7 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
     }
     at.mask(hv);
     at.mask(yv);
+    if (full_gate) at.mask(gv);
 
     float r[NV][8];
 #pragma unroll
@@ -390,6 +396,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
       load_row(row, cur);
     }
     at.mask(cur.y);
+    if (full_gate) at.mask(cur.g);
     float rho_y = 1.0f;
     if (post) {
       float s[1] = {0.0f};

@@ -187,6 +187,21 @@ def test_special_values_stay_in_their_rows():
     assert torch.isnan(g.dw_pre).any()
 
 
+@pytest.mark.parametrize("what", ["w_pre", "w_post", "gate", "full gate"])
+@pytest.mark.parametrize("cols", [5, 511, 777, 2047, 2041, 4099, 9001])
+def test_infinite_weights_near_the_odd_end_of_a_row(cols, what):
+    """The last threads of a row read columns that are not theirs: what stands there counts once."""
+    k = _case(3, cols, gate="full" if what == "full gate" else "vector", seed=cols)
+    at = max(cols - 8, 0)
+    if what == "full gate":
+        k["gate"][1, at] = float("inf")
+    else:
+        k[what][at] = float("-inf")
+    _check_forward(k, {}, pf8.block_norm(**k))
+    dr, dx = _rand((3, cols), 41), _rand((3, cols), 42)
+    _check_backward(k, {}, dr, dx, pf8.block_norm_backward(dr, dx, **k))
+
+
 def test_gradient_against_differences_of_the_kernel():
     """dh and dy against differences of the kernel's own forward, in the direction of each gradient."""
     rows, cols = 4, 256
