@@ -56,11 +56,11 @@ def _rows(t: Tensor, name: str, shape, device) -> Tuple[int, int]:
 def _vector(t: Tensor, name: str, cols: int, dtype, device) -> int:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (weights and a [cols] gate share one type), got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != cols:
+    if t.shape != (cols,):
         raise ValueError(f"{name} must have the shape ({cols},), got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.stride(0) != 1 and cols != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -136,21 +136,15 @@ def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-class _on:
-    """Make a tensor's device the current one for a call, where it is not."""
-
-    __slots__ = ("ctx",)
-
-    def __init__(self, device: torch.device):
-        self.ctx = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _call(fn, device: torch.device, *args) -> None:
+    """A library call that enqueues on the current stream of a device, made the current one where it is not."""
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(device))
+    if status != L.PF8_OK:
+        L.check(status, fn.__name__)
 
 
 def _forward(h, y, w_pre, w_post, gate, residual_scale, branch_scale, eps, unit_offset, r_out, x_out, codes):
@@ -181,9 +175,7 @@ def _forward(h, y, w_pre, w_post, gate, residual_scale, branch_scale, eps, unit_
         if x_out is not None:
             _may_write(x_out, "x_out", [(h, True), (y, True), *rest])
     if rows:
-        with _on(dev):
-            L.check(L.pf8_block_norm(rows, cols, *args, pr, ldr, px, ldx, pq, ldq, ps, lds,
-                                     _stream(dev)), "pf8_block_norm")
+        _call(L.pf8_block_norm, dev, rows, cols, *args, pr, ldr, px, ldx, pq, ldq, ps, lds)
     return (h if r is None else r), x, q, s
 
 
@@ -248,17 +240,18 @@ def block_norm_backward(dr: Optional[Tensor], dx: Optional[Tensor], h: Tensor, y
             if accumulate:
                 raise ValueError(f"accumulate needs {name}")
             out = torch.empty(cols, dtype=torch.float32, device=dev)
+            return out, out.data_ptr()
         return out, _vector(out, name, cols, torch.float32, dev)
 
     dw_pre, p_pre = column(dw_pre_out, "dw_pre_out", dx is not None)
     dw_post, p_post = column(dw_post_out, "dw_post_out", w_post is not None)
     dgate, p_gate = column(dgate_out, "dgate_out", gate is not None and not full)
+    sums = [t for t in (dw_pre, dw_post, dgate) if t is not None]
     ld_dg = 0
     if full:
         dgate, p_gate, ld_dg = _output(None, "", h)
     dh, p_dh, _ = _output(None, "", h)
     dy, p_dy, _ = (None, 0, 0) if y is None else _output(None, "", h)
-    sums = [t for t in (dw_pre, dw_post, None if full else dgate) if t is not None]
     if accumulate or dw_pre_out is not None or dw_post_out is not None or dgate_out is not None:
         operands = [t for t in (dr, dx, h, y, w_pre, w_post, gate) if t is not None and t.numel()]
         for i, t in enumerate(sums):
@@ -276,10 +269,8 @@ def block_norm_backward(dr: Optional[Tensor], dx: Optional[Tensor], h: Tensor, y
     if sums:
         nws = L.pf8_block_norm_bwd_workspace(rows, cols)
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
-    with _on(dev):
-        L.check(L.pf8_block_norm_bwd(rows, cols, pdr, ldr, pdx, ldx, *args, p_dh, cols, p_dy, cols,
-                                     p_gate, ld_dg, p_pre, p_post, int(accumulate), 0 if ws is None else ws.data_ptr(), nws,
-                                     _stream(dev)), "pf8_block_norm_bwd")
+    _call(L.pf8_block_norm_bwd, dev, rows, cols, pdr, ldr, pdx, ldx, *args, p_dh, cols, p_dy, cols,
+          p_gate, ld_dg, p_pre, p_post, int(accumulate), 0 if ws is None else ws.data_ptr(), nws)
     return BlockNormGrads(dh, dy, dgate, dw_pre, dw_post)
 
 

@@ -12,7 +12,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib as L
-from .norm import _on, _stream
+from .norm import _call
 
 # Steep at zero (slope 3.4445), so that small singular values grow fast; after five steps values
 # above 1e-2 of the norm lie between 0.7 and 1.2.
@@ -65,8 +65,6 @@ def newton_schulz(g: torch.Tensor, steps: int = 5, coefficients: Sequence = QUIN
     coef = (ctypes.c_float * (3 * steps))(*(v for c in triples for v in c))
     size = L.pf8_newton_schulz_workspace(batch, m, n)
     ws = torch.empty(size, dtype=torch.uint8, device=g.device)
-    with _on(g.device):
-        L.check(L.pf8_newton_schulz(batch, m, n, g0, ldg, sg, L.PF8_F32 if g.dtype == torch.float32 else L.PF8_BF16,
-                                    steps, coef, eps, o0, ldo, so, ws.data_ptr(), size,
-                                    _stream(g.device)), "pf8_newton_schulz")
+    _call(L.pf8_newton_schulz, g.device, batch, m, n, g0, ldg, sg, L.PF8_F32 if g.dtype == torch.float32 else L.PF8_BF16,
+          steps, coef, eps, o0, ldo, so, ws.data_ptr(), size)
     return out
