@@ -135,4 +135,5 @@ def test_newton_schulz_workspace():
     size = L.pf8_newton_schulz_workspace
     assert size(0, 5, 5) == size(1, 0, 5) == size(1, 5, -1) == size(1, 32769, 32769) == size(1, 5, 1048577) == 0
     assert size(65536, 5, 5) == 0 and size(1, 1, 1) > 0
-    assert size(1, 2048, 512) == size(1, 512, 2048) >= 2048 * 512 * 10
+    # an element is kept as a transposed FP16 operand in two buffers and an FP16 remainder: 6 bytes
+    assert size(1, 2048, 512) == size(1, 512, 2048) >= 2048 * 512 * 6
