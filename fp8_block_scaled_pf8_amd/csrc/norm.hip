@@ -119,8 +119,15 @@ __device__ __forceinline__ void clear(Slot<WAVES, N> (&slots)[2]) {
 
 // 1 / sqrt(mean + eps) from a row's sum of (v * sq)^2. sq is a power of two (exact) near
 // 1/sqrt(cols), so that the sum overflows only where the mean does: v up to 2^63 gets its norm.
+// The instruction's result is off by up to a step; one Newton step v + v (1 - a v v) / 2, with a v in two
+// parts, leaves half a step (a square root and a division leave up to one between them, and take longer).
 __device__ __forceinline__ float inv_rms(float sum_sq, const NormArgs& p) {
-  return 1.0f / __builtin_sqrtf(__builtin_fmaf(sum_sq, p.inv_sum, p.eps));
+  const float a = __builtin_fmaf(sum_sq, p.inv_sum, p.eps);
+  if (!(a >= 0x1p-100f && a <= 0x1p100f)) return 1.0f / __builtin_sqrtf(a);  // zeros, subnormals, infinities, NaN too
+  const float v = __builtin_amdgcn_rsqf(a);
+  const float high = a * v, low = __builtin_fmaf(a, v, -high);
+  const float e = __builtin_fmaf(-low, v, __builtin_fmaf(-high, v, 1.0f));
+  return __builtin_fmaf(v, 0.5f * e, v);
 }
 __device__ __forceinline__ float add_sq(float v, float sq, float s) {
   const float t = v * sq;
