@@ -22,11 +22,12 @@
 //    1 - a, and there the rounding of X would enter 2.4-fold. In a matrix of low rank the diagonal
 //    is small, and B' times the rounding alone, without the diagonal's part, would be noise outside
 //    of the matrix's column space, which grows by a in every step.
-//  * A matrix of at most 64 x 512 or 128 x 256 stays in one workgroup, and its X enters the update as a sum of
-//    two FP16 values (22 bits), diagonal or not: few entries average out little of the rounding noise.
+//  * A matrix of at most 64 x 512 or 128 x 256 stays in one workgroup (X in FP32), and its X enters the
+//    update as a sum of two FP16 values, diagonal or not: few entries average out little of the
+//    rounding noise.
 // Against float64, besides the BF16 rounding of the result (1.7e-3 of its 2-norm), the result is off
-// by up to 1.3e-3 of its 2-norm (2.8e-3 where a few entries carry the norm of a larger matrix); BF16
-// operands would give 1.4e-2.
+// by up to 1.3e-3 of its 2-norm (2.8e-3 where a few entries carry the norm); BF16 operands would give
+// 1.4e-2.
 //
 // Layout. X lives in the workspace, padded to multiples of 128 with zeros that stay zero, so the
 // products have no edges: Xc [q][p] (two buffers in turn; the update's operand, and A's by transposing
@@ -591,7 +592,8 @@ __device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, i
 
 // The lower tiles of a symmetric product, K = q of X (POLY = false) or p of A' (true). SPLIT: K is cut into
 // gridDim.z parts; each part of a tile leaves as FP32 sums in 64x64 regions, for ns_finish_kernel.
-// Otherwise a workgroup makes a whole tile and finishes it.
+// Otherwise a workgroup makes a whole tile and finishes it. Bound as the update is; 12288 values along K for
+// the triangle of 2048 x 2048: 57.5 us (1.0 PFLOP/s on the 128x256 tiles) and 7.6 us for joining three parts.
 template <int BM, int BN, int WM, int WN, int NST, bool POLY, bool SPLIT>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, int turn, float cb, float cc) {
   using G = Tile<BM, BN, WM, WN, NST, !POLY>;
@@ -720,7 +722,9 @@ __device__ __forceinline__ h8 swap_halves(h8 v) {
   return __builtin_bit_cast(h8, w);
 }
 
-// X is read before the product, so that it arrives behind its first stages.
+// X is read before the product, so that it arrives behind its first stages. Bound by the matrix cores and the
+// LDS reads that feed them; among the other kernels 12288 x 2048 takes 125 us (825 TFLOP/s), the last step,
+// which writes BF16 only, 121 us.
 template <int BM, int BN, int WM, int WN, int NST, bool LAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, int turn) {
   using G = Tile<BM, BN, WM, WN, NST, false>;
@@ -837,7 +841,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
 // ------------------------------------------------------------------------------ small matrices
 // One matrix of at most P x (NS P) per workgroup, all steps in one launch: the waves hold a WM x 32 part of every
 // P x P slab of X^T in registers (FP32); the products' operands go through LDS as FP16, X in the update as value
-// and remainder. 16 matrices of 128 x 128, five steps: 40 us with 16 waves of 32 x 32, 48 with 8 of 64 x 32.
+// and remainder. Bound by the chain of short products, each behind a barrier and 16-wave traffic through LDS:
+// 128 x 128, five steps: 26.8 us with 16 waves of 32 x 32, 28.9 with 8 of 64 x 32, for one matrix as for 16.
 template <int P, int WM, int NS, typename T>
 __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsArgs a, NsCoef coef, int steps) {
   constexpr int TM = WM / 32, TN = 1, kWaves = (P / WM) * (P / 32), PITCH = P + 8;  // 16 rows' 16-byte reads of one column fall into different banks
@@ -1048,10 +1053,10 @@ int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 // How a size is run. Tile shapes are chosen by the time that a model of the kernels gives: a card's 256 CUs
 // take one workgroup each (two of 64x64), a stage of 64 K values costs a workgroup 0.34 us (128x128), 0.5 us
 // (128x256) or 0.3 us (64x64, two on a CU; 0.14 us alone), and a launch with its first loads and its last
-// stores the rest. Measured against it, for the lower triangle of 2048 x 2048 with K = 2048 / 12288:
-// 64x64 22.2 / 124 us, 128x128 18.9 / 73 us, 128x256 with K in two parts 21.5 / 67 us; of 1024 x 1024 with
-// K = 1664: 64x64 7.0 us, 128x128 13.9 us. Update of 2048 x 2048: 128x128 23.5 us, 128x256 29.2 us, 64x64
-// 42.4 us; of 12288 x 2048: 154, 114 and 239 us.
+// stores the rest. Measured against it, each kernel by itself, for the lower triangle of 2048 x 2048 with
+// K = 2048 / 12288: 64x64 21.8 / 122 us, 128x128 18.4 / 73 us, 128x256 with K in three parts 23 / 65 us; of
+// 1024 x 1024 with K = 1664: 64x64 7.1 us, 128x128 13.7 us. Update of 2048 x 2048: 128x128 21.6 us, 128x256
+// 27.5 us, 64x64 42 us; of 12288 x 2048: 122, 90 and 237 us; of 1664 x 1024: 12.5, 17.6 and 9.5 us.
 enum Shape { k64x64, k128x128, k128x256 };
 struct Plan {
   int64_t pp, qp;

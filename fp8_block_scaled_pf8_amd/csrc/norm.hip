@@ -4,8 +4,10 @@
 // Bound: HBM. Forward 8 bytes an element (h, y in; r, x out), backward 12 (h, y, dr, dx in; dh, dy
 // out), one more bf16 each way for a gate per element; a few dozen FP32 operations an element.
 // Each row is read once: its values stay in registers between the row sums, 8 consecutive bf16 per
-// thread and step. A row belongs to 64, 256 or 1024 threads; sums run over a wave by DPP and, with
-// several waves, once through LDS.
+// thread and step. A row belongs to a wave (up to 512 columns forward) or to a workgroup of as many
+// waves as it fills; sums run over a wave by DPP and, with several waves, once through LDS.
+// 8192 x 2048: forward 25.4 us (5.3 TB/s), backward 52.5 us (3.8 TB/s, of which 5 us are the column
+// sums); backward 4096 x 6144 with a gate per element 88 us (4.6 TB/s).
 #include "pf8_device.h"
 #include "pf8_train_launch.h"
 
@@ -138,7 +140,7 @@ __device__ __forceinline__ float add_sq(float v, float sq, float s) {
 // fewer than 8 columns are left, the thread takes the row's last 8 all the same, so that they come by one
 // load, and masks those that belong to the thread before it: they count as zeros, and are not stored.
 // (Loads put together from pieces would be waited for where they are made, and no longer travel during the
-// row before: 8192 x 2047 backward took 143 us, 2048 columns 51 us.) kEven: there is
+// row before: 8192 x 2047 backward took 143 us, now 54; 2048 columns 47, all from the caches.) kEven: there is
 // no such step. kTiny: rows of under 8 columns, loaded value by value, zeros behind.
 enum Tail { kEven, kOdd, kTiny };
 template <int NV, Tail TAIL>
@@ -566,8 +568,9 @@ __global__ __launch_bounds__(kSumCols * kSumSlices) void norm_colsum_kernel(cons
 }  // namespace
 
 // Workgroups for `units` units of work (rows, or four of them): no more than the card's 256 CUs hold at
-// once, and evenly loaded. 8192 x 2048 forward: 28.9 us with 1024 workgroups of 8 rows, 31.8 with 2048, 36.9
-// with one for each row; backward 55.9 us with 745, 61.5 with 512, 69.7 with 1024.
+// once, and evenly loaded. With inputs in the caches, 8192 x 2048 forward: 22.9 us with 1024 workgroups of 8
+// rows, 23.8 with twice as many, 24.4 with one for each row; backward 47.0 us with 512, 51.7 with 745, 57.5
+// with 1024 (each writes a row of partial sums).
 static int64_t even_groups(int64_t units, int64_t per_cu) {
   const int64_t most = 256 * (per_cu < 1 ? 1 : per_cu), each = (units + most - 1) / most;
   return (units + each - 1) / each;
@@ -581,8 +584,8 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
     return hipGetLastError();
   };
   // A row by one wave, by up to four with the next row on its way (88 registers: 20 waves on a CU), or by up to
-  // 16 without (wide rows have enough loads in flight: 4096 x 6144 with a full gate 56.3 us, 59.5 us by half the
-  // waves with the next row on its way).
+  // 16 without (wide rows have enough loads in flight: 4096 x 6144 with a full gate 39.9 us, 40.7 us by half the
+  // waves with the next row on its way; 1003 x 5407 12.3 us, 16.9).
   const int threads = (cols + 511) / 512 * 64;  // 8 values each
   if (cols < 8) return go(norm_fwd_kernel<true, 1, 256, true, kTiny>, even_groups((rows + 3) / 4, 5), 256);
   auto by_width = [&](auto tail) {
@@ -601,7 +604,7 @@ static int norm_bwd_threads(int64_t cols) {
   return static_cast<int>((cols + 512 * steps - 1) / (512 * steps) * 64);
 }
 
-// (12 waves on a CU with 158 registers each, or 8 with 256)
+// Eight waves on a CU: see even_groups. (The kernels' registers would allow more.)
 int64_t norm_bwd_groups(int64_t rows, int64_t cols) {
   return even_groups(rows, 512 / norm_bwd_threads(cols));
 }

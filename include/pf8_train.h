@@ -116,10 +116,10 @@ int64_t pf8_block_norm_bwd_workspace(int64_t rows, int64_t cols);
  * eps: >= 0. A matrix of zeros gives zeros (NaN with eps = 0); one that holds a NaN or an infinity
  *      gives NaN everywhere.
  *
- * Precision: X, the diagonals of X X^T and of the polynomial, and every sum are FP32 or FP64; the matrix
- * products' operands are FP16, scaled by powers of two. Besides the BF16 rounding of the result
- * (1.7e-3 of its 2-norm) the result is off by up to 1.5e-3 of its 2-norm, by up to 3e-3 where a few
- * entries carry the norm of a large matrix. The same call gives the same bits.
+ * Precision: X is kept to 22 bits or more; the diagonals of X X^T and of the polynomial, and every sum,
+ * are FP32 or FP64; the matrix products' operands are FP16, scaled by powers of two. Besides the BF16
+ * rounding of the result (1.7e-3 of its 2-norm) the result is off by up to 1.5e-3 of its 2-norm, by up
+ * to 3e-3 where a few entries carry the norm. The same call gives the same bits.
  *
  * workspace: pf8_newton_schulz_workspace(batch, m, n) bytes, 256-byte aligned.
  */
