@@ -357,7 +357,9 @@ __global__ __launch_bounds__(THREADS) void norm_fwd_kernel(NormFwdArgs a) {
 
 // Backward: workgroup b takes rows b, b + G, ... (the next row on its way as above); every thread sums its
 // own columns' weight and gate gradients over the workgroup's rows in registers and writes one row of
-// partial sums.
+// partial sums. Where registers are short (over 8192 columns, and over 2048 where a row's odd end takes masks)
+// no row is on its way and the two weights' sums lie in LDS, a thread at its own places: 4096 x 16384 in 460 us,
+// 635 with the sums in registers, which spilled; 4096 x 5407 in 148 us, 195 with all of it in registers.
 template <int NV, int THREADS, bool AHEAD, Tail TAIL>
 __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_sums) {
   __shared__ Slot<THREADS / 64, 2> slots[2];
@@ -370,13 +372,35 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
   const float inv_n = 1.0f / static_cast<float>(cols);
   const Weights<NV, TAIL, AHEAD> w_pre(pre ? p.w_pre : nullptr, p.wf32, p.offset, at), w_post(p.w_post, p.wf32, p.offset, at),
       gate(full_gate ? nullptr : p.gate, p.wf32, 0.0f, at);
-  float acc[3][NV][8];
+  constexpr int kParked = AHEAD ? 0 : 2;  // of the sums for w_pre, w_post and the gate
+  __shared__ float4 parked[AHEAD ? 1 : kParked * NV * 2][AHEAD ? 1 : THREADS];
+  float acc[3 - kParked][NV][8];
+  auto get_sum = [&](auto j, int i, float (&f)[8]) {
+    if constexpr (decltype(j)::value < kParked) {
+      const float4 a = parked[(decltype(j)::value * NV + i) * 2][threadIdx.x], b = parked[(decltype(j)::value * NV + i) * 2 + 1][threadIdx.x];
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
 #pragma unroll
-  for (int j = 0; j < 3; ++j)
+      for (int k = 0; k < 8; ++k) f[k] = acc[decltype(j)::value - kParked][i][k];
+    }
+  };
+  auto put_sum = [&](auto j, int i, const float (&f)[8]) {
+    if constexpr (decltype(j)::value < kParked) {
+      parked[(decltype(j)::value * NV + i) * 2][threadIdx.x] = make_float4(f[0], f[1], f[2], f[3]);
+      parked[(decltype(j)::value * NV + i) * 2 + 1][threadIdx.x] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int k = 0; k < 8; ++k) acc[decltype(j)::value - kParked][i][k] = f[k];
+    }
+  };
+  using Pre = std::integral_constant<int, 0>;
+  using Post = std::integral_constant<int, 1>;
+  using Gate = std::integral_constant<int, 2>;
+  {
+    const float none[8] = {};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[j][i][k] = 0.0f;
+    for (int i = 0; i < NV; ++i) put_sum(Pre{}, i, none), put_sum(Post{}, i, none), put_sum(Gate{}, i, none);
+  }
   int turn = 0;
   auto sum = [&](auto& s) {
     row_sum<THREADS / 64>(s, slots[turn]);
@@ -402,6 +426,7 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
       cur = next;
       if (row + gridDim.x < p.rows) load_row(row + gridDim.x, next);
     } else {
+      asm volatile("" ::: "memory");  // weights are loaded where they are used, not kept
       load_row(row, cur);
     }
     at.mask(cur.y);
@@ -433,8 +458,6 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
 
     at.mask(cur.dr);
     float d[NV][8];  // the gradient that reaches r
-#pragma unroll
-    for (int i = 0; i < NV; ++i) unpack8(cur.dr[i], d[i]);
     if (pre) {
       at.mask(cur.h);
       at.mask(cur.dx);
@@ -464,16 +487,22 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
       const float m = s[1] * rho_r * (inv_n / p.sq);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float x[8], w[8];
+        float x[8], w[8], dw[8];
         unpack8(cur.dx[i], x);
         w_pre.get(i, at, w);
+        get_sum(Pre{}, i, dw);
+        unpack8(cur.dr[i], d[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float rn = rr[i][k] * rho_r;
-          acc[0][i][k] = __builtin_fmaf(x[k], rn, acc[0][i][k]);
+          dw[k] = __builtin_fmaf(x[k], rn, dw[k]);
           d[i][k] += rho_r * (x[k] * w[k] - rn * m);
         }
+        put_sum(Pre{}, i, dw);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) unpack8(cur.dr[i], d[i]);
     }
     if (a.dh) {
 #pragma unroll
@@ -488,27 +517,31 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float u[8], g[8], o[8];
+      float u[8], g[8], o[8], dg[8];
       branch_values(i, u, g);
+      get_sum(Gate{}, i, dg);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const float v = p.branch_scale * d[i][k];
         o[k] = v * u[k];
-        acc[2][i][k] += o[k];
+        dg[k] += o[k];
         d[i][k] = v * g[k];
       }
+      put_sum(Gate{}, i, dg);
       if (a.dgate_full) at.store(a.dgate_full + row * a.ld_dgate, i, o);
       if (post) {
-        float y[8], w[8];
+        float y[8], w[8], dw[8];
         unpack8(cur.y[i], y);
         w_post.get(i, at, w);
+        get_sum(Post{}, i, dw);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const float yn = y[k] * rho_y;
-          acc[1][i][k] = __builtin_fmaf(d[i][k], yn, acc[1][i][k]);
+          dw[k] = __builtin_fmaf(d[i][k], yn, dw[k]);
           d[i][k] *= w[k];
           s[0] = __builtin_fmaf(d[i][k], yn, s[0]);
         }
+        put_sum(Post{}, i, dw);
       }
     }
     float m2 = 0.0f;
@@ -529,16 +562,19 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
   }
 
   float* out = a.partial + static_cast<int64_t>(blockIdx.x) * n_sums * cols;
+  auto write_sum = [&](auto j) {
+    if (!a.sums[decltype(j)::value]) return;
 #pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    if (!a.sums[j]) continue;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      float f[8];
+      get_sum(j, i, f);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k >= at.first[i] && at.c[i] + k < cols) out[at.c[i] + k] = acc[j][i][k];
+        if (k >= at.first[i] && at.c[i] + k < cols) out[at.c[i] + k] = f[k];
+    }
     out += cols;
-  }
+  };
+  write_sum(Pre{}), write_sum(Post{}), write_sum(Gate{});
 }
 
 // Column sums of the workgroups' partial rows [groups][n_sums * cols], in a fixed order: 8 threads
@@ -598,15 +634,15 @@ hipError_t launch_norm_fwd(const NormFwdArgs& a, hipStream_t stream) {
   return cols % 8 ? by_width(std::integral_constant<Tail, kOdd>{}) : by_width(std::integral_constant<Tail, kEven>{});
 }
 
-// Threads of a row in the backward pass: whole waves, one, two or four steps of 8 values each.
+// Threads of a row in the backward pass: whole waves, one or two steps of 8 values each.
 static int norm_bwd_threads(int64_t cols) {
-  const int64_t steps = cols <= 2048 ? 1 : cols <= 8192 ? 2 : 4;
+  const int64_t steps = cols <= 2048 ? 1 : 2;
   return static_cast<int>((cols + 512 * steps - 1) / (512 * steps) * 64);
 }
 
 // Eight waves on a CU: see even_groups. (The kernels' registers would allow more.)
 int64_t norm_bwd_groups(int64_t rows, int64_t cols) {
-  return even_groups(rows, 512 / norm_bwd_threads(cols));
+  return even_groups(rows, 512 / norm_bwd_threads(cols));  // (at least one)
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
@@ -624,8 +660,8 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
   auto by_width = [&](auto tail) {
     constexpr Tail T = decltype(tail)::value;
     if (cols <= 2048) return go(norm_bwd_kernel<1, 256, true, T>, threads);
-    if (cols <= 8192) return go(norm_bwd_kernel<2, 512, true, T>, threads);
-    return go(norm_bwd_kernel<4, 512, false, T>, threads);
+    if (cols <= 8192) return go(norm_bwd_kernel<2, 512, T == kEven, T>, threads);
+    return go(norm_bwd_kernel<2, 1024, false, T>, threads);
   };
   const hipError_t e = cols < 8   ? go(norm_bwd_kernel<1, 256, true, kTiny>, threads)
                        : cols % 8 ? by_width(std::integral_constant<Tail, kOdd>{})
