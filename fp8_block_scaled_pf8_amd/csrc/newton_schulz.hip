@@ -342,14 +342,14 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t id, uint32_t all) {
 template <int BM, int BN>
 __device__ __forceinline__ void triangle_tile(int t, int& ti, int& tj) {
   constexpr int kTwo = BM == BN ? 1 : 2;  // pairs of tiles make a square
-  static_assert(BM == BN || BM == 2 * BN || BN == 2 * BM, "square or two to one");
+  static_assert(BM == BN || BN == 2 * BM, "square or twice as wide");
   const int u = t / kTwo;
   int i = static_cast<int>((__builtin_sqrtf(8.0f * static_cast<float>(u) + 1.0f) - 1.0f) * 0.5f);
   while (i * (i + 1) / 2 > u) --i;
   while ((i + 1) * (i + 2) / 2 <= u) ++i;
   const int j = u - i * (i + 1) / 2, odd = t % kTwo;
   ti = BN > BM ? 2 * i + odd : i;
-  tj = BM > BN ? 2 * j + odd : j;
+  tj = j;
 }
 
 // A finished tile passes through LDS to leave in whole rows, as it is and transposed. Lanes hold four
@@ -723,7 +723,7 @@ __device__ __forceinline__ h8 swap_halves(h8 v) {
 }
 
 // X is read before the product, so that it arrives behind its first stages. Bound by the matrix cores and the
-// LDS reads that feed them; among the other kernels 12288 x 2048 takes 125 us (825 TFLOP/s), the last step,
+// LDS reads that feed them; among the other kernels 12288 x 2048 takes 125 us (820 TFLOP/s), the last step,
 // which writes BF16 only, 121 us.
 template <int BM, int BN, int WM, int WN, int NST, bool LAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, int turn) {

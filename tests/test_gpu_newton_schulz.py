@@ -103,6 +103,31 @@ def test_weight_sizes(m, n):
     assert ((got - ref).norm() / ref.norm()).item() <= 2.3e-3
 
 
+@pytest.mark.parametrize("batch,m,n", [(1, 5000, 5000), (1, 5700, 5760), (1, 9000, 1300), (16, 1500, 700), (6, 256, 4352),
+                                       (200, 250, 300), (3, 1100, 1150)])
+def test_tile_shapes(batch, m, n):
+    """Sizes that take the larger tiles in each of the products, K in parts and whole, two steps against
+    float64 on the GPU. FP16 rounds an operand by 2^-11 / sqrt(3) = 2.8e-4 in the root mean square, and no
+    product weighs it with more than |b s^2 + c s^4| <= 2.9 (s up to 1.1): 8.2e-4 for each of six operand
+    roundings at most, 4.9e-3 together, and 1.7e-3 for BF16. The roundings spread like the values: three
+    times as much in any single block of 64 x 64."""
+    g = _matrix("gauss", m, n, seed=batch + m, batch=batch)
+    x = g.double()
+    x = x / (torch.linalg.vector_norm(x, dim=(1, 2), keepdim=True) + 1e-7)
+    x = x.transpose(1, 2).contiguous() if m > n else x
+    for _ in range(2):
+        a = torch.bmm(x, x.transpose(1, 2).contiguous())
+        x = COEF[0] * x + torch.bmm(COEF[1] * a + COEF[2] * torch.bmm(a, a), x)
+    ref = x.transpose(1, 2) if m > n else x
+    off = pf8.newton_schulz(g, steps=2).double() - ref
+    tol = (4.9e-3 ** 2 + 1.75e-3 ** 2) ** 0.5
+    assert (torch.linalg.vector_norm(off, dim=(1, 2)) <= tol * torch.linalg.vector_norm(ref, dim=(1, 2))).all()
+    pad = (0, -n % 64, 0, -m % 64)
+    blocks = [torch.nn.functional.pad(t, pad).unflatten(2, (-1, 64)).unflatten(1, (-1, 64)).square().sum((2, 4)).sqrt()
+              for t in (off, ref)]
+    assert (blocks[0] <= 3 * tol * blocks[1]).all()
+
+
 @pytest.mark.parametrize("batch,m,n", [(1, 70, 90), (3, 64, 64), (16, 128, 128), (5, 130, 200), (4, 300, 129), (40, 20, 36),
                                        (70, 256, 128)])
 def test_stacks(batch, m, n):
