@@ -164,6 +164,40 @@ def test_outputs_in_the_inputs_place():
     assert torch.equal(y, want[0]) and torch.equal(h, want[1])
 
 
+@pytest.mark.parametrize("cols", [3, 509, 1003, 2047, 4099, 9001])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (False, False)])
+def test_outputs_in_the_inputs_place_with_odd_rows(cols, post, pre):
+    """The last threads of a row read columns that others have already overwritten."""
+    k = _case(1500, cols, post, pre, gate="full", seed=cols)
+    want = pf8.block_norm(**k)
+    for swap in (False, True):
+        h, y = k["h"].clone(), k["y"].clone()
+        r, x = (y, h) if swap else (h, y)
+        pf8.block_norm(**{**k, "h": h, "y": y}, r_out=r, x_out=x if pre else None)
+        assert torch.equal(r, want[0]) and (not pre or torch.equal(x, want[1]))
+
+
+@pytest.mark.parametrize("cols", [5, 512, 777, 2048, 5407, 8192, 9001])
+def test_gradients_in_the_inputs_place(cols):
+    """What the C interface allows: dh and dy in the memory of dr, dx, h or y."""
+    from fp8_block_scaled_pf8_amd import _lib as L
+    rows = 700
+    k = _case(rows, cols, seed=cols)
+    dr, dx = _rand((rows, cols), 31), _rand((rows, cols), 32)
+    want = pf8.block_norm_backward(dr, dx, **k)
+    ws = torch.empty(L.pf8_block_norm_bwd_workspace(rows, cols), dtype=torch.uint8, device=DEV)
+    for i, j in ((0, 3), (1, 2), (2, 3), (3, 1)):
+        t = [v.clone() for v in (dr, dx, k["h"], k["y"])]
+        sums = torch.empty((3, cols), device=DEV)
+        L.check(L.pf8_block_norm_bwd(
+            rows, cols, t[0].data_ptr(), cols, t[1].data_ptr(), cols, t[2].data_ptr(), cols, t[3].data_ptr(), cols,
+            k["w_post"].data_ptr(), k["gate"].data_ptr(), 0, k["w_pre"].data_ptr(), L.PF8_BF16, 1.0, 1.0, 0.0, 1e-6,
+            t[i].data_ptr(), cols, t[j].data_ptr(), cols, sums[2].data_ptr(), 0, sums[0].data_ptr(), sums[1].data_ptr(), 0,
+            ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream))
+        assert torch.equal(t[i], want.dh) and torch.equal(t[j], want.dy)
+        assert all(torch.equal(a, b) for a, b in zip(sums, (want.dw_pre, want.dw_post, want.dgate)))
+
+
 def test_special_values_stay_in_their_rows():
     k = _case(8, 640, gate="none")
     k["h"][1, 5] = float("nan")
