@@ -17,17 +17,18 @@
 //    (A A)_ij = sum A'_ik A'_kj + (d_i + d_j) A'_ij off the diagonal.
 //  * FP16 values are scaled by powers of two (X 2^12, A 2^10, B 2^9), so that entries down to 2^-26 of
 //    the norm keep all an operand's bits and singular values up to 8 stay in range.
-//  * The diagonal's part of B X takes a row of X whole where the diagonal's element is large, and
-//    the row's FP16 rounding elsewhere (kOwnRow). A matrix of full rank ends with diagonals near
-//    1 - a, and there the rounding of X would enter 2.4-fold. In a matrix of low rank the diagonal
-//    is small, and B' times the rounding alone, without the diagonal's part, would be noise outside
-//    of the matrix's column space, which grows by a in every step.
+//  * In every step but the last, the whole of B multiplies one and the same FP16 rounding of X, its
+//    diagonal too: B times anything lies in X's column space, so the rounding's part outside of it is
+//    gone. With X whole under the diagonal, of some rows or of all, that part would stay, and grow by a
+//    in every step behind (a rank-one G came out 4 % off where one row carries most of it). The last
+//    step's diagonal takes X whole: nothing grows any more, and of a matrix of full rank, whose diagonals
+//    end near 1 - a, the rounding would enter 2.4-fold.
 //  * A matrix of at most 64 x 512 or 128 x 256 stays in one workgroup (X in FP32), and its X enters the
 //    update as a sum of two FP16 values, diagonal or not: few entries average out little of the
 //    rounding noise.
-// Against float64, besides the BF16 rounding of the result (1.7e-3 of its 2-norm), the result is off
-// by up to 1.3e-3 of its 2-norm (2.8e-3 where a few entries carry the norm); BF16 operands would give
-// 1.4e-2.
+// Against float64, besides the BF16 rounding of the result (1.7e-3 of its 2-norm), five steps are off by
+// 1.1e-3 of its 2-norm for Gaussian gradients and up to 2e-3 for others (5e-3 where few entries carry the norm,
+// 1.5e-2 where all entries are of a few magnitudes and round alike); BF16 operands would give eight times that.
 //
 // Layout. X lives in the workspace, padded to multiples of 128 with zeros that stay zero, so the
 // products have no edges: Xc [q][p] (two buffers in turn; the update's operand, and A's by transposing
@@ -62,9 +63,6 @@ struct NsCoef {
 constexpr float kSX = 4096.0f, kSA = 1024.0f, kSB = 512.0f;  // powers of two that FP16 operands carry
 constexpr int kRegion = 64 * 64;
 constexpr int64_t kPad = 64;  // values that FP16 rows are longer than padded: see "Layout"
-// a diagonal element of B over this part of |a - 1| (which a matrix of full rank with singular values
-// near one has) multiplies X whole
-constexpr float kOwnRow = 2.0f / 3.0f;
 
 // In a 64x64 region of a product, block (bi, bj) of 32x32 and register 4 g + e of lane l hold the
 // element (32 bi + l % 32, 32 bj + 8 g + 4 (l / 32) + e). FP32 sums lie there four registers a lane, the
@@ -766,7 +764,6 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
   G::zero(acc);
   G::run(xc + j0 * a.ldp, a.ldp, B + i0 * a.ldp, a.ldp, 0, static_cast<int>(a.pp / G::BK), bufs, acc);
 
-  const float own_from = kOwnRow * __builtin_fabsf(ca - 1.0f);
   const float* d = a.db + b * a.pp + i0;
   h4 v[TM][TN][4];
 #pragma unroll
@@ -774,13 +771,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
 #pragma unroll
     for (int pair = 0; pair < 2; ++pair) {
       f4 dn[2];
-      bool own[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2; ++h)
         dn[h] = *reinterpret_cast<const f4*>(d + wn * WN + 32 * j + 8 * (2 * pair + h) + 4 * (lane >> 5));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) own[4 * h + e] = __builtin_fabsf(dn[h][e]) > own_from;
-      }
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         // .. and the halves exchange, so that it has the four columns of each g that its sums belong to
@@ -790,7 +783,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
         for (int k = 0; k < 8; ++k) {
           const int h = k >> 2, e = k & 3, g = 2 * pair + h;
           const float yh = static_cast<float>(hi[k]), x = yh + static_cast<float>(lo[k]);
-          const float y = __builtin_fmaf(ca, x, __builtin_fmaf(dn[h][e], own[k] ? x : yh, acc[i][j][4 * g + e] * (1.0f / kSB)));
+          const float y = __builtin_fmaf(ca, x, __builtin_fmaf(dn[h][e], LAST ? x : yh, acc[i][j][4 * g + e] * (1.0f / kSB)));
           if (LAST) {
             v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y * (1.0f / kSX)));
           } else {

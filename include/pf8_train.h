@@ -118,8 +118,12 @@ int64_t pf8_block_norm_bwd_workspace(int64_t rows, int64_t cols);
  *
  * Precision: X is kept to 22 bits or more; the diagonals of X X^T and of the polynomial, and every sum,
  * are FP32 or FP64; the matrix products' operands are FP16, scaled by powers of two. Besides the BF16
- * rounding of the result (1.7e-3 of its 2-norm) the result is off by up to 1.5e-3 of its 2-norm, by up
- * to 3e-3 where a few entries carry the norm. The same call gives the same bits.
+ * rounding of the result (1.7e-3 of its 2-norm), five steps of the usual kind are off by up to 2e-3 of the
+ * result's 2-norm (of any rank, also where few rows carry the gradient); by up to 5e-3 where under 64
+ * entries do, and by up to 1.5e-2 where all entries have one of a few magnitudes (a constant matrix), whose
+ * roundings are alike. What rounding puts outside the space of a gradient of low rank grows by a in every
+ * step, as it does in FP32: rank one is off by up to 4e-3 after eight steps and 4e-2 after ten. The same call
+ * gives the same bits.
  *
  * workspace: pf8_newton_schulz_workspace(batch, m, n) bytes, 256-byte aligned.
  */

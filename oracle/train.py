@@ -95,8 +95,8 @@ def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
 
     X is kept; its rounding enters the products (with `pairs`, in B X as value plus remainder). The
     diagonals of A = X X^T and of B = b A + c A A are kept, their other elements rounded. The
-    diagonal of B multiplies X where its element is over 2/3 |a - 1| (with `pairs`, everywhere),
-    X's rounding elsewhere.
+    diagonal of B multiplies X's rounding as the rest of B does, and X itself in the last step (with
+    `pairs`, in every step).
     """
     f16 = lambda a, s: (a * s).astype(np.float16).astype(np.float64) / s  # noqa: E731
     x = np.asarray(g, dtype=np.float64)
@@ -104,7 +104,7 @@ def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
     tall = x.shape[0] > x.shape[1]
     x = x.T if tall else x
     off = 1.0 - np.eye(x.shape[0])
-    for a, b, c in coefficients:
+    for step, (a, b, c) in enumerate(coefficients):
         xh = f16(x, 2.0 ** 12)
         xp = xh + (f16(x - xh, 2.0 ** 12) if pairs else 0.0)
         gram = xh @ xh.T
@@ -113,6 +113,6 @@ def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
         square = gram @ gram
         poly = b * gram + c * (square + (d[:, None] + d[None, :]) * gram)
         diag = (b * d + c * (np.diag(square) + d * d))[:, None]
-        own = x if pairs else np.where(np.abs(diag) > 2.0 / 3.0 * abs(a - 1.0), x, xh)
+        own = x if pairs or step + 1 == len(coefficients) else xh
         x = a * x + diag * own + f16(poly * off, 2.0 ** 9) @ xp
     return x.T if tall else x
