@@ -15,8 +15,9 @@
 //  * A and B = b A + c A A are split into their diagonals, kept in FP32, and the rest in FP16:
 //    near the end A is close to a multiple of the identity and the diagonal carries nearly all.
 //    (A A)_ij = sum A'_ik A'_kj + (d_i + d_j) A'_ij off the diagonal.
-//  * FP16 values are scaled by powers of two (X 2^12, A 2^10, B 2^9), so that entries down to 2^-26 of
-//    the norm keep all an operand's bits and singular values up to 8 stay in range.
+//  * FP16 values are scaled by powers of two (X 2^12, A 2^10, B by its step's coefficients: poly_scale), so
+//    that entries down to 2^-26 of the norm keep all an operand's bits and singular values up to 8 stay in
+//    range.
 //  * In every step but the last, the whole of B multiplies one and the same FP16 rounding of X, its
 //    diagonal too: B times anything lies in X's column space, so the rounding's part outside of it is
 //    gone. With X whole under the diagonal, of some rows or of all, that part would stay, and grow by a
@@ -57,10 +58,10 @@ typedef float f16v __attribute__((ext_vector_type(16)));
 
 // The steps' coefficients, by value: the host's array is not read after the call.
 struct NsCoef {
-  float v[64][3];
+  float v[64][5];  // a, b, c, poly_scale(b, c) and its reciprocal
 };
 
-constexpr float kSX = 4096.0f, kSA = 1024.0f, kSB = 512.0f;  // powers of two that FP16 operands carry
+constexpr float kSX = 4096.0f, kSA = 1024.0f;  // powers of two that FP16 operands carry
 constexpr int kRegion = 64 * 64;
 constexpr int64_t kPad = 64;  // values that FP16 rows are longer than padded: see "Layout"
 
@@ -568,11 +569,11 @@ __device__ __forceinline__ h4 gram_elements(const NsArgs& a, int b, int64_t m, i
 __device__ __forceinline__ const h4* poly_a16(const NsArgs& a, int b, int64_t m, int64_t n) {
   return reinterpret_cast<const h4*>(a.a16 + (static_cast<int64_t>(b) * a.pp + m) * a.ldp + n);
 }
-__device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, int64_t n, f4 s, h4 av, float cb, float cc) {
+__device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, int64_t n, f4 s, h4 av, float cb, float cc, float sb) {
   const float* d = a.da + b * a.pp;
   const float dm = d[m];
   const f4 dn = *reinterpret_cast<const f4*>(d + n);
-  const float from = (cb + cc * dm) * (kSB / kSA), by = cc * (kSB / kSA), squares = cc * (kSB / (kSA * kSA));
+  const float from = (cb + cc * dm) * (sb / kSA), by = cc * (sb / kSA), squares = cc * (sb / (kSA * kSA));
   h4 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -593,7 +594,7 @@ __device__ __forceinline__ h4 poly_elements(const NsArgs& a, int b, int64_t m, i
 // Otherwise a workgroup makes a whole tile and finishes it. Bound as the update is; 12288 values along K for
 // the triangle of 2048 x 2048: 57.5 us (1.0 PFLOP/s on the 128x256 tiles) and 7.6 us for joining three parts.
 template <int BM, int BN, int WM, int WN, int NST, bool POLY, bool SPLIT>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, int turn, float cb, float cc) {
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsArgs a, int turn, float cb, float cc, float sb) {
   using G = Tile<BM, BN, WM, WN, NST, !POLY>;
   constexpr int TM = G::TM, TN = G::TN;
   PF8_NS_BUFFERS(bufs, G, NST);
@@ -648,7 +649,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsAr
           *reinterpret_cast<f4*>(out + to) = v;
         } else {
           h4 h;
-          if constexpr (POLY) h = poly_elements(a, b, r0 + m, c0 + n, v, av[i][j][g], cb, cc);
+          if constexpr (POLY) h = poly_elements(a, b, r0 + m, c0 + n, v, av[i][j][g], cb, cc, sb);
           else h = gram_elements(a, b, r0 + m, c0 + n, v);
           put_row<BN>(staged<G::kStage, BM, BN, 0>(bufs, m), m, n, h);
           put_col<BM>(staged<G::kStage, BN, BM, NST / 2>(bufs, n + (lane & 3)), m, n + (lane & 3), h);
@@ -662,7 +663,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_sym_kernel(NsAr
 
 // Adds the parts of one 64x64 region in their order, and writes what is stored of it.
 template <int BM, int BN, bool POLY>
-__global__ __launch_bounds__(256) void ns_finish_kernel(NsArgs a, int tiles, int splits, float cb, float cc) {
+__global__ __launch_bounds__(256) void ns_finish_kernel(NsArgs a, int tiles, int splits, float cb, float cc, float sb) {
   constexpr int kPer = (BM / 64) * (BN / 64);
   __shared__ __align__(16) uint8_t rows[64 * 64 * 2], cols[64 * 64 * 2];
   const Buffers bufs = {rows, cols, rows, rows};
@@ -685,7 +686,7 @@ __global__ __launch_bounds__(256) void ns_finish_kernel(NsArgs a, int tiles, int
     const int lane = t & 63, g = (t >> 6) & 3, bj = (t >> 8) & 1, bi = t >> 9;
     const int m = 32 * bi + (lane & 31), n = 32 * bj + 8 * g + 4 * (lane >> 5);
     h4 h;
-    if constexpr (POLY) h = poly_elements(a, b, r0 + m, c0 + n, s[u], *poly_a16(a, b, r0 + m, c0 + n), cb, cc);
+    if constexpr (POLY) h = poly_elements(a, b, r0 + m, c0 + n, s[u], *poly_a16(a, b, r0 + m, c0 + n), cb, cc, sb);
     else h = gram_elements(a, b, r0 + m, c0 + n, s[u]);
     put_row<64>(rows + m * 128, m, n, h);
     put_col<64>(cols + (n + (lane & 3)) * 128, m, n + (lane & 3), h);
@@ -724,7 +725,7 @@ __device__ __forceinline__ h8 swap_halves(h8 v) {
 // LDS reads that feed them; among the other kernels 12288 x 2048 takes 125 us (820 TFLOP/s), the last step,
 // which writes BF16 only, 121 us.
 template <int BM, int BN, int WM, int WN, int NST, bool LAST>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, int turn) {
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, float inv_sb, int turn) {
   using G = Tile<BM, BN, WM, WN, NST, false>;
   constexpr int TM = G::TM, TN = G::TN;
   PF8_NS_BUFFERS(bufs, G, NST);
@@ -783,7 +784,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(N
         for (int k = 0; k < 8; ++k) {
           const int h = k >> 2, e = k & 3, g = 2 * pair + h;
           const float yh = static_cast<float>(hi[k]), x = yh + static_cast<float>(lo[k]);
-          const float y = __builtin_fmaf(ca, x, __builtin_fmaf(dn[h][e], LAST ? x : yh, acc[i][j][4 * g + e] * (1.0f / kSB)));
+          const float y = __builtin_fmaf(ca, x, __builtin_fmaf(dn[h][e], LAST ? x : yh, acc[i][j][4 * g + e] * inv_sb));
           if (LAST) {
             v[i][j][g][e] = __builtin_bit_cast(_Float16, bf16_bits(y * (1.0f / kSX)));
           } else {
@@ -911,7 +912,7 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
     });
   };
   for (int step = 0; step < steps; ++step) {
-    const float ca = coef.v[step][0], cb = coef.v[step][1], cc = coef.v[step][2];
+    const float ca = coef.v[step][0], cb = coef.v[step][1], cc = coef.v[step][2], sb = coef.v[step][3], inv_sb = coef.v[step][4];
     clear();
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -972,7 +973,7 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
     blocks([&](int bi, int bj) {
       const int m = row(bi);
       const float dm = da[m];
-      const float from = (cb + cc * dm) * (kSB / kSA), by = cc * (kSB / kSA), squares = cc * (kSB / (kSA * kSA));
+      const float from = (cb + cc * dm) * (sb / kSA), by = cc * (sb / kSA), squares = cc * (sb / (kSA * kSA));
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int n = col(bj, 4 * u);
@@ -1022,7 +1023,7 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
       blocks([&](int bi, int bj) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          z[s][bi][bj][r] = __builtin_fmaf(db[col(bj, r)], z[s][bi][bj][r], acc[bi][bj][r] * (1.0f / kSB));
+          z[s][bi][bj][r] = __builtin_fmaf(db[col(bj, r)], z[s][bi][bj][r], acc[bi][bj][r] * inv_sb);
       });
     }
     __syncthreads();  // the last slab and B' have been read
@@ -1039,6 +1040,16 @@ __global__ __launch_bounds__(64 * (P / WM) * (P / 32)) void ns_small_kernel(NsAr
         if (i < pe && j < qe) out[tall ? j * a.ldo + i : i * a.ldo + j] = bf16_bits(z[s][bi][bj][r] * (1.0f / kSX));
       }
     });
+}
+
+// The power of two that B's FP16 elements carry. Those off the diagonal are at most half as large as B's eigenvalues
+// b s^2 + c s^4 lie apart, 32 |b| + 2048 |c| for s up to 8; 60000 leaves the operands' roundings room below FP16's
+// 65504. The usual quintic takes 8: elements under 2^-17 lose bits, at most 2^-28 beside the a that B is added to.
+float poly_scale(float b, float c) {
+  const float most = 32.0f * __builtin_fabsf(b) + 2048.0f * __builtin_fabsf(c);
+  float s = 512.0f;
+  while (s * most > 60000.0f) s *= 0.5f;
+  return s;
 }
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -1142,33 +1153,34 @@ int64_t align256(int64_t v) { return round_up(v, 256); }
 }  // namespace
 
 template <bool POLY>
-static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, int turn, float cb, float cc, hipStream_t stream) {
+static void launch_sym(const NsArgs& a, Shape shape, int splits, uint32_t batch, int turn, float cb, float cc, float sb,
+                       hipStream_t stream) {
   const uint32_t tiles = static_cast<uint32_t>(triangle_tiles(shape, a.pp));
   const dim3 grid(tiles, batch, static_cast<uint32_t>(splits));
   if constexpr (!POLY) {
     if (shape == k64x64 && splits > 1) {
-      hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, false, true>), grid, dim3(256), 0, stream, a, turn, cb, cc);
-      hipLaunchKernelGGL((ns_finish_kernel<64, 64, false>), dim3(tiles, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
+      hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, false, true>), grid, dim3(256), 0, stream, a, turn, cb, cc, sb);
+      hipLaunchKernelGGL((ns_finish_kernel<64, 64, false>), dim3(tiles, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc, sb);
       return;
     }
   }
   if (shape == k64x64) {
-    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, turn, cb, cc);
+    hipLaunchKernelGGL((ns_sym_kernel<64, 64, 32, 32, 4, POLY, false>), grid, dim3(256), 0, stream, a, turn, cb, cc, sb);
   } else if (shape == k128x128) {
-    hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, turn, cb, cc);
+    hipLaunchKernelGGL((ns_sym_kernel<128, 128, 64, 64, 4, POLY, false>), grid, dim3(256), 0, stream, a, turn, cb, cc, sb);
   } else {
-    hipLaunchKernelGGL((ns_sym_kernel<128, 256, 64, 64, 3, POLY, true>), grid, dim3(512), 0, stream, a, turn, cb, cc);
-    hipLaunchKernelGGL((ns_finish_kernel<128, 256, POLY>), dim3(tiles * 8, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc);
+    hipLaunchKernelGGL((ns_sym_kernel<128, 256, 64, 64, 3, POLY, true>), grid, dim3(512), 0, stream, a, turn, cb, cc, sb);
+    hipLaunchKernelGGL((ns_finish_kernel<128, 256, POLY>), dim3(tiles * 8, batch), dim3(256), 0, stream, a, static_cast<int>(tiles), splits, cb, cc, sb);
   }
 }
 
 template <bool LAST>
-static void launch_update(const NsArgs& a, Shape shape, uint32_t batch, float ca, int turn, hipStream_t stream) {
+static void launch_update(const NsArgs& a, Shape shape, uint32_t batch, float ca, float inv_sb, int turn, hipStream_t stream) {
   const int64_t bm = shape == k64x64 ? 64 : 128, bn = shape == k64x64 ? 64 : shape == k128x128 ? 128 : 256;
   const dim3 grid(static_cast<uint32_t>((a.qp / bm) * (a.pp / bn)), batch);
-  if (shape == k64x64) hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 32, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
-  else if (shape == k128x128) hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, turn);
-  else hipLaunchKernelGGL((ns_update_kernel<128, 256, 64, 64, 3, LAST>), grid, dim3(512), 0, stream, a, ca, turn);
+  if (shape == k64x64) hipLaunchKernelGGL((ns_update_kernel<64, 64, 32, 32, 4, LAST>), grid, dim3(256), 0, stream, a, ca, inv_sb, turn);
+  else if (shape == k128x128) hipLaunchKernelGGL((ns_update_kernel<128, 128, 64, 64, 4, LAST>), grid, dim3(256), 0, stream, a, ca, inv_sb, turn);
+  else hipLaunchKernelGGL((ns_update_kernel<128, 256, 64, 64, 3, LAST>), grid, dim3(512), 0, stream, a, ca, inv_sb, turn);
 }
 
 // Workspace parts, in order: X's remainders, two Xc, A, B, their diagonals, A's partial tiles, norms.
@@ -1209,8 +1221,11 @@ int64_t ns_workspace(int64_t batch, int64_t m, int64_t n) {
 hipError_t launch_newton_schulz(NsArgs a, int64_t batch, int steps, const float* coef, void* workspace, hipStream_t stream) {
   if (is_small(a.m, a.n)) {
     NsCoef c{};
-    for (int s = 0; s < steps; ++s)
+    for (int s = 0; s < steps; ++s) {
       for (int k = 0; k < 3; ++k) c.v[s][k] = coef[3 * s + k];
+      c.v[s][3] = poly_scale(coef[3 * s + 1], coef[3 * s + 2]);
+      c.v[s][4] = 1.0f / c.v[s][3];
+    }
     return a.gf32 ? launch_small<float>(a, c, steps, static_cast<uint32_t>(batch), stream)
                   : launch_small<uint16_t>(a, c, steps, static_cast<uint32_t>(batch), stream);
   }
@@ -1227,11 +1242,11 @@ hipError_t launch_newton_schulz(NsArgs a, int64_t batch, int steps, const float*
   }
   if (hipError_t e = hipGetLastError()) return e;
   for (int s = 0; s < steps; ++s) {
-    const float ca = coef[3 * s], cb = coef[3 * s + 1], cc = coef[3 * s + 2];
-    launch_sym<false>(a, p.gram, p.gram_splits, nb, s & 1, cb, cc, stream);
-    launch_sym<true>(a, p.poly, p.poly_splits, nb, s & 1, cb, cc, stream);
-    if (s + 1 < steps) launch_update<false>(a, p.update, nb, ca, s & 1, stream);
-    else launch_update<true>(a, p.update, nb, ca, s & 1, stream);
+    const float ca = coef[3 * s], cb = coef[3 * s + 1], cc = coef[3 * s + 2], sb = poly_scale(cb, cc);
+    launch_sym<false>(a, p.gram, p.gram_splits, nb, s & 1, cb, cc, sb, stream);
+    launch_sym<true>(a, p.poly, p.poly_splits, nb, s & 1, cb, cc, sb, stream);
+    if (s + 1 < steps) launch_update<false>(a, p.update, nb, ca, 1.0f / sb, s & 1, stream);
+    else launch_update<true>(a, p.update, nb, ca, 1.0f / sb, s & 1, stream);
     if (hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;

@@ -94,7 +94,8 @@ def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
     """newton_schulz with the FP16 roundings of a kernel's product operands, all else in float64.
 
     X is kept; its rounding enters the products (with `pairs`, in B X as value plus remainder). The
-    diagonals of A = X X^T and of B = b A + c A A are kept, their other elements rounded. The
+    diagonals of A = X X^T and of B = b A + c A A are kept, their other elements rounded, B's times a
+    power of two that holds singular values up to 8 (half of what b s^2 + c s^4 can differ by). The
     diagonal of B multiplies X's rounding as the rest of B does, and X itself in the last step (with
     `pairs`, in every step).
     """
@@ -114,5 +115,6 @@ def newton_schulz_operands(g, coefficients, eps=1e-7, pairs=False):
         poly = b * gram + c * (square + (d[:, None] + d[None, :]) * gram)
         diag = (b * d + c * (np.diag(square) + d * d))[:, None]
         own = x if pairs or step + 1 == len(coefficients) else xh
-        x = a * x + diag * own + f16(poly * off, 2.0 ** 9) @ xp
+        scale = 2.0 ** min(9.0, np.floor(np.log2(60000.0 / (32.0 * abs(b) + 2048.0 * abs(c) + 1e-9))))
+        x = a * x + diag * own + f16(poly * off, scale) @ xp
     return x.T if tall else x

@@ -180,3 +180,54 @@ def test_kernel_on_strong_rows_over_noise(m, n):
     ref = (x.t() if m > n else x).cpu().numpy()
     off = np.linalg.norm(pf8.newton_schulz(g).cpu().double().numpy() - ref) / np.linalg.norm(ref)
     assert off <= _allowed(GENERAL, ref), off
+
+
+# ------------------------------------------------------------------------------ the largest singular values
+# Steps that bring the one singular value to nearly 8, the largest that the header allows between the steps, and a
+# polynomial there. Half the square of a two-row matrix of equal rows stands off the diagonal of A and of B.
+LARGE = [
+    [(4.0, 0.0, 0.0), QUINTIC],
+    [(7.9, 0.0, 0.0), QUINTIC],
+    [(7.9, 0.0, 0.0), (1.0, -64.0, 0.0)],
+    [(7.9, 0.0, 0.0), (64.0, 64.0, 64.0)],
+    [(2.0, 0.0, 0.0), (3.9, 0.0, 0.0), (0.5, 1.0, -3.0)],
+]
+
+
+def _equal_rows(m, n, opposite=False):
+    x = np.zeros((m, n), dtype=np.float32)
+    x[2] = np.random.default_rng(m).standard_normal(n)
+    x[m - 3] = -x[2] if opposite else x[2]
+    return x
+
+
+def _large_allowed(coef, ref):
+    """Up to the last step nothing is rounded but X's FP32 form. There the rows are the same but for the sign, so their
+    roundings are alike: in the root mean square over a row at most half a step u each, of X (in A twice, in the
+    product once), of A and of B, 3 u of A, 6 u of A A, 2 u more of the two together."""
+    u, s = 2.0 ** -11, np.prod([c[0] for c in coef[:-1]])
+    a, b, c = coef[-1]
+    b, c = b * s ** 2, c * s ** 4
+    return u * (3 * abs(b) + 6 * abs(c) + 2 * abs(b + c)) / abs(a + b + c) + 2.0 ** -8
+
+
+@pytest.mark.parametrize("coef", LARGE)
+@pytest.mark.parametrize("shape", [(300, 400), (60, 100)])
+def test_operands_hold_the_largest_singular_values(shape, coef):
+    g = _equal_rows(*shape)
+    ref = train.newton_schulz(g, coef)
+    got = train.newton_schulz_operands(g, coef, pairs=_pairs(*shape))
+    assert np.linalg.norm(got - ref) <= _large_allowed(coef, ref) * np.linalg.norm(ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("coef", LARGE)
+@pytest.mark.parametrize("shape", [(300, 400), (400, 1300), (1300, 1400), (60, 100), (100, 120)])
+def test_kernel_holds_the_largest_singular_values(shape, coef):
+    import fp8_block_scaled_pf8_amd as pf8
+
+    for opposite in (False, True):
+        g = _equal_rows(*shape, opposite)
+        ref = train.newton_schulz(g, coef)
+        got = pf8.newton_schulz(torch.from_numpy(g).cuda(), steps=len(coef), coefficients=coef).cpu().double().numpy()
+        assert np.linalg.norm(got - ref) <= _large_allowed(coef, ref) * np.linalg.norm(ref)
