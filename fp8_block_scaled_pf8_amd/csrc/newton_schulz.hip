@@ -2,16 +2,18 @@
 // X = G / (|G|_F + eps). Contract in include/pf8_train.h.
 //
 // Bound: the matrix cores. With X [p, q] (p <= q; a tall G is taken transposed) a step is
-// p^2 q multiply-adds for A and p^3 / 2 for A A, both symmetric and formed for their lower tiles
+// p^2 q / 2 multiply-adds for A and p^3 / 2 for A A, both symmetric and formed for their lower tiles
 // only, and p^2 q for the update.
 //
 // Number formats. The products run on FP16 operands with FP32 accumulation; what adds up over the
 // steps has more bits:
-//  * X itself is kept as the sum of two FP16 values, the operand and its remainder (22 bits, 4 bytes
-//    an element and step less to move than FP32 beside the operand: 12288 x 2048 in 1221 us, 1268). The
-//    update adds a X from both; only the small product B X is formed from X's FP16 rounding. (Rounding X itself would put noise into directions whose singular
-//    value is nearly zero, which the iteration multiplies by a in every step: a rank-one G came
-//    out 15 % off.)
+//  * X itself is kept as the sum of two FP16 values, the operand and its remainder (4 bytes an element and
+//    step less to move than FP32 beside the operand: 12288 x 2048 in 1221 us, 1268). That is 22 bits of
+//    entries down to 2^-14 (X starts with norm 1); the remainder's steps end at 2^-36, which leaves 18 bits of
+//    an entry of 2^-18. All entries of a Gaussian 12288 x 2048 together are off by 4e-8, in FP32 2.5e-8. The
+//    update adds a X from both; only the small product B X is formed from X's FP16 rounding. (Rounding X
+//    itself would put noise into directions whose singular value is nearly zero, which the iteration
+//    multiplies by a in every step: a rank-one G came out 15 % off.)
 //  * A and B = b A + c A A are split into their diagonals, kept in FP32, and the rest in FP16:
 //    near the end A is close to a multiple of the identity and the diagonal carries nearly all.
 //    (A A)_ij = sum A'_ik A'_kj + (d_i + d_j) A'_ij off the diagonal.
@@ -28,8 +30,8 @@
 //    update as a sum of two FP16 values, diagonal or not: few entries average out little of the
 //    rounding noise.
 // Against float64, besides the BF16 rounding of the result (1.7e-3 of its 2-norm), five steps are off by
-// 1.1e-3 of its 2-norm for Gaussian gradients and up to 2e-3 for others (5e-3 where few entries carry the norm,
-// 1.5e-2 where all entries are of a few magnitudes and round alike); BF16 operands would give eight times that.
+// 1.1e-3 of its 2-norm for Gaussian gradients, up to 2e-3 for others of many rows and up to 1.5e-2 for those of
+// a few elements or magnitudes, which round alike; BF16 operands would give eight times that.
 //
 // Layout. X lives in the workspace, padded to multiples of 128 with zeros that stay zero, so the
 // products have no edges: Xc [q][p] (two buffers in turn; the update's operand, and A's by transposing

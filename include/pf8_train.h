@@ -116,13 +116,15 @@ int64_t pf8_block_norm_bwd_workspace(int64_t rows, int64_t cols);
  * eps: >= 0. A matrix of zeros gives zeros (NaN with eps = 0); one that holds a NaN or an infinity
  *      gives NaN everywhere.
  *
- * Precision: X is kept to 22 bits or more; the diagonals of X X^T and of the polynomial, and every sum,
- * are FP32 or FP64; the matrix products' operands are FP16, scaled by powers of two. Besides the BF16
- * rounding of the result (1.7e-3 of its 2-norm), five steps of the usual kind are off by up to 2e-3 of the
- * result's 2-norm (of any rank, also where few rows carry the gradient); by up to 5e-3 where under 64
- * entries do, and by up to 1.5e-2 where all entries have one of a few magnitudes (a constant matrix), whose
- * roundings are alike. What rounding puts outside the space of a gradient of low rank grows by a in every
- * step, as it does in FP32: rank one is off by up to 4e-3 after eight steps and 4e-2 after ten. The same call
+ * Precision: between the steps X is the sum of two FP16 values, which hold an element to 2^-23 of itself
+ * or to 2^-37, whichever is more (X starts with norm 1; FP32 in matrices of at most 64 x 512 or 128 x 256).
+ * The diagonals of X X^T and of the polynomial, and every sum, are FP32 or FP64; the matrix products'
+ * operands are FP16, scaled by powers of two. Besides the BF16 rounding of the result (1.7e-3 of its 2-norm)
+ * five steps of the usual kind leave it off by 0.2e-3 to 1.5e-3 of its 2-norm, up to 2e-3, whatever its rank.
+ * Roundings average out less where few elements carry the gradient: up to 4e-3 with under ten rows (or
+ * columns), up to 1.5e-2 with under 64 elements, or where all elements have one of a few magnitudes (a
+ * constant matrix). What rounding puts outside the space of a gradient of low rank grows by a in every step,
+ * as in an FP32 evaluation: rank one is about 3e-3 off after eight steps and 3e-2 after ten. The same call
  * gives the same bits.
  *
  * workspace: pf8_newton_schulz_workspace(batch, m, n) bytes, 256-byte aligned.

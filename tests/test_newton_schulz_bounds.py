@@ -7,10 +7,11 @@ A step X <- a X + f(A) X, f(A) = b A + c A A, rounds its operands to FP16: half 
 |f| <= 2.9 (s up to 1.2), and A = X X^T from both sides with sqrt(2) |b + 2 c s^2| s^2 <= 3.4 (at s^2 = 0.7 to
 1.4): together 4.5 * 2.1e-4 = 9.4e-4 a step. A step hands on a change of the singular vectors as it is, and
 of a singular value near one with a factor of about one. Five steps at most have singular values near one:
-sqrt(5) * 9.4e-4 = 2.1e-3, stated as 2e-3. Where under 64 entries carry the norm they may all be near
-their largest error, 2.36 times the root mean square: 5e-3. Where the entries take few magnitudes, the
-roundings of a step are alike and do not average out: 1.5e-2 (a constant matrix, whose iteration is one
-of scalars: 1.45e-2 the largest of 400000 sizes).
+sqrt(5) * 9.4e-4 = 2.1e-3, stated as 2e-3. Where few entries carry the norm they may all be near their largest
+error, 2.36 times the root mean square: 5e-3 for those drawn here. The header says 4e-3 for under ten rows and
+1.5e-2 for under 64 entries, which covers unlucky ones: the largest of 3000 and of 12000 drawn were 3.5e-3
+and 9.8e-3. Where the entries take few magnitudes, the roundings of a step are alike and do not average out:
+1.5e-2 (a constant matrix, whose iteration is one of scalars: 1.45e-2 the largest of 400000 sizes).
 
 The BF16 rounding of the result: 1.7e-3 (1 + 1.8 / sqrt(N)) of the 2-norm, at most 2^-8, N = (sum y^2)^2 /
 sum y^4; independent of the rest where N >= 64, else the two add.
