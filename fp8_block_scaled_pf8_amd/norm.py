@@ -373,7 +373,8 @@ class BlockNorm(torch.nn.Module):
     """Post-norm, gate, residual sum and pre-norm between two blocks: ``r, x = norm(h, y)``.
 
     ``pre`` / ``post`` choose which of the two norms there are; ``gate`` adds a learned [cols] gate
-    (started at ``gate_init``), and a gate per token can be passed to ``forward`` instead. Weights are
+    (started at ``gate_init``), and a gate per token can be passed to ``forward`` instead. Without y (before
+    a model's first block) x is h's pre-norm and the rest stands aside. Weights are
     kept in ``dtype`` (BF16 as the rest of the model, or FP32). With ``fp32_main_grad`` every weight
     carries a float32 ``main_grad`` that each backward pass adds to, and its ``grad`` stays None.
     """
@@ -400,14 +401,16 @@ class BlockNorm(torch.nn.Module):
         self.w_post = weight(post, fill)
         self.gate = weight(gate, gate_init)
 
-    def _operands(self, gate):
+    def _operands(self, y, gate):
         if gate is not None and self.gate is not None:
             raise ValueError("this BlockNorm has a learned gate: none can be passed")
+        if gate is not None and y is None:
+            raise ValueError("without a branch y there is no gate")
         return self.w_pre, self.w_post, self.gate if gate is None else gate
 
     def forward(self, h: Tensor, y: Optional[Tensor] = None, gate: Optional[Tensor] = None
                 ) -> Tuple[Tensor, Optional[Tensor]]:
-        w_pre, w_post, g = self._operands(gate)
+        w_pre, w_post, g = self._operands(y, gate)
         main = tuple(getattr(w, "main_grad", None) for w in (w_pre, w_post, g if gate is None else None))
         if y is None:
             return fp8_block_norm(h, None, w_pre, eps=self.eps, unit_offset=self.unit_offset,
@@ -419,7 +422,7 @@ class BlockNorm(torch.nn.Module):
     def quantised(self, h: Tensor, y: Optional[Tensor] = None, gate: Optional[Tensor] = None
                   ) -> Tuple[Tensor, Tensor, Tensor]:
         """(r, codes, scales) of 2-D h and y, for ``fprop`` (no gradients; see ``block_norm_quant``)."""
-        w_pre, w_post, g = self._operands(gate)
+        w_pre, w_post, g = self._operands(y, gate)
         if y is None:
             return block_norm_quant(h, None, w_pre, eps=self.eps, unit_offset=self.unit_offset)
         return block_norm_quant(h, y, w_pre, w_post, g, self.residual_scale, self.branch_scale, self.eps,

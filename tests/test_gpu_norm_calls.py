@@ -40,3 +40,15 @@ def test_captured_backward_adds_to_the_callers_buffers(rows, cols):
         assert all(torch.equal(a, b) for a, b in zip(sums.values(), want)), i
         assert torch.equal(g.dh, eager.dh) and torch.equal(g.dy, eager.dy)
     assert g.dw_pre is sums["dw_pre_out"] and g.dw_post is sums["dw_post_out"] and g.dgate is sums["dgate_out"]
+
+
+def test_a_gate_without_a_branch_is_refused():
+    """As block_norm refuses it: there is nothing that the gate could multiply."""
+    norm = pf8.BlockNorm(256, device=DEV)
+    h, gate = _rand((4, 256), 1), _rand((4, 256), 2)
+    for call in (norm, norm.quantised):
+        with pytest.raises(ValueError, match="gate"):
+            call(h, None, gate)
+        call(h)
+    learned = pf8.BlockNorm(256, gate=True, device=DEV)
+    assert learned(h)[1].shape == h.shape  # the first block's norm: the module's own gate waits for a branch
