@@ -109,20 +109,36 @@ def _output(out: Optional[Tensor], name: str, like: Tensor) -> Tuple[Tensor, int
     return out, out.data_ptr(), like.shape[1]
 
 
-def _extent(t: Tensor) -> Tuple[int, int]:
-    """First byte and the byte behind the last of a 2-D tensor with at least one element."""
-    n = (t.shape[0] - 1) * t.stride(0) + (t.shape[1] - 1) * t.stride(1) + 1
-    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+def _rows_meet(a: Tuple[int, int, int, int], b: Tuple[int, int, int, int]) -> bool:
+    """Whether two sets of rows share memory; each (first byte, byte behind the last, bytes of a row, pitch or 0 of
+    a single row). Rows of one pitch may lie between one another's; rows of different pitches count as
+    shared where their extents meet."""
+    (a0, a1, wa, pa), (b0, b1, wb, pb) = a, b
+    if a1 <= b0 or b1 <= a0:
+        return False
+    pitch = pa or pb
+    if not pitch or (pb or pitch) != pitch:
+        return True
+    ahead = (b0 - a0) % pitch
+    return ahead < wa or ahead + wb > pitch
+
+
+def _rows_at(t: Tensor) -> Tuple[int, int, int, int]:
+    """_rows_meet's view of a 1-D or 2-D tensor with at least one element and contiguous rows."""
+    first, size = t.data_ptr(), t.element_size()
+    width = t.shape[-1] * size
+    pitch = t.stride(0) * size if t.dim() == 2 and t.shape[0] > 1 else 0
+    return first, first + (t.shape[0] - 1) * pitch + width, width, pitch
 
 
 def _may_write(out: Tensor, name: str, others) -> None:
     """Raise if `out` shares memory with another operand without being the very same rows of it."""
-    a, b = _extent(out)
+    a = _rows_at(out)
     for o, same_ok in others:
         if o is None or o.device != out.device:
             continue
-        c, d = _extent(o) if o.dim() == 2 else (o.data_ptr(), o.data_ptr() + o.numel() * o.element_size())
-        if a < d and c < b and not (same_ok and a == c and (out.shape[0] == 1 or out.stride(0) == o.stride(0))):
+        b = _rows_at(o)
+        if _rows_meet(a, b) and not (same_ok and a[0] == b[0] and a[3] == b[3]):
             raise ValueError(f"{name} overlaps another operand")
 
 
@@ -255,11 +271,8 @@ def block_norm_backward(dr: Optional[Tensor], dx: Optional[Tensor], h: Tensor, y
     if accumulate or dw_pre_out is not None or dw_post_out is not None or dgate_out is not None:
         operands = [t for t in (dr, dx, h, y, w_pre, w_post, gate) if t is not None and t.numel()]
         for i, t in enumerate(sums):
-            a, b = t.data_ptr(), t.data_ptr() + 4 * cols
-            for o in operands + sums[:i]:
-                c, d = _extent(o) if o.dim() == 2 else (o.data_ptr(), o.data_ptr() + o.numel() * o.element_size())
-                if a < d and c < b:
-                    raise ValueError("a gradient buffer overlaps another operand")
+            if any(_rows_meet(_rows_at(t), _rows_at(o)) for o in operands + sums[:i]):
+                raise ValueError("a gradient buffer overlaps another operand")
     if rows == 0:
         if not accumulate:
             for t in sums:

@@ -12,7 +12,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib as L
-from .norm import _call
+from .norm import _call, _rows_meet
 
 # Steep at zero (slope 3.4445), so that small singular values grow fast; after five steps values
 # above 1e-2 of the norm lie between 0.7 and 1.2.
@@ -57,14 +57,18 @@ def newton_schulz(g: torch.Tensor, steps: int = 5, coefficients: Sequence = QUIN
         stride = t.stride(0) if batch > 1 else 0
         if (n > 1 and t.stride(-1) != 1) or ld < n or (batch > 1 and stride < (m - 1) * ld + n):
             raise ValueError(f"{name} must have contiguous rows, and neither its rows nor its matrices may overlap")
-        first = t.data_ptr()
-        layouts.append((ld, stride, first, first + ((batch - 1) * stride + (m - 1) * ld + n) * t.element_size()))
-    (ldg, sg, g0, g1), (ldo, so, o0, o1) = layouts
-    if g0 < o1 and o0 < g1:
+        first, size = t.data_ptr(), t.element_size()
+        # one pitch for all rows of a stack, or all its matrices as single pieces
+        whole = batch > 1 and m > 1 and stride % ld
+        width = (m - 1) * ld + n if whole else n
+        pitch = stride if whole or m == 1 else ld
+        layouts.append((ld, stride, (first, first + ((batch - 1) * stride + (m - 1) * ld + n) * size, width * size, pitch * size)))
+    (ldg, sg, at_g), (ldo, so, at_o) = layouts
+    if _rows_meet(at_g, at_o):
         raise ValueError("out overlaps g")
     coef = (ctypes.c_float * (3 * steps))(*(v for c in triples for v in c))
     size = L.pf8_newton_schulz_workspace(batch, m, n)
     ws = torch.empty(size, dtype=torch.uint8, device=g.device)
-    _call(L.pf8_newton_schulz, g.device, batch, m, n, g0, ldg, sg, L.PF8_F32 if g.dtype == torch.float32 else L.PF8_BF16,
-          steps, coef, eps, o0, ldo, so, ws.data_ptr(), size)
+    _call(L.pf8_newton_schulz, g.device, batch, m, n, at_g[0], ldg, sg, L.PF8_F32 if g.dtype == torch.float32 else L.PF8_BF16,
+          steps, coef, eps, at_o[0], ldo, so, ws.data_ptr(), size)
     return out

@@ -52,3 +52,37 @@ def test_a_gate_without_a_branch_is_refused():
         call(h)
     learned = pf8.BlockNorm(256, gate=True, device=DEV)
     assert learned(h)[1].shape == h.shape  # the first block's norm: the module's own gate waits for a branch
+
+
+def test_results_beside_their_inputs_in_one_buffer():
+    """Column ranges of one buffer: their rows lie between one another's, and none is shared."""
+    buf = torch.zeros((9, 1024), dtype=BF, device=DEV)
+    h, y, r, x = (buf[:, 256 * i:256 * i + 256] for i in range(4))
+    h.copy_(_rand((9, 256), 1, 2.0))
+    y.copy_(_rand((9, 256), 2))
+    w = _rand((256,), 3)
+    want = pf8.block_norm(h, y, w, w)
+    got = pf8.block_norm(h, y, w, w, r_out=r, x_out=x)
+    assert got[0] is r and got[1] is x
+    assert torch.equal(r, want[0]) and torch.equal(x, want[1])
+    for r_bad in (buf[:, 200:456], buf[:, 500:756], buf[:, 255:511]):
+        with pytest.raises(ValueError, match="overlaps"):
+            pf8.block_norm(h, y, w, w, r_out=r_bad)
+    # another pitch over the same memory
+    wide = torch.zeros((4, 512), dtype=BF, device=DEV)
+    with pytest.raises(ValueError, match="overlaps"):
+        pf8.block_norm(wide[:, :256], None, w, x_out=wide.view(-1)[256:1280].view(4, 256))
+
+
+def test_orthogonalised_beside_its_gradient_in_one_buffer():
+    buf = torch.zeros((3, 40, 160), dtype=BF, device=DEV)
+    g, out = buf[..., :80], buf[..., 80:]
+    g.copy_(_rand((3, 40, 80), 1))
+    want = pf8.newton_schulz(g)
+    assert pf8.newton_schulz(g, out=out) is out and torch.equal(out, want)
+    out.zero_()
+    assert torch.equal(pf8.newton_schulz(g[1], out=out[1]), want[1])
+    assert torch.equal(pf8.newton_schulz(g[:, :1], out=out[:, :1]), pf8.newton_schulz(g[:, :1]))
+    for bad in (buf[..., 79:159], buf[..., :80], buf[:, :, 40:120]):
+        with pytest.raises(ValueError, match="overlaps"):
+            pf8.newton_schulz(g, out=bad)

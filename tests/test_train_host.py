@@ -137,3 +137,25 @@ def test_newton_schulz_workspace():
     assert size(65536, 5, 5) == 0 and size(1, 1, 1) > 0
     # an element is kept as a transposed FP16 operand in two buffers and an FP16 remainder: 6 bytes
     assert size(1, 2048, 512) == size(1, 512, 2048) >= 2048 * 512 * 6
+
+
+def test_rows_that_share_memory_are_found():
+    """Against the sets of bytes: never missed, and exact where the pitches are one or a side is a single row."""
+    import itertools
+
+    from fp8_block_scaled_pf8_amd.norm import _rows_meet
+
+    def rows(first, count, width, pitch):
+        at = {first + r * pitch + b for r in range(count) for b in range(width)}
+        return at, (first, max(at) + 1, width, pitch if count > 1 else 0)
+
+    for (f, n, w, p), (k, v, q) in itertools.product(
+            itertools.product(range(0, 30), (1, 3), (1, 3, 5), (5, 8)), itertools.product((1, 2, 4), (2, 5), (5, 8))):
+        a, at_a = rows(f, n, w, p)
+        b, at_b = rows(12, k, v, q)
+        shared, found = bool(a & b), _rows_meet(at_a, at_b)
+        assert found == _rows_meet(at_b, at_a)
+        assert found if shared else True
+        if n > 1 and k > 1 and p == q and not shared:
+            # (rows beyond one side's end count as its own: they lie within the other's extent)
+            assert not found or not rows(f, 20, w, p)[0].isdisjoint(rows(12, 20, v, q)[0] | rows(12 - 10 * q, 20, v, q)[0])
