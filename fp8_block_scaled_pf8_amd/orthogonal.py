@@ -40,8 +40,11 @@ def newton_schulz(g: torch.Tensor, steps: int = 5, coefficients: Sequence = QUIN
                          f"{L.PF8_NS_MAX_LONG} (the longer), got {m} x {n}")
     if batch > L.PF8_NS_MAX_BATCH:
         raise ValueError(f"newton_schulz takes up to {L.PF8_NS_MAX_BATCH} matrices at once, got {batch}")
-    if isinstance(steps, bool) or int(steps) != steps or not 1 <= steps <= L.PF8_NS_MAX_STEPS:
+    if isinstance(steps, bool) or not 1 <= steps <= L.PF8_NS_MAX_STEPS or int(steps) != steps:
         raise ValueError(f"steps must be 1 to {L.PF8_NS_MAX_STEPS}, got {steps}")
+    steps = int(steps)
+    if len(coefficients) == 0:
+        raise ValueError("coefficients must not be empty")
     triples = [tuple(coefficients)] * steps if not hasattr(coefficients[0], "__len__") else [tuple(c) for c in coefficients]
     if len(triples) != steps or any(len(c) != 3 for c in triples):
         raise ValueError(f"coefficients must be one (a, b, c) or {steps} of them")

@@ -86,3 +86,13 @@ def test_orthogonalised_beside_its_gradient_in_one_buffer():
     for bad in (buf[..., 79:159], buf[..., :80], buf[:, :, 40:120]):
         with pytest.raises(ValueError, match="overlaps"):
             pf8.newton_schulz(g, out=bad)
+
+
+def test_orthogonalisation_takes_whole_numbers_of_steps_of_any_type():
+    g = _rand((20, 30), 1)
+    want = pf8.newton_schulz(g, steps=3)
+    assert torch.equal(pf8.newton_schulz(g, steps=3.0), want)
+    assert torch.equal(pf8.newton_schulz(g, steps=torch.tensor(3)), want)
+    for bad in (dict(steps=2.5), dict(steps=float("inf")), dict(steps=float("nan")), dict(coefficients=())):
+        with pytest.raises(ValueError):
+            pf8.newton_schulz(g, **bad)
