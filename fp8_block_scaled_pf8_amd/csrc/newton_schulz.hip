@@ -725,7 +725,7 @@ __device__ __forceinline__ h8 swap_halves(h8 v) {
 
 // X is read before the product, so that it arrives behind its first stages. Bound by the matrix cores and the
 // LDS reads that feed them; among the other kernels 12288 x 2048 takes 125 us (820 TFLOP/s), the last step,
-// which writes BF16 only, 121 us.
+// which writes BF16 only, 120 us.
 template <int BM, int BN, int WM, int WN, int NST, bool LAST>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void ns_update_kernel(NsArgs a, float ca, float inv_sb, int turn) {
   using G = Tile<BM, BN, WM, WN, NST, false>;
