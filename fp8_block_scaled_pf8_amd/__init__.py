@@ -1,8 +1,9 @@
 """Block-scaled FP8 (E4M3) linear-layer quantisers and GEMM for AMD MI355X (gfx950), with the
-training operators around the layer (block norm, Newton-Schulz orthogonalisation).
+training operators around the layer (block norm, Newton-Schulz orthogonalisation) and a decoder layer's steps around
+its products (head norms with rotation, activations).
 
-The computation lives in libpf8.so (HIP kernels behind a C ABI, include/pf8.h and
-include/pf8_train.h); this package is its Python binding. Importing it fails when the library has not been built.
+The computation lives in libpf8.so (HIP kernels behind a C ABI: include/pf8.h, include/pf8_train.h and
+include/pf8_layer.h); this package is its Python binding. Importing it fails when the library has not been built.
 """
 from . import _lib
 from ._lib import (
@@ -17,6 +18,8 @@ from ._lib import (
     PF8_GEMM_PROMOTE,
     PF8_WGRAD,
     pf8_abi_version,
+    pf8_act_bwd,
+    pf8_act_bwd_workspace,
     pf8_block_gemm,
     pf8_block_gemm_f32,
     pf8_block_gemm_variant,
@@ -26,12 +29,18 @@ from ._lib import (
     pf8_gemm_bf16,
     pf8_newton_schulz,
     pf8_newton_schulz_workspace,
+    pf8_qk_norm_rope,
+    pf8_qk_norm_rope_bwd,
+    pf8_qk_norm_rope_bwd_workspace,
     pf8_quant_act_1x128,
     pf8_quant_act_dual,
     pf8_quant_fwd,
     pf8_quant_w_128x128,
     pf8_strerror,
 )
+from .epilogue import ActGrads, act_backward
+from .heads import (QKNormRope, QKNormRopeFunction, QKNormRopeGrads, fp8_qk_norm_rope, qk_norm_rope,
+                    qk_norm_rope_backward)
 from .linear import Fp8Linear, Fp8LinearFunction, fp8_linear
 from .norm import (BlockNorm, BlockNormFunction, BlockNormGrads, block_norm, block_norm_backward, block_norm_quant,
                    fp8_block_norm)
@@ -49,4 +58,7 @@ __all__ = [
     "PF8_BF16", "PF8_F32", "pf8_block_norm", "pf8_block_norm_bwd", "pf8_block_norm_bwd_workspace",
     "BlockNorm", "BlockNormFunction", "BlockNormGrads", "block_norm", "block_norm_backward", "block_norm_quant",
     "fp8_block_norm", "pf8_newton_schulz", "pf8_newton_schulz_workspace", "newton_schulz",
+    "pf8_qk_norm_rope", "pf8_qk_norm_rope_bwd", "pf8_qk_norm_rope_bwd_workspace", "pf8_act_bwd", "pf8_act_bwd_workspace",
+    "QKNormRope", "QKNormRopeFunction", "QKNormRopeGrads", "fp8_qk_norm_rope", "qk_norm_rope", "qk_norm_rope_backward",
+    "ActGrads", "act_backward",
 ]

@@ -1,4 +1,5 @@
-"""ctypes binding of libpf8 (include/pf8.h, include/pf8_train.h): the C entry points under the same names.
+"""ctypes binding of libpf8 (include/pf8.h, include/pf8_train.h, include/pf8_layer.h): the C entry points under the
+same names.
 
 Argument marshalling only: pointers are passed as Python ints (device addresses), sizes as
 ints, the stream as a hipStream_t handle (int, 0 = null stream). Every function returns the
@@ -23,10 +24,14 @@ PF8_OK, PF8_EINVAL, PF8_ESHAPE, PF8_EALIGN, PF8_ENODEV, PF8_ELAUNCH = range(6)
 PF8_ALONG_COLS, PF8_ALONG_ROWS = 0, 1
 PF8_FPROP, PF8_DGRAD, PF8_WGRAD = 0, 1, 2
 PF8_GEMM_AUTO, PF8_GEMM_MX_SCALED, PF8_GEMM_PROMOTE = 0, 1, 2
-PF8_BF16, PF8_F32 = 0, 1
+PF8_BF16, PF8_F32, PF8_F64 = 0, 1, 2
+PF8_I32, PF8_I64 = 0, 1
+PF8_BLOCKED, PF8_CYCLED = 0, 1
+PF8_HEAD_MAX_DIM, PF8_HEAD_MAX_AXES, PF8_HEAD_MAX_HEADS = 512, 4, 65536
+PF8_ACT_NONE, PF8_ACT_RELU, PF8_ACT_RELU2, PF8_ACT_SILU, PF8_ACT_GELU, PF8_ACT_GELU_TANH = range(6)
 PF8_NORM_MAX_COLS = 16384
 PF8_NS_MAX_SHORT, PF8_NS_MAX_LONG, PF8_NS_MAX_BATCH, PF8_NS_MAX_STEPS = 32768, 1048576, 65535, 64
-ABI_VERSION = 6
+ABI_VERSION = 7
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -65,6 +70,24 @@ TRAIN_SIGNATURES = {
     "pf8_newton_schulz_workspace": (_i64, [_i64, _i64, _i64]),
 }
 
+# one [tokens, heads, head_dim] array: address, strides of tokens and heads
+_HEADS = [_vp, _i64, _i64]
+# what both directions of the head norm take behind the arrays: w_q .. rotary_scale
+_HEAD_IN = [_vp, _vp, _int, _f32, _f32, _vp, _int, _i64, _i64, _vp, _int, _i64, _int, _vp, _int, _int, _f32]
+
+# name -> (restype, argtypes); mirrors include/pf8_layer.h
+LAYER_SIGNATURES = {
+    "pf8_qk_norm_rope": (
+        _int, [_i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, *_HEAD_IN, *_HEADS, *_HEADS, _vp]),
+    "pf8_qk_norm_rope_bwd": (
+        _int, [_i64, _i64, *_HEADS, *_HEADS, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _i64, *_HEAD_IN, *_HEADS, *_HEADS,
+               _vp, _vp, _int, _vp, _i64, _vp]),
+    "pf8_qk_norm_rope_bwd_workspace": (_i64, [_i64, _i64, _i64, _i64]),
+    "pf8_act_bwd": (
+        _int, [_i64, _i64, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp, _int, _vp, _i64, _vp]),
+    "pf8_act_bwd_workspace": (_i64, [_i64, _i64, _int]),
+}
+
 
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
@@ -72,7 +95,7 @@ def _load() -> ctypes.CDLL:
             f"libpf8.so is not built ({LIB_PATH}); run `python fp8_block_scaled_pf8_amd/build.py` "
             "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in {**SIGNATURES, **TRAIN_SIGNATURES}.items():
+    for name, (res, args) in {**SIGNATURES, **TRAIN_SIGNATURES, **LAYER_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
@@ -153,6 +176,15 @@ def pf8_newton_schulz(batch, m, n, g, ldg, stride_g, gtype, steps, coefficients,
 
 def pf8_newton_schulz_workspace(batch, m, n) -> int:
     return LIB.pf8_newton_schulz_workspace(batch, m, n)
+
+
+# The entry points of include/pf8_layer.h, called as they are: a Python function that hands on some 40 arguments
+# costs two microseconds, half of what the smallest of these calls take on the GPU.
+pf8_qk_norm_rope = LIB.pf8_qk_norm_rope
+pf8_qk_norm_rope_bwd = LIB.pf8_qk_norm_rope_bwd
+pf8_qk_norm_rope_bwd_workspace = LIB.pf8_qk_norm_rope_bwd_workspace
+pf8_act_bwd = LIB.pf8_act_bwd
+pf8_act_bwd_workspace = LIB.pf8_act_bwd_workspace
 
 
 def pf8_strerror(status: int) -> str:

@@ -7,28 +7,16 @@
 #include <cmath>
 
 #include "../../include/pf8_train.h"
+#include "abi_check.h"
 #include "pf8_train_launch.h"
 
 namespace {
 
-constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
-template <typename... T>
-bool any_too_big(T... v) {
-  return ((v > kMaxDim) || ...);
-}
-
-bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-
-int device_status() {
-  int count = 0;
-  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
-    (void)hipGetLastError();  // clear the sticky error of a failed query
-    return PF8_ENODEV;
-  }
-  return PF8_OK;
-}
-
-int launch_status(hipError_t e) { return e == hipSuccess ? PF8_OK : PF8_ELAUNCH; }
+using pf8::aligned;
+using pf8::any_too_big;
+using pf8::device_status;
+using pf8::kMaxDim;
+using pf8::launch_status;
 
 // What the block norm's two directions check alike.
 int check_norm_inputs(int64_t rows, int64_t cols, const void* h, int64_t ldh, const void* y, int64_t ldy,

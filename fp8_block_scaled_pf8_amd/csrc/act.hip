@@ -1,0 +1,146 @@
+// Backward of an activation, gated or not, with the bias's gradient (gfx950). Formulas in include/pf8_layer.h.
+//
+// Bound: HBM. 6 bytes a value of dd without a gate (dd, z in, dz out), 10 with one.
+// A thread keeps 8 columns and walks rows; a workgroup is as many threads wide as the columns ask for (up
+// to 256, 2048 columns), the rest of its 256 threads take further rows. Column sums stay in registers over
+// a thread's rows, meet in LDS, and a workgroup writes one row of partial sums.
+#include "act_device.h"
+#include "pf8_layer_launch.h"
+#include "pf8_train_launch.h"
+#include "row_device.h"
+
+namespace pf8 {
+
+namespace {
+
+// How the last, ragged step of a row is taken: kOdd: the row's last 8 columns, of which the first belong to the
+// thread before and are neither counted nor stored; kTiny: rows of under 8 columns, value by value.
+enum RowEnd { kEven, kOdd, kTiny };
+
+template <int ACT, bool GATED, RowEnd END>
+__global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int wide) {
+  const int tx = threadIdx.x & (wide - 1), ty = threadIdx.x / wide, high = 256 / wide;
+  const int cols = a.cols;
+  int c = 8 * (static_cast<int>(blockIdx.x) * wide + tx);
+  const int n = cols - c;  // columns from here
+  const int first = END == kTiny || n >= 8 ? 0 : n <= 0 ? 8 : 8 - n;
+  if (END == kOdd && n < 8) c = cols - 8;
+  const bool any = n > 0;
+  auto load = [&](const uint16_t* row) {
+    return END == kTiny ? load_few(row + c, n) : load8(row + c);
+  };
+  auto store = [&](uint16_t* row, const float (&f)[8]) {
+    const uint4 v = pack8(f);
+    uint16_t* p = row + c;
+    if constexpr (END == kTiny) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (k < n) p[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+    } else if (END == kEven || first == 0) {
+      *reinterpret_cast<u128_a2*>(p) = u128_a2{v.x, v.y, v.z, v.w};
+    } else {
+      store_last(p, v, 8 - first);
+    }
+  };
+  constexpr int PARTS = GATED ? 2 : 1;
+  constexpr bool HAS_Z = ACT != PF8_ACT_NONE;
+  float sums[PARTS][8] = {};
+  const int64_t step = static_cast<int64_t>(gridDim.y) * high;
+  for (int64_t row = static_cast<int64_t>(blockIdx.y) * high + ty; any && row < a.rows; row += step) {
+    float d[8], z[8], o[8];
+    const uint4 dv = load(a.dd + row * a.lddd);
+    uint4 zv, uv;
+    if constexpr (HAS_Z) zv = load(a.z + row * a.ldz);
+    if constexpr (GATED) uv = load(a.z + row * a.ldz + cols);
+    unpack8(dv, d);
+    if constexpr (HAS_Z) unpack8(zv, z);
+    if constexpr (GATED) {
+      float u[8], up[8];
+      unpack8(uv, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float value, slope;
+        act_both<ACT>(z[k], value, slope);
+        o[k] = d[k] * u[k] * slope;
+        up[k] = d[k] * value;
+        sums[1][k] += up[k];
+      }
+      if (a.dz) store(a.dz + row * a.lddz + cols, up);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float value = 0.0f, slope = 1.0f;
+        if constexpr (HAS_Z) act_both<ACT>(z[k], value, slope);
+        o[k] = d[k] * slope;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[0][k] += o[k];
+    if (a.dz) store(a.dz + row * a.lddz, o);
+  }
+  if (!a.partial) return;
+  __shared__ float sh[256][9];
+  float* out = a.partial + static_cast<int64_t>(blockIdx.y) * PARTS * cols;
+#pragma unroll
+  for (int part = 0; part < PARTS; ++part) {
+    if (high > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sh[threadIdx.x][k] = sums[part][k];
+      __syncthreads();
+      if (ty == 0) {
+        for (int y = 1; y < high; ++y)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sums[part][k] += sh[y * wide + tx][k];
+      }
+    }
+    if (ty == 0 && any) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k >= first && c + k < cols) out[part * cols + c + k] = sums[part][k];
+    }
+  }
+}
+
+}  // namespace
+
+// Threads of a workgroup along a row: a power of two.
+static int act_bwd_wide(int64_t cols) {
+  int wide = 1;
+  while (wide < 256 && 8 * wide < cols) wide *= 2;
+  return wide;
+}
+
+int64_t act_bwd_groups(int64_t rows, int64_t cols, int gated) {
+  const int64_t wide = act_bwd_wide(cols), strips = (cols + 8 * wide - 1) / (8 * wide), high = 256 / wide;
+  const int64_t most = (rows + high - 1) / high, want = (1024 + strips - 1) / strips;
+  return most < want ? most : want;
+}
+
+hipError_t launch_act_bwd(const ActBwdArgs& a, float* dbias, int accumulate, hipStream_t stream) {
+  const int wide = act_bwd_wide(a.cols);
+  const int64_t strips = (a.cols + 8 * wide - 1) / (8 * wide), groups = act_bwd_groups(a.rows, a.cols, a.gated);
+  auto go = [&](auto act, auto gated, auto end) {
+    hipLaunchKernelGGL((act_bwd_kernel<decltype(act)::value, decltype(gated)::value, decltype(end)::value>),
+                       dim3(static_cast<uint32_t>(strips), static_cast<uint32_t>(groups)), dim3(256), 0, stream, a, wide);
+    return hipGetLastError();
+  };
+  auto by_end = [&](auto act, auto gated) {
+    if (a.cols < 8) return go(act, gated, std::integral_constant<RowEnd, kTiny>{});
+    if (a.cols % 8) return go(act, gated, std::integral_constant<RowEnd, kOdd>{});
+    return go(act, gated, std::integral_constant<RowEnd, kEven>{});
+  };
+  const hipError_t e = by_activation(a.act, [&](auto act) {
+    if constexpr (decltype(act)::value != PF8_ACT_NONE) {
+      if (a.gated) return by_end(act, std::true_type{});
+    }
+    return by_end(act, std::false_type{});
+  });
+  if (e != hipSuccess || !dbias) return e;
+  const int width = a.gated ? 2 * a.cols : a.cols;
+  float* outs[3] = {dbias, nullptr, nullptr};
+  return launch_column_sums(a.partial, static_cast<int>(groups), width, width, outs, accumulate, stream);
+}
+
+}  // namespace pf8

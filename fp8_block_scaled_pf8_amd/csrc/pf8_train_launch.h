@@ -58,6 +58,9 @@ hipError_t launch_norm_fwd(const NormFwdArgs& args, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormBwdArgs& args, hipStream_t stream);
 // Workgroups of the backward pass, each with one row of partial column sums.
 int64_t norm_bwd_groups(int64_t rows, int64_t cols);
+// Column sums of partial rows [groups][width], in a fixed order, into outs[c / cols][c % cols]; accumulate: added.
+hipError_t launch_column_sums(const float* partial, int groups, int width, int cols, float* const (&outs)[3],
+                              int accumulate, hipStream_t stream);
 
 // Newton-Schulz orthogonalisation; the launcher fills in what lies in the workspace.
 struct NsArgs {
