@@ -1,6 +1,6 @@
 """Block-scaled FP8 (E4M3) linear-layer quantisers and GEMM for AMD MI355X (gfx950), with the
 training operators around the layer (block norm, Newton-Schulz orthogonalisation) and a decoder layer's steps around
-its products (head norms with rotation, activations).
+its products (head norms with rotation, products with bias, activation and residual in their epilogue).
 
 The computation lives in libpf8.so (HIP kernels behind a C ABI: include/pf8.h, include/pf8_train.h and
 include/pf8_layer.h); this package is its Python binding. Importing it fails when the library has not been built.
@@ -26,6 +26,7 @@ from ._lib import (
     pf8_block_norm,
     pf8_block_norm_bwd,
     pf8_block_norm_bwd_workspace,
+    pf8_fprop_act,
     pf8_gemm_bf16,
     pf8_newton_schulz,
     pf8_newton_schulz_workspace,
@@ -38,7 +39,7 @@ from ._lib import (
     pf8_quant_w_128x128,
     pf8_strerror,
 )
-from .epilogue import ActGrads, act_backward
+from .epilogue import ActGrads, act_backward, fprop_act
 from .heads import (QKNormRope, QKNormRopeFunction, QKNormRopeGrads, fp8_qk_norm_rope, qk_norm_rope,
                     qk_norm_rope_backward)
 from .linear import Fp8Linear, Fp8LinearFunction, fp8_linear
@@ -60,5 +61,5 @@ __all__ = [
     "fp8_block_norm", "pf8_newton_schulz", "pf8_newton_schulz_workspace", "newton_schulz",
     "pf8_qk_norm_rope", "pf8_qk_norm_rope_bwd", "pf8_qk_norm_rope_bwd_workspace", "pf8_act_bwd", "pf8_act_bwd_workspace",
     "QKNormRope", "QKNormRopeFunction", "QKNormRopeGrads", "fp8_qk_norm_rope", "qk_norm_rope", "qk_norm_rope_backward",
-    "ActGrads", "act_backward",
+    "pf8_fprop_act", "ActGrads", "act_backward", "fprop_act",
 ]

@@ -16,6 +16,9 @@ bool any_too_big(T... v) {
   return ((v > kMaxDim) || ...);
 }
 
+// A GEMM tile's rows are addressed from its first by signed 32-bit offsets: 256 rows x pitch in bytes.
+constexpr int64_t kMaxTilePitch = kMaxDim / 256;
+
 inline bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 inline int device_status() {

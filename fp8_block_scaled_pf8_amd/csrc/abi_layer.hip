@@ -199,4 +199,34 @@ pf8_status pf8_act_bwd(int64_t rows, int64_t cols, const void* dd, int64_t lddd,
   return launch_status(pf8::launch_act_bwd(a, dbias, accumulate, static_cast<hipStream_t>(hip_stream)));
 }
 
+pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* a_dscale,
+                         int64_t ld_as, const void* b, int64_t ldb, const float* b_dscale, int64_t ld_bs,
+                         const void* bias, pf8_dtype btype, pf8_activation activation, int gated,
+                         const void* residual, int64_t ldr, void* z, int64_t ldz, void* d, int64_t ldd,
+                         void* hip_stream) {
+  if (!a || !a_dscale || !b || !b_dscale || !d || m <= 0 || n <= 0 || k <= 0) return PF8_EINVAL;
+  if ((btype != PF8_BF16 && btype != PF8_F32) || (gated != 0 && gated != 1)) return PF8_EINVAL;
+  if (activation < PF8_ACT_NONE || activation > PF8_ACT_GELU_TANH || (gated && activation == PF8_ACT_NONE))
+    return PF8_EINVAL;
+  if (any_too_big(m, n, k, lda, ld_as, ldb, ld_bs, residual ? ldr : 0, z ? ldz : 0, ldd)) return PF8_ESHAPE;
+  if (k % 128 != 0 || (gated && n % 128 != 0)) return PF8_ESHAPE;
+  const int64_t cols = gated ? n / 2 : n;
+  if (lda < k || ldb < k || ld_as < m || ld_bs < k / 128 || ldd < cols || (residual && ldr < cols) || (z && ldz < n))
+    return PF8_EINVAL;
+  if (lda > pf8::kMaxTilePitch || ldb > pf8::kMaxTilePitch || ldd > pf8::kMaxTilePitch / 2 ||
+      (residual && ldr > pf8::kMaxTilePitch / 2) || (z && ldz > pf8::kMaxTilePitch / 2))
+    return PF8_ESHAPE;
+  if ((m + 63) / 64 > 65535 * int64_t{64}) return PF8_ESHAPE;
+  if (!aligned(a, 16) || !aligned(b, 16) || lda % 16 || ldb % 16 || !aligned(a_dscale, 4) || !aligned(b_dscale, 4) ||
+      !aligned(bias, btype == PF8_F32 ? 4 : 2) || !aligned(d, 16) || ldd % 8 || !aligned(residual, 16) ||
+      (residual && ldr % 8) || !aligned(z, 16) || (z && ldz % 8))
+    return PF8_EALIGN;
+  if (int e = device_status()) return e;
+  const pf8::FpropActArgs args{m, n, k, static_cast<const uint8_t*>(a), lda, a_dscale, ld_as,
+                               static_cast<const uint8_t*>(b), ldb, b_dscale, ld_bs, bias, btype == PF8_F32, activation,
+                               gated, static_cast<const uint16_t*>(residual), ldr, static_cast<uint16_t*>(z), ldz,
+                               static_cast<uint16_t*>(d), ldd};
+  return launch_status(pf8::launch_fprop_act(args, static_cast<hipStream_t>(hip_stream)));
+}
+
 }  // extern "C"

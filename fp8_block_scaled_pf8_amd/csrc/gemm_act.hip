@@ -1,0 +1,163 @@
+// Block-scaled FP8 product with bias, activation and residual in its epilogue (gfx950). Formulas in
+// include/pf8_layer.h.
+#include "act_device.h"
+#include "gemm_device.h"
+#include "pf8_layer_launch.h"
+#include "row_device.h"
+
+namespace pf8 {
+
+namespace {
+
+__device__ __forceinline__ float act_any(int act, float z) {
+  switch (act) {
+    case PF8_ACT_RELU: return act_value<PF8_ACT_RELU>(z);
+    case PF8_ACT_RELU2: return act_value<PF8_ACT_RELU2>(z);
+    case PF8_ACT_SILU: return act_value<PF8_ACT_SILU>(z);
+    case PF8_ACT_GELU: return act_value<PF8_ACT_GELU>(z);
+    case PF8_ACT_GELU_TANH: return act_value<PF8_ACT_GELU_TANH>(z);
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float bias_at(const FpropActArgs& p, int64_t j) {
+  return p.bias_f32 ? static_cast<const float*>(p.bias)[j] : bf_lo(static_cast<const uint16_t*>(p.bias)[j]);
+}
+
+// Few tokens. A workgroup of 8 waves owns 16 columns of d (and the 16 or 32 rows of W that make them) for up to
+// 16 MT tokens; its waves take the 128-wide K blocks in turn, each with its own loads straight into registers: no
+// row of W is read by two waves, so LDS would only be a detour. One v_mfma_f32_16x16x128_f8f6f4 covers a K block of 16
+// rows of W and 16 tokens; its partial is scaled into the wave's FP32 sum. The eight sums meet in LDS, added in
+// the waves' order.
+template <int MT, bool GATED>
+__global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
+  constexpr int WAVES = 8, PARTS = GATED ? 2 : 1, U = MT == 4 ? 2 : 4;  // U: K blocks whose loads go out together
+  __shared__ v4f red[WAVES][PARTS][MT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, quarter = lane >> 4;
+  const int64_t cols = GATED ? p.n / 2 : p.n;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t m0 = (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * 16 * MT;
+  if (m0 >= p.m) return;
+  const int nk = static_cast<int>(p.k / kGroup);
+  const uint8_t* w[PARTS];
+  const float* sw[PARTS];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    const int64_t first = n0 + i * cols;
+    w[i] = p.b + (i * cols + min64(n0 + l16, cols - 1)) * p.ldb + quarter * 32;
+    sw[i] = p.b_dscale + (first >> 7) * p.ld_bs;
+  }
+  const uint8_t* x[MT];
+  const float* sx[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int64_t row = min64(m0 + 16 * t + l16, p.m - 1);
+    x[t] = p.a + row * p.lda + quarter * 32;
+    sx[t] = p.a_dscale + row;
+  }
+  v4f acc[PARTS][MT];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[i][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int kb = wave; kb < nk; kb += WAVES * U) {
+    v8i fw[U][PARTS], fx[U][MT];
+    float a[U][MT], b[U][PARTS];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = min(kb + u * WAVES, nk - 1);
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i) {
+        fw[u][i] = lds_read32(w[i] + at * kGroup, 0, 16);
+        b[u][i] = sw[i][at];
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        fx[u][t] = lds_read32(x[t] + at * kGroup, 0, 16);
+        a[u][t] = sx[t][at * p.ld_as];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb + u * WAVES >= nk) break;
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[u][i], fx[u][t], zero, 0, 0, 0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][t][r] = __builtin_fmaf(part[r], a[u][t] * b[u][i], acc[i][t][r]);
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) red[wave][i][t][lane] = acc[i][t];
+  __syncthreads();
+  // a thread takes 4 consecutive columns of a token
+  const int t = threadIdx.x >> 6;
+  if (t >= MT) return;
+  const int64_t m = m0 + 16 * t + l16, n = n0 + 4 * quarter;
+  if (m >= p.m || n >= cols) return;
+  const int left = static_cast<int>(min64(4, cols - n));
+  float v[PARTS][4];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    v4f s = red[0][i][t][lane];
+#pragma unroll
+    for (int g = 1; g < WAVES; ++g) s += red[g][i][t][lane];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[i][r] = s[r];
+    if (p.bias) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < left) v[i][r] += bias_at(p, i * cols + n + r);
+    }
+  }
+  auto store = [&](uint16_t* out, const float (&f)[4]) {
+    const uint32_t w0 = pack2(f[0], f[1]), w1 = pack2(f[2], f[3]);
+    if (left == 4) {
+      *reinterpret_cast<u64_a2*>(out) = u64_a2{w0, w1};
+      return;
+    }
+    out[0] = static_cast<uint16_t>(w0);
+    if (left > 1) out[1] = static_cast<uint16_t>(w0 >> 16);
+    if (left > 2) out[2] = static_cast<uint16_t>(w1);
+  };
+  if (p.z) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) store(p.z + m * p.ldz + i * cols + n, v[i]);
+  }
+  float d[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    d[r] = act_any(p.act, v[0][r]);
+    if constexpr (GATED) d[r] *= v[PARTS - 1][r];
+    if (p.residual && r < left) d[r] += bf_lo(p.residual[m * p.ldr + n + r]);
+  }
+  store(p.d + m * p.ldd + n, d);
+}
+
+}  // namespace
+
+template <int MT>
+static hipError_t launch_few(const FpropActArgs& a, hipStream_t stream) {
+  const int64_t cols = a.gated ? a.n / 2 : a.n, rows = (a.m + 16 * MT - 1) / (16 * MT);
+  const int64_t high = rows < 32768 ? rows : 32768;
+  const dim3 grid(static_cast<uint32_t>((cols + 15) / 16), static_cast<uint32_t>(high),
+                  static_cast<uint32_t>((rows + high - 1) / high));
+  if (a.gated) hipLaunchKernelGGL((fprop_act_few_kernel<MT, true>), grid, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((fprop_act_few_kernel<MT, false>), grid, dim3(512), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_fprop_act(const FpropActArgs& a, hipStream_t stream) {
+  if (a.m <= 16) return launch_few<1>(a, stream);
+  if (a.m <= 32) return launch_few<2>(a, stream);
+  return launch_few<4>(a, stream);
+}
+
+}  // namespace pf8

@@ -63,4 +63,28 @@ struct ActBwdArgs {
 hipError_t launch_act_bwd(const ActBwdArgs& args, float* dbias, int accumulate, hipStream_t stream);
 int64_t act_bwd_groups(int64_t rows, int64_t cols, int gated);
 
+// The forward product with its epilogue; d is [m, gated ? n / 2 : n].
+struct FpropActArgs {
+  int64_t m, n, k;
+  const uint8_t* a;
+  int64_t lda;
+  const float* a_dscale;
+  int64_t ld_as;
+  const uint8_t* b;
+  int64_t ldb;
+  const float* b_dscale;
+  int64_t ld_bs;
+  const void* bias;  // or null
+  int bias_f32;
+  int act, gated;
+  const uint16_t* residual;  // or null
+  int64_t ldr;
+  uint16_t* z;  // or null
+  int64_t ldz;
+  uint16_t* d;
+  int64_t ldd;
+};
+
+hipError_t launch_fprop_act(const FpropActArgs& args, hipStream_t stream);
+
 }  // namespace pf8

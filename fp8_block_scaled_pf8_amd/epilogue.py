@@ -8,12 +8,13 @@ has the details.
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional
+from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
 from . import _lib as L
 from .norm import _call, _may_write, _rows, _rows_at, _rows_meet, _vector
+from .ops import GROUP, out_pitch
 
 Tensor = torch.Tensor
 
@@ -34,6 +35,107 @@ def _activation(activation: Optional[str], gated: bool) -> int:
     if gated and not code:
         raise ValueError("a gated product needs an activation for its gate")
     return code
+
+
+def _aligned_rows(t: Tensor, name: str, shape, device) -> Tuple[int, int]:
+    """(address, pitch) of a bf16 matrix that the product's epilogue reads or writes 16 bytes at a time."""
+    p, ld = _rows(t, name, shape, device)
+    if shape[0] == 1:
+        ld = -(-shape[1] // 8) * 8
+    if p % 16 or ld % 8:
+        raise ValueError(f"{name} must be 16-byte aligned with a row pitch of a multiple of 8")
+    return p, ld
+
+
+def _codes(t: Tensor, name: str) -> Tuple[int, int]:
+    if not isinstance(t, Tensor) or t.dim() != 2 or t.dtype != torch.uint8:
+        raise TypeError(f"{name} must be a 2-D uint8 tensor of codes")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a HIP device")
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 or rows > 1 and ld < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), cols if rows == 1 else ld
+
+
+def _scales(t: Tensor, name: str, rows: int, cols: int, device) -> Tuple[int, int]:
+    if not isinstance(t, Tensor) or t.dtype != torch.float32 or t.dim() != 2:
+        raise TypeError(f"{name} must be a 2-D float32 tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape[0] < rows or t.shape[1] < cols:
+        raise ValueError(f"{name} must cover [{rows}, {cols}], got {tuple(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1 or rows > 1 and ld < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), max(ld, cols)
+
+
+def _new_result(rows: int, cols: int, device) -> Tuple[Tensor, int, int]:
+    """A bf16 result in rows of 16 bytes or a multiple of it (a view of a wider buffer where cols asks for it)."""
+    pitch = out_pitch(cols, 2) if rows > 1 else -(-cols // 8) * 8
+    t = torch.empty((rows, pitch), dtype=torch.bfloat16, device=device)
+    return (t if pitch == cols else t[:, :cols]), t.data_ptr(), pitch
+
+
+def fprop_act(qx: Tensor, sx: Tensor, qw: Tensor, sw: Tensor, bias: Optional[Tensor] = None,
+              activation: Optional[str] = None, gated: bool = False, residual: Optional[Tensor] = None,
+              save_z: bool = False, out: Optional[Tensor] = None, z_out: Optional[Tensor] = None
+              ) -> Union[Tensor, Tuple[Tensor, Tensor]]:
+    """d = act(X W^T + bias) + residual from X's row-mode codes and W's tile codes, as ``fprop`` takes them.
+
+    ``gated``: the first half of W's rows makes the gate g, the second u, and d = act(g) * u + residual has half
+    the columns; W's rows are then a multiple of 128. bias is bf16 or float32 [rows of W], residual bf16 of d's
+    shape. d is bf16, and so is z = X W^T + bias, which ``act_backward`` takes: returned as (d, z) with ``save_z`` or
+    z_out. out may be residual itself. No tokens: empty results.
+    """
+    pa, lda = _codes(qx, "qx")
+    pb, ldb = _codes(qw, "qw")
+    dev = qx.device
+    (m, k), n = qx.shape, qw.shape[0]
+    if qw.shape[1] != k:
+        raise ValueError(f"reduction dims differ: qx {tuple(qx.shape)}, qw {tuple(qw.shape)}")
+    if qw.device != dev:
+        raise ValueError(f"qw must be on {dev}, got {qw.device}")
+    if k < GROUP or k % GROUP:
+        raise ValueError(f"the reduction dimension must be a multiple of {GROUP}, got {k}")
+    if n < 1:
+        raise ValueError("qw must have at least one row")
+    code = _activation(activation, gated)
+    if gated and n % GROUP:
+        raise ValueError(f"a gated product needs a multiple of {GROUP} weight rows, got {n}")
+    pas, ld_as = _scales(sx, "sx", k // GROUP, m, dev)
+    pbs, ld_bs = _scales(sw, "sw", -(-n // GROUP), k // GROUP, dev)
+    cols = n // 2 if gated else n
+    pbias, btype = 0, L.PF8_BF16
+    if bias is not None:
+        if bias.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"bias must be bfloat16 or float32, got {bias.dtype}")
+        pbias = _vector(bias, "bias", n, bias.dtype, dev)
+        btype = L.PF8_F32 if bias.dtype == torch.float32 else L.PF8_BF16
+    shape = torch.Size((m, cols))
+    pr = ldr = pz = ldz = 0
+    if residual is not None:
+        pr, ldr = _aligned_rows(residual, "residual", shape, dev)
+    if out is None:
+        out, pd, ldd = _new_result(m, cols, dev)
+    else:
+        pd, ldd = _aligned_rows(out, "out", shape, dev)
+        if m:
+            _may_write(out, "out", [(residual, True), (qx, False), (qw, False), (sx, False), (sw, False), (bias, False),
+                                    (z_out, False)])
+    z = z_out
+    if z is not None:
+        pz, ldz = _aligned_rows(z, "z_out", torch.Size((m, n)), dev)
+        if m:
+            _may_write(z, "z_out", [(t, False) for t in (residual, qx, qw, sx, sw, bias)])
+    elif save_z:
+        z, pz, ldz = _new_result(m, n, dev)
+    if m:
+        _call(L.pf8_fprop_act, dev, m, n, k, pa, lda, pas, ld_as, pb, ldb, pbs, ld_bs, pbias, btype, code, int(gated), pr,
+              ldr, pz, ldz, pd, ldd)
+    return out if z is None else (out, z)
 
 
 def act_backward(dd: Tensor, z: Optional[Tensor], activation: Optional[str], gated: bool = False,

@@ -1,7 +1,7 @@
 /*
  * pf8_layer.h - C ABI of a decoder layer's steps around its FP8 products (same library, libpf8): the
- * norms of queries and keys for each head with the rotation by positions, and its backward pass; the
- * backward pass of activations.
+ * norms of queries and keys for each head with the rotation by positions, the product with bias,
+ * activation and residual in its epilogue, and the backward passes of both.
  *
  * The conventions of pf8.h and pf8_train.h hold: device pointers owned by the caller, validation on the
  * host before anything is enqueued, nothing allocated or kept. Pointers that are host pointers say so.
@@ -126,6 +126,31 @@ pf8_status pf8_act_bwd(int64_t rows, int64_t cols, const void* dd, int64_t lddd,
 
 /* Bytes of the workspace of pf8_act_bwd; 0 for sizes that it refuses. Needs no device. */
 int64_t pf8_act_bwd_workspace(int64_t rows, int64_t cols, int gated);
+
+/*
+ * Block-scaled FP8 product with bias, activation and residual in its epilogue:
+ *
+ *   z = (the forward product of pf8_block_gemm, PF8_FPROP) + bias       in FP32
+ *   d = act(z) + residual                                               gated = 0: d [m, n]
+ *   d = act(z[:, :n/2]) * z[:, n/2:] + residual                         gated = 1: d [m, n/2]
+ *
+ * d and z are each rounded to BF16 once, from FP32.
+ *
+ * Operands, scales, alignment and limits are those of pf8_block_gemm with PF8_FPROP (m, n >= 1,
+ * k % 128 == 0, power-of-two scales; b_dscale[(j / 128) * ld_bs + kb], ld_bs >= k / 128), and its accumulation
+ * contract holds for z before its rounding. Up to 64 rows the sum over K is formed in parts, joined in a fixed order;
+ * the same call gives the same bits each time.
+ * gated: 0 or 1; with 1, n is a multiple of 128 and the activation is not PF8_ACT_NONE.
+ * bias: [n] of btype (PF8_BF16 or PF8_F32), or NULL.
+ * residual: bf16, d's shape, pitch ldr, or NULL. May be d itself (same address and pitch).
+ * z: bf16 [m, n], pitch ldz, what pf8_act_bwd takes; or NULL: not wanted. Overlaps nothing.
+ * d, z and residual: 16-byte aligned, pitches multiples of 8.
+ */
+pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* a_dscale,
+                         int64_t ld_as, const void* b, int64_t ldb, const float* b_dscale, int64_t ld_bs,
+                         const void* bias, pf8_dtype btype, pf8_activation activation, int gated,
+                         const void* residual, int64_t ldr, void* z, int64_t ldz, void* d, int64_t ldd,
+                         void* hip_stream);
 
 #ifdef __cplusplus
 }

@@ -139,8 +139,39 @@ def test_act_refuses(kw, want):
 def test_act_workspace():
     f = L.pf8_act_bwd_workspace
     assert f(1, 1, 0) > 0 and f(100, 64, 1) == 2 * f(100, 64, 0)
-    for bad in ((0, 1, 0), (1, 0, 0), (1, 1, 2), (BIG, 1, 0), (1, BIG, 0), (1, BIG // 2, 0)):
+    for bad in ((0, 1, 0), (1, 0, 0), (1, 1, 2), (BIG, 1, 0), (1, BIG, 0), (1, BIG // 2, 1)):
         assert f(*bad) == 0
     if not _gpu():
         assert _act() == L.PF8_ENODEV
         assert _act(z=0, act=0, gated=0, dz=0) == L.PF8_ENODEV
+
+
+def _prod(**kw):
+    a = dict(m=8, n=256, k=256, a=P[0], lda=256, a_ds=P[1], ld_as=8, b=P[2], ldb=256, b_ds=P[3], ld_bs=2, bias=P[4], btype=0,
+             act=3, gated=1, residual=P[5], ldr=128, z=P[6], ldz=256, d=P[7], ldd=128)
+    a.update(kw)
+    return L.pf8_fprop_act(*a.values(), 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(m=0), "EINVAL"), (dict(n=-1), "EINVAL"), (dict(k=0), "EINVAL"), (dict(a=0), "EINVAL"), (dict(a_ds=0), "EINVAL"),
+    (dict(b=0), "EINVAL"), (dict(b_ds=0), "EINVAL"), (dict(d=0), "EINVAL"), (dict(btype=2), "EINVAL"), (dict(gated=2), "EINVAL"),
+    (dict(act=-1), "EINVAL"), (dict(act=6), "EINVAL"), (dict(act=0), "EINVAL"), (dict(lda=255), "EINVAL"),
+    (dict(ldb=255), "EINVAL"), (dict(ld_as=7), "EINVAL"), (dict(ld_bs=1), "EINVAL"), (dict(ldd=127), "EINVAL"),
+    (dict(ldr=127), "EINVAL"), (dict(ldz=255), "EINVAL"), (dict(gated=0), "EINVAL"), (dict(k=192), "ESHAPE"),
+    (dict(n=192), "ESHAPE"), (dict(m=BIG, ld_as=BIG), "ESHAPE"), (dict(lda=1 << 24), "ESHAPE"), (dict(ldd=1 << 23), "ESHAPE"),
+    (dict(ldz=1 << 23), "ESHAPE"), (dict(ldr=1 << 23), "ESHAPE"), (dict(ldz=BIG), "ESHAPE"),
+    (dict(a=P[0] + 8), "EALIGN"), (dict(b=P[2] + 8), "EALIGN"), (dict(lda=264), "EALIGN"), (dict(ldb=264), "EALIGN"),
+    (dict(a_ds=P[1] + 2), "EALIGN"), (dict(b_ds=P[3] + 2), "EALIGN"), (dict(bias=P[4] + 1), "EALIGN"),
+    (dict(bias=P[4] + 2, btype=1), "EALIGN"), (dict(d=P[7] + 8), "EALIGN"), (dict(ldd=132), "EALIGN"),
+    (dict(residual=P[5] + 8), "EALIGN"), (dict(ldr=132), "EALIGN"), (dict(z=P[6] + 8), "EALIGN"), (dict(ldz=260), "EALIGN"),
+])
+def test_product_refuses(kw, want):
+    assert _prod(**kw) == _status(want)
+
+
+def test_product_takes():
+    if not _gpu():
+        for kw in (dict(), dict(bias=0), dict(residual=0, ldr=0), dict(z=0, ldz=0), dict(act=0, gated=0, n=128, ldz=128),
+                   dict(residual=P[7])):
+            assert _prod(**kw) == L.PF8_ENODEV
