@@ -6,6 +6,8 @@
 #include <type_traits>
 
 #include "../../include/pf8_layer.h"
+#include "pf8_layer_launch.h"
+#include "row_device.h"
 
 namespace pf8 {
 
@@ -24,12 +26,34 @@ __device__ __forceinline__ float tanh_argument2(float& z) {
   return 2.0f * kTanhScale * z * __builtin_fmaf(kTanhCube * z, z, 1.0f);
 }
 
+// The normal distribution Phi(z) = (1 + erf(z / sqrt 2)) / 2, and e = exp(-z^2 / 2). Below zero Phi = e h(|z|) with
+// h(a) = exp(a^2 / 2) Phi(-a), a smooth function that falls as 1 / a: h(a) = t P(t), t = 1 / (1 + 0.3 a), with P of
+// degree 7 fitted for the least relative error on 0 .. 14 (1.5e-7, in FP32 5e-7; beyond, e vanishes). No difference of
+// near values below zero, one minus that above. 16 instructions with two slow ones; erff takes some 50.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170368f);
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, __builtin_fabsf(z), 1.0f));
+  float p = 0.035674771606f;
+  p = __builtin_fmaf(p, t, -0.157203072659f);
+  p = __builtin_fmaf(p, t, 0.206353490033f);
+  p = __builtin_fmaf(p, t, -0.053683630295f);
+  p = __builtin_fmaf(p, t, 0.128561619854f);
+  p = __builtin_fmaf(p, t, 0.099913493968f);
+  p = __builtin_fmaf(p, t, 0.120753955764f);
+  p = __builtin_fmaf(p, t, 0.119629298845f);
+  const float q = e * t * p;
+  return z > 0.0f ? 1.0f - q : q;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == PF8_ACT_RELU) return z <= 0.0f ? 0.0f : z;  // NaN stays NaN
   if constexpr (ACT == PF8_ACT_RELU2) return z <= 0.0f ? 0.0f : z * z;
   if constexpr (ACT == PF8_ACT_SILU) return z * sigmoid(z);
-  if constexpr (ACT == PF8_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752440f));
+  if constexpr (ACT == PF8_ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
   if constexpr (ACT == PF8_ACT_GELU_TANH) {
     float y = z;
     return z * sigmoid(tanh_argument2(y));
@@ -51,10 +75,10 @@ __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
     value = z * s;
     slope = s * __builtin_fmaf(z, 1.0f - s, 1.0f);
   } else if constexpr (ACT == PF8_ACT_GELU) {
-    const float p = 0.5f * (1.0f + erff(z * 0.70710678118654752440f));
-    const float density = 0.39894228040143267794f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170368f);
+    float e;
+    const float p = normal_cdf(z, e);
     value = z * p;
-    slope = __builtin_fmaf(z, density, p);
+    slope = __builtin_fmaf(z * 0.39894228040143267794f, e, p);
   } else if constexpr (ACT == PF8_ACT_GELU_TANH) {
     float y = z;
     const float s = sigmoid(tanh_argument2(y));
@@ -64,6 +88,11 @@ __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
     value = z;
     slope = 1.0f;
   }
+}
+
+// Element j of a product's bias.
+__device__ __forceinline__ float bias_at(const FpropActArgs& p, int64_t j) {
+  return p.bias_f32 ? static_cast<const float*>(p.bias)[j] : bf_lo(static_cast<const uint16_t*>(p.bias)[j]);
 }
 
 // Calls f with the activation as an integral constant.

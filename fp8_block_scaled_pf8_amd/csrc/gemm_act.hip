@@ -20,14 +20,10 @@ __device__ __forceinline__ float act_any(int act, float z) {
   }
 }
 
-__device__ __forceinline__ float bias_at(const FpropActArgs& p, int64_t j) {
-  return p.bias_f32 ? static_cast<const float*>(p.bias)[j] : bf_lo(static_cast<const uint16_t*>(p.bias)[j]);
-}
-
-// Few tokens. A workgroup of 8 waves owns 16 columns of d (and the 16 or 32 rows of W that make them) for up to
-// 16 MT tokens; its waves take the 128-wide K blocks in turn, each with its own loads straight into registers: no
+// Few tokens. A workgroup of 8 waves owns 16 columns of d (and the 16 or 32 rows of W that make them) for up
+// to 16 MT tokens; its waves take the 128-wide K blocks in turn, each with its own loads straight into registers: no
 // row of W is read by two waves, so LDS would only be a detour. One v_mfma_f32_16x16x128_f8f6f4 covers a K block of 16
-// rows of W and 16 tokens; its partial is scaled into the wave's FP32 sum. The eight sums meet in LDS, added in
+// rows of W and 16 tokens; its partial is scaled into the wave's FP32 sum. The waves' sums meet in LDS, added in
 // the waves' order.
 template <int MT, bool GATED>
 __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
@@ -37,8 +33,6 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   const int l16 = lane & 15, quarter = lane >> 4;
   const int64_t cols = GATED ? p.n / 2 : p.n;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const int64_t m0 = (static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y) * 16 * MT;
-  if (m0 >= p.m) return;
   const int nk = static_cast<int>(p.k / kGroup);
   const uint8_t* w[PARTS];
   const float* sw[PARTS];
@@ -52,7 +46,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   const float* sx[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int64_t row = min64(m0 + 16 * t + l16, p.m - 1);
+    const int64_t row = min64(16 * t + l16, p.m - 1);
     x[t] = p.a + row * p.lda + quarter * 32;
     sx[t] = p.a_dscale + row;
   }
@@ -67,7 +61,8 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
     float a[U][MT], b[U][PARTS];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = min(kb + u * WAVES, nk - 1);
+      const int at = kb + u * WAVES;
+      if (at >= nk) break;
 #pragma unroll
       for (int i = 0; i < PARTS; ++i) {
         fw[u][i] = lds_read32(w[i] + at * kGroup, 0, 16);
@@ -100,7 +95,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   // a thread takes 4 consecutive columns of a token
   const int t = threadIdx.x >> 6;
   if (t >= MT) return;
-  const int64_t m = m0 + 16 * t + l16, n = n0 + 4 * quarter;
+  const int64_t m = 16 * t + l16, n = n0 + 4 * quarter;
   if (m >= p.m || n >= cols) return;
   const int left = static_cast<int>(min64(4, cols - n));
   float v[PARTS][4];
@@ -145,19 +140,56 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
 
 template <int MT>
 static hipError_t launch_few(const FpropActArgs& a, hipStream_t stream) {
-  const int64_t cols = a.gated ? a.n / 2 : a.n, rows = (a.m + 16 * MT - 1) / (16 * MT);
-  const int64_t high = rows < 32768 ? rows : 32768;
-  const dim3 grid(static_cast<uint32_t>((cols + 15) / 16), static_cast<uint32_t>(high),
-                  static_cast<uint32_t>((rows + high - 1) / high));
-  if (a.gated) hipLaunchKernelGGL((fprop_act_few_kernel<MT, true>), grid, dim3(512), 0, stream, a);
-  else hipLaunchKernelGGL((fprop_act_few_kernel<MT, false>), grid, dim3(512), 0, stream, a);
+  const dim3 grid(static_cast<uint32_t>(((a.gated ? a.n / 2 : a.n) + 15) / 16)), block(512);
+  if (a.gated) hipLaunchKernelGGL((fprop_act_few_kernel<MT, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((fprop_act_few_kernel<MT, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
+// Modelled times in microseconds, from sweeps of 1 to 8192 rows over weights of 12288 x 2048 (gated and not), 2048 x
+// 6144, 2048 x 2048, 1000 x 1536 and 6144 x 6144 (gated); what the models choose was within 8 % of the best
+// choice, but for a few sizes next to a border. As an example, 64 rows on 2048 x 6144: 17.2 us by the kernel for few
+// tokens, 15.9 by 64 x 64 tiles, 21.9 by 128 x 128; 32 rows: 11.3 and the same.
+
+// Few tokens: a start, then K blocks of each workgroup, whose tokens' operands every workgroup loads anew; more
+// workgroups than CUs share the memory's rate.
+static double few_cost(const FpropActArgs& a) {
+  const double rows = static_cast<double>(a.n) / 16 / 256;
+  return 3.0 + (rows > 1.0 ? rows : 1.0) * static_cast<double>(a.k) / 1024 * (0.5 + 0.03 * static_cast<double>(a.m));
+}
+
+// Tiles of one shape: a start, then rounds of one tile on each of 256 CUs, each of them by K and with its own end. A
+// round that fills the card takes longer than a tile alone (clock, L2).
+struct TileCost {
+  int bm, bn;
+  double start, alone, full, end;  // alone, full: for 1024 of K
+  double operator()(const FpropActArgs& a) const {
+    const int64_t out = a.gated ? bn / 2 : bn, cols = a.gated ? a.n / 2 : a.n;
+    const int64_t tiles = (a.m + bm - 1) / bm * ((cols + out - 1) / out), rounds = (tiles + 255) / 256;
+    const double fill = tiles < 256 ? static_cast<double>(tiles) / 256 : 1.0;
+    return start + static_cast<double>(rounds) * ((alone + (full - alone) * fill) * static_cast<double>(a.k) / 1024 + end);
+  }
+};
+
 hipError_t launch_fprop_act(const FpropActArgs& a, hipStream_t stream) {
-  if (a.m <= 16) return launch_few<1>(a, stream);
-  if (a.m <= 32) return launch_few<2>(a, stream);
-  return launch_few<4>(a, stream);
+  constexpr TileCost kShapes[] = {{256, 256, 7.0, 8.1, 12.2, 3.0},
+                                  {256, 128, 7.0, 4.4, 8.0, 1.0},
+                                  {128, 128, 6.0, 2.65, 4.7, 0.0},
+                                  {64, 64, 4.0, 2.0, 2.1, 0.1}};
+  int best = 0;
+  double cost[4];
+  for (int i = 0; i < 4; ++i) {
+    cost[i] = kShapes[i](a);
+    if (cost[i] < cost[best]) best = i;
+  }
+  if (a.m <= 64 && few_cost(a) < cost[best])
+    return a.m <= 16 ? launch_few<1>(a, stream) : a.m <= 32 ? launch_few<2>(a, stream) : launch_few<4>(a, stream);
+  switch (best) {
+    case 0: return launch_fprop_act_tiles<256, 256>(a, stream);
+    case 1: return launch_fprop_act_tiles<256, 128>(a, stream);
+    case 2: return launch_fprop_act_tiles<128, 128>(a, stream);
+    default: return launch_fprop_act_tiles<64, 64>(a, stream);
+  }
 }
 
 }  // namespace pf8

@@ -86,5 +86,8 @@ struct FpropActArgs {
 };
 
 hipError_t launch_fprop_act(const FpropActArgs& args, hipStream_t stream);
+// By tiles of BM rows and BN rows of W.
+template <int BM, int BN>
+hipError_t launch_fprop_act_tiles(const FpropActArgs& args, hipStream_t stream);
 
 }  // namespace pf8
