@@ -42,7 +42,7 @@ from ._lib import (
 from .epilogue import ActGrads, act_backward, fprop_act
 from .heads import (QKNormRope, QKNormRopeFunction, QKNormRopeGrads, fp8_qk_norm_rope, qk_norm_rope,
                     qk_norm_rope_backward)
-from .linear import Fp8Linear, Fp8LinearFunction, fp8_linear
+from .linear import Fp8Linear, Fp8LinearActFunction, Fp8LinearFunction, fp8_linear, fp8_linear_act
 from .norm import (BlockNorm, BlockNormFunction, BlockNormGrads, block_norm, block_norm_backward, block_norm_quant,
                    fp8_block_norm)
 from .orthogonal import newton_schulz
@@ -55,7 +55,7 @@ __all__ = [
     "pf8_abi_version", "pf8_block_gemm", "pf8_block_gemm_f32", "pf8_block_gemm_variant", "pf8_gemm_bf16", "pf8_quant_act_1x128", "pf8_quant_act_dual",
     "pf8_quant_fwd", "pf8_quant_w_128x128", "pf8_strerror",
     "LinearStep", "block_gemm", "block_gemm_f32", "dgrad", "fprop", "gemm_bf16", "quant_act_1x128", "quant_act_dual",
-    "quant_w_128x128", "wgrad", "wgrad_f32", "Fp8Linear", "Fp8LinearFunction", "fp8_linear",
+    "quant_w_128x128", "wgrad", "wgrad_f32", "Fp8Linear", "Fp8LinearActFunction", "Fp8LinearFunction", "fp8_linear", "fp8_linear_act",
     "PF8_BF16", "PF8_F32", "pf8_block_norm", "pf8_block_norm_bwd", "pf8_block_norm_bwd_workspace",
     "BlockNorm", "BlockNormFunction", "BlockNormGrads", "block_norm", "block_norm_backward", "block_norm_quant",
     "fp8_block_norm", "pf8_newton_schulz", "pf8_newton_schulz_workspace", "newton_schulz",

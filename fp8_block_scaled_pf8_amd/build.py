@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
@@ -43,28 +45,43 @@ def lib_path() -> str:
     return os.path.join(PKG_DIR, LIB_NAME)
 
 
+def _jobs() -> int:
+    """Compilers at once: MAX_JOBS where it is set, else the CPUs of this process, 16 at most."""
+    if os.environ.get("MAX_JOBS", "").isdigit():
+        return max(1, int(os.environ["MAX_JOBS"]))
+    return min(16, len(os.sched_getaffinity(0)))
+
+
 def build(asm_dir: "str | None" = None, verbose: bool = False) -> str:
-    """Compile every source for gfx950 and link libpf8.so next to this file. Returns its path."""
+    """Compile every source for gfx950, side by side, and link libpf8.so next to this file. Returns its path."""
     cc = hipcc()
     out = lib_path()
     tmp = out + ".tmp"
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    cmd = [cc, *HIPCC_FLAGS, "-shared", "-o", tmp, *srcs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    errs = [ln for ln in (res.stderr or "").splitlines() if "packed-fp32-ops" not in ln]
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(errs))
-    if verbose and errs:
-        print("\n".join(errs), file=sys.stderr)
-    os.replace(tmp, out)
     if asm_dir:
         os.makedirs(asm_dir, exist_ok=True)
-        for s in srcs:
-            base = os.path.splitext(os.path.basename(s))[0]
-            subprocess.run([cc, *HIPCC_FLAGS, "--cuda-device-only", "-S", "-o", os.path.join(asm_dir, base + ".s"), s],
-                           check=True, capture_output=True)
+
+    def run(args):
+        cmd = [cc, *HIPCC_FLAGS, *args]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        errs = [ln for ln in (res.stderr or "").splitlines() if "packed-fp32-ops" not in ln]
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(errs))
+        if verbose and errs:
+            print("\n".join(errs), file=sys.stderr)
+
+    with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(_jobs()) as pool:
+        objects, work = [], []
+        for source in SOURCES:
+            src, base = os.path.join(CSRC, source), os.path.splitext(source)[0]
+            objects.append(os.path.join(objs, base + ".o"))
+            work.append(["-c", "-o", objects[-1], src])
+            if asm_dir:
+                work.append(["--cuda-device-only", "-S", "-o", os.path.join(asm_dir, base + ".s"), src])
+        list(pool.map(run, work))
+        run(["-shared", "-o", tmp, *objects])
+    os.replace(tmp, out)
     return out
 
 
