@@ -174,7 +174,7 @@ int64_t pf8_act_bwd_workspace(int64_t rows, int64_t cols, int gated) {
   if (rows <= 0 || cols <= 0 || (gated != 0 && gated != 1) || any_too_big(rows, cols) ||
       any_too_big((gated ? 2 : 1) * cols))
     return 0;
-  return pf8::act_bwd_groups(rows, cols, gated) * (gated ? 2 : 1) * cols * 4;
+  return pf8::act_bwd_groups(rows, cols) * (gated ? 2 : 1) * cols * 4;
 }
 
 pf8_status pf8_act_bwd(int64_t rows, int64_t cols, const void* dd, int64_t lddd, const void* z, int64_t ldz,

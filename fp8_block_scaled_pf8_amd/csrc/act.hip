@@ -2,7 +2,7 @@
 //
 // Bound: HBM. 6 bytes a value of dd without a gate (dd, z in, dz out), 10 with one.
 // A thread keeps 8 columns and walks rows; a workgroup is as many threads wide as the columns ask for (up
-// to 256, 2048 columns), the rest of its 256 threads take further rows. Column sums stay in registers over
+// to 256), the rest of its 256 threads take further rows. Column sums stay in registers over
 // a thread's rows, meet in LDS, and a workgroup writes one row of partial sums.
 #include "act_device.h"
 #include "pf8_layer_launch.h"
@@ -46,38 +46,50 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int wide) {
   constexpr int PARTS = GATED ? 2 : 1;
   constexpr bool HAS_Z = ACT != PF8_ACT_NONE;
   float sums[PARTS][8] = {};
+  // ROWS rows at a time, all their loads first
+  constexpr int ROWS = GATED ? 2 : 4;
   const int64_t step = static_cast<int64_t>(gridDim.y) * high;
-  for (int64_t row = static_cast<int64_t>(blockIdx.y) * high + ty; any && row < a.rows; row += step) {
-    float d[8], z[8], o[8];
-    const uint4 dv = load(a.dd + row * a.lddd);
-    uint4 zv, uv;
-    if constexpr (HAS_Z) zv = load(a.z + row * a.ldz);
-    if constexpr (GATED) uv = load(a.z + row * a.ldz + cols);
-    unpack8(dv, d);
-    if constexpr (HAS_Z) unpack8(zv, z);
-    if constexpr (GATED) {
-      float u[8], up[8];
-      unpack8(uv, u);
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * high + ty; any && r0 < a.rows; r0 += ROWS * step) {
+    uint4 dv[ROWS], zv[ROWS], uv[ROWS];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float value, slope;
-        act_both<ACT>(z[k], value, slope);
-        o[k] = d[k] * u[k] * slope;
-        up[k] = d[k] * value;
-        sums[1][k] += up[k];
-      }
-      if (a.dz) store(a.dz + row * a.lddz + cols, up);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float value = 0.0f, slope = 1.0f;
-        if constexpr (HAS_Z) act_both<ACT>(z[k], value, slope);
-        o[k] = d[k] * slope;
-      }
+    for (int j = 0; j < ROWS; ++j) {
+      const int64_t row = r0 + j * step;
+      if (row >= a.rows) break;
+      dv[j] = load(a.dd + row * a.lddd);
+      if constexpr (HAS_Z) zv[j] = load(a.z + row * a.ldz);
+      if constexpr (GATED) uv[j] = load(a.z + row * a.ldz + cols);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sums[0][k] += o[k];
-    if (a.dz) store(a.dz + row * a.lddz, o);
+    for (int j = 0; j < ROWS; ++j) {
+      const int64_t row = r0 + j * step;
+      if (row >= a.rows) break;
+      float d[8], z[8], o[8];
+      unpack8(dv[j], d);
+      if constexpr (HAS_Z) unpack8(zv[j], z);
+      if constexpr (GATED) {
+        float u[8], up[8];
+        unpack8(uv[j], u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float value, slope;
+          act_both<ACT>(z[k], value, slope);
+          o[k] = d[k] * u[k] * slope;
+          up[k] = d[k] * value;
+          sums[1][k] += up[k];
+        }
+        if (a.dz) store(a.dz + row * a.lddz + cols, up);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float value = 0.0f, slope = 1.0f;
+          if constexpr (HAS_Z) act_both<ACT>(z[k], value, slope);
+          o[k] = d[k] * slope;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sums[0][k] += o[k];
+      if (a.dz) store(a.dz + row * a.lddz, o);
+    }
   }
   if (!a.partial) return;
   __shared__ float sh[256][9];
@@ -105,22 +117,30 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int wide) {
 
 }  // namespace
 
-// Threads of a workgroup along a row: a power of two.
-static int act_bwd_wide(int64_t cols) {
+// Threads of a workgroup along a row: a power of two, up to `most`. With column sums one wave of them, so that a
+// workgroup takes four rows at a time and there are few rows of partial sums to join.
+static int act_bwd_wide(int64_t cols, bool sums) {
+  const int most = sums ? 64 : 256;
   int wide = 1;
-  while (wide < 256 && 8 * wide < cols) wide *= 2;
+  while (wide < most && 8 * wide < cols) wide *= 2;
   return wide;
 }
 
-int64_t act_bwd_groups(int64_t rows, int64_t cols, int gated) {
-  const int64_t wide = act_bwd_wide(cols), strips = (cols + 8 * wide - 1) / (8 * wide), high = 256 / wide;
-  const int64_t most = (rows + high - 1) / high, want = (1024 + strips - 1) / strips;
-  return most < want ? most : want;
+// Workgroups along the rows: up to 8 on a CU in all; with column sums 8 rows a thread at the least, where there are.
+static int64_t act_bwd_blocks(int64_t rows, int64_t cols, bool sums) {
+  const int64_t wide = act_bwd_wide(cols, sums), strips = (cols + 8 * wide - 1) / (8 * wide), high = 256 / wide;
+  const int64_t most = (rows + high - 1) / high, want = (2048 + strips - 1) / strips;
+  const int64_t groups = most < want ? most : want;
+  if (!sums) return groups;
+  const int64_t few = (rows + 8 * high - 1) / (8 * high);
+  return groups < few ? groups : few;
 }
 
+int64_t act_bwd_groups(int64_t rows, int64_t cols) { return act_bwd_blocks(rows, cols, true); }
+
 hipError_t launch_act_bwd(const ActBwdArgs& a, float* dbias, int accumulate, hipStream_t stream) {
-  const int wide = act_bwd_wide(a.cols);
-  const int64_t strips = (a.cols + 8 * wide - 1) / (8 * wide), groups = act_bwd_groups(a.rows, a.cols, a.gated);
+  const int wide = act_bwd_wide(a.cols, dbias != nullptr);
+  const int64_t strips = (a.cols + 8 * wide - 1) / (8 * wide), groups = act_bwd_blocks(a.rows, a.cols, dbias != nullptr);
   auto go = [&](auto act, auto gated, auto end) {
     hipLaunchKernelGGL((act_bwd_kernel<decltype(act)::value, decltype(gated)::value, decltype(end)::value>),
                        dim3(static_cast<uint32_t>(strips), static_cast<uint32_t>(groups)), dim3(256), 0, stream, a, wide);

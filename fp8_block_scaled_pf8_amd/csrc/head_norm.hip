@@ -154,14 +154,39 @@ struct Turns {
   int axis[MULTI ? N : 1];
   __device__ __forceinline__ Turns(const Lane<KIND>& at, const HeadNormArgs& p) {
 #pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = 0.0;
+    if (!p.freq) return;
+    bool whole = false;  // the lane's pairs are all rotated: their frequencies by vector loads
+    if constexpr (KIND != kSingle) whole = at.rotated == 8;
+    if (whole) {
+      if constexpr (KIND != kSingle) {
+        if (p.f64) {
+          const double* w = static_cast<const double*>(p.freq) + at.p0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = w[i];
+        } else {
+          const float* w = static_cast<const float*>(p.freq) + at.p0;
+          const f128_a4 a = *reinterpret_cast<const f128_a4*>(w), b = *reinterpret_cast<const f128_a4*>(w + 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = static_cast<double>(a[i]), f[i + 4] = static_cast<double>(b[i]);
+        }
+      }
+    } else if (p.f64) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (at.rot(i)) f[i] = static_cast<const double*>(p.freq)[at.pair(i)];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (at.rot(i)) f[i] = static_cast<double>(static_cast<const float*>(p.freq)[at.pair(i)]);
+    }
+#pragma unroll
     for (int i = 0; i < N; ++i) {
-      f[i] = 0.0;
-      if constexpr (MULTI) axis[i] = 0;
-      if (!at.rot(i)) continue;
-      const int k = at.pair(i);
-      f[i] = (p.f64 ? static_cast<const double*>(p.freq)[k] : static_cast<double>(static_cast<const float*>(p.freq)[k])) *
-             0.15915494309189533577;
+      f[i] *= 0.15915494309189533577;
       if constexpr (MULTI) {
+        const int k = at.pair(i);
+        axis[i] = 0;
+        if (!at.rot(i)) continue;
         if (p.cycled) {
           const int a = k % p.axes;
           const int lim = a == 0 ? p.share[0] : a == 1 ? p.share[1] : a == 2 ? p.share[2] : p.share[3];
@@ -183,8 +208,11 @@ struct Turns {
       pos[a] = 0.0;
       if (MULTI && a >= p.axes) continue;
       const int64_t k = token * p.pos_st + a * p.pos_sa;
-      pos[a] = p.p64 ? static_cast<double>(static_cast<const int64_t*>(p.pos)[k])
-                     : static_cast<double>(static_cast<const int32_t*>(p.pos)[k]);
+      // a 64-bit position's low half and high half (or the sign of a 32-bit one)
+      const int32_t* q = static_cast<const int32_t*>(p.pos) + (p.p64 ? 2 * k : k);
+      const uint32_t low = static_cast<uint32_t>(q[0]);
+      const int32_t high = p.p64 ? q[1] : q[0] >> 31;
+      pos[a] = __builtin_fma(static_cast<double>(high), 0x1p32, static_cast<double>(low));
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -203,17 +231,32 @@ struct Turns {
 template <Kind KIND>
 __device__ __forceinline__ void head_weights(const void* w, const HeadNormArgs& p, const Lane<KIND>& at,
                                              float (&wa)[Lane<KIND>::N], float (&wb)[Lane<KIND>::N]) {
-  auto get = [&](int k) {
-    return (p.wf32 ? static_cast<const float*>(w)[k] : bf_lo(static_cast<const uint16_t*>(w)[k])) + p.offset;
-  };
+  constexpr int N = Lane<KIND>::N;
 #pragma unroll
-  for (int i = 0; i < Lane<KIND>::N; ++i) {
-    wa[i] = wb[i] = 1.0f;
-    if (w && at.any()) {
-      if (KIND != kSingle || at.own(i)) wa[i] = get(at.place_a(i));
-      if (at.has_b(i)) wb[i] = get(at.place_b(i));
+  for (int i = 0; i < N; ++i) wa[i] = wb[i] = 1.0f;
+  if (!w || !at.any()) return;
+  if constexpr (KIND == kSingle) {
+    auto get = [&](int k) { return p.wf32 ? static_cast<const float*>(w)[k] : bf_lo(static_cast<const uint16_t*>(w)[k]); };
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (at.own(i)) wa[i] = get(at.place_a(i)) + p.offset;
+      if (at.has_b(i)) wb[i] = get(at.place_b(i)) + p.offset;
     }
+    return;
+  } else if (p.wf32) {
+    const float* v = static_cast<const float*>(w);
+    const f128_a4 q[4] = {*reinterpret_cast<const f128_a4*>(v + at.e0), *reinterpret_cast<const f128_a4*>(v + at.e0 + 4),
+                          *reinterpret_cast<const f128_a4*>(v + at.e1), *reinterpret_cast<const f128_a4*>(v + at.e1 + 4)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      wa[i] = KIND == kNext ? q[i / 2][2 * i % 4] : q[i / 4][i % 4];
+      wb[i] = KIND == kNext ? q[i / 2][2 * i % 4 + 1] : q[2 + i / 4][i % 4];
+    }
+  } else {
+    Lane<KIND>::unpack(at.load(static_cast<const uint16_t*>(w)), wa, wb);
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i) wa[i] += p.offset, wb[i] += p.offset;
 }
 
 // A group's items: up to HC consecutive heads of a token.
@@ -426,7 +469,7 @@ hipError_t launch_head_norm_bwd(HeadNormArgs a, float* const (&dw)[2], int accum
     return hipGetLastError();
   });
   if (e != hipSuccess || a.n_sums == 0) return e;
-  return launch_column_sums(a.partial, static_cast<int>(blocks), a.n_sums * a.dim, a.dim, outs, accumulate, stream);
+  return launch_column_sums_deep(a.partial, static_cast<int>(blocks), a.n_sums * a.dim, a.dim, outs, accumulate, stream);
 }
 
 }  // namespace pf8

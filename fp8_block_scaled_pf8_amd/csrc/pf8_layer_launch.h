@@ -61,7 +61,7 @@ struct ActBwdArgs {
 };
 
 hipError_t launch_act_bwd(const ActBwdArgs& args, float* dbias, int accumulate, hipStream_t stream);
-int64_t act_bwd_groups(int64_t rows, int64_t cols, int gated);
+int64_t act_bwd_groups(int64_t rows, int64_t cols);
 
 // The forward product with its epilogue; d is [m, gated ? n / 2 : n].
 struct FpropActArgs {
