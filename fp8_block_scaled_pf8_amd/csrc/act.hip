@@ -126,13 +126,13 @@ static int act_bwd_wide(int64_t cols, bool sums) {
   return wide;
 }
 
-// Workgroups along the rows: up to 8 on a CU in all; with column sums 8 rows a thread at the least, where there are.
+// Workgroups along the rows: up to 8 on a CU in all; with column sums 4 rows a thread at the least, where there are.
 static int64_t act_bwd_blocks(int64_t rows, int64_t cols, bool sums) {
   const int64_t wide = act_bwd_wide(cols, sums), strips = (cols + 8 * wide - 1) / (8 * wide), high = 256 / wide;
   const int64_t most = (rows + high - 1) / high, want = (2048 + strips - 1) / strips;
   const int64_t groups = most < want ? most : want;
   if (!sums) return groups;
-  const int64_t few = (rows + 8 * high - 1) / (8 * high);
+  const int64_t few = (rows + 4 * high - 1) / (4 * high);
   return groups < few ? groups : few;
 }
 

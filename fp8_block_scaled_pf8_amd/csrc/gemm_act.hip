@@ -32,7 +32,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quarter = lane >> 4;
   const int64_t cols = GATED ? p.n / 2 : p.n;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, m0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
   const int nk = static_cast<int>(p.k / kGroup);
   const uint8_t* w[PARTS];
   const float* sw[PARTS];
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   const float* sx[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int64_t row = min64(16 * t + l16, p.m - 1);
+    const int64_t row = min64(m0 + 16 * t + l16, p.m - 1);
     x[t] = p.a + row * p.lda + quarter * 32;
     sx[t] = p.a_dscale + row;
   }
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   // a thread takes 4 consecutive columns of a token
   const int t = threadIdx.x >> 6;
   if (t >= MT) return;
-  const int64_t m = 16 * t + l16, n = n0 + 4 * quarter;
+  const int64_t m = m0 + 16 * t + l16, n = n0 + 4 * quarter;
   if (m >= p.m || n >= cols) return;
   const int left = static_cast<int>(min64(4, cols - n));
   float v[PARTS][4];
@@ -140,22 +140,26 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
 
 template <int MT>
 static hipError_t launch_few(const FpropActArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(((a.gated ? a.n / 2 : a.n) + 15) / 16)), block(512);
+  const dim3 grid(static_cast<uint32_t>(((a.gated ? a.n / 2 : a.n) + 15) / 16), static_cast<uint32_t>((a.m + 16 * MT - 1) / (16 * MT))),
+      block(512);
   if (a.gated) hipLaunchKernelGGL((fprop_act_few_kernel<MT, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((fprop_act_few_kernel<MT, false>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
 // Modelled times in microseconds, from sweeps of 1 to 8192 rows over weights of 12288 x 2048 (gated and not), 2048 x
-// 6144, 2048 x 2048, 1000 x 1536 and 6144 x 6144 (gated); what the models choose was within 8 % of the best
-// choice, but for a few sizes next to a border. As an example, 64 rows on 2048 x 6144: 17.2 us by the kernel for few
-// tokens, 15.9 by 64 x 64 tiles, 21.9 by 128 x 128; 32 rows: 11.3 and the same.
+// 6144, 2048 x 2048, 4096 x 2048, 1000 x 1536, 512 x 4096 and 6144 x 6144 (gated); what the models choose was within 8 %
+// of the best choice, but for a few sizes next to a border. As an example, 64 rows on 2048 x 6144: 11.4 us by the
+// kernel for few tokens, 32 of them a workgroup (13.9 by 16, 16.8 by 64), 16.0 by 64 x 64 tiles, 21.9 by 128 x 128.
 
-// Few tokens: a start, then K blocks of each workgroup, whose tokens' operands every workgroup loads anew; more
-// workgroups than CUs share the memory's rate.
+// Few tokens, 16 MT of them a workgroup: a start, then its K blocks, with its tokens' operands; more workgroups than
+// CUs share the memory's rate.
+template <int MT>
 static double few_cost(const FpropActArgs& a) {
-  const double rows = static_cast<double>(a.n) / 16 / 256;
-  return 3.0 + (rows > 1.0 ? rows : 1.0) * static_cast<double>(a.k) / 1024 * (0.5 + 0.03 * static_cast<double>(a.m));
+  const int64_t groups = (a.m + 16 * MT - 1) / (16 * MT);
+  const double share = static_cast<double>(a.n) / 16 / 256 * static_cast<double>(groups);
+  const double tokens = static_cast<double>(a.m < 16 * MT ? a.m : 16 * MT);
+  return 3.0 + (share > 1.0 ? share : 1.0) * static_cast<double>(a.k) / 1024 * (0.5 + 0.028 * tokens);
 }
 
 // Tiles of one shape: a start, then rounds of one tile on each of 256 CUs, each of them by K and with its own end. A
@@ -182,8 +186,10 @@ hipError_t launch_fprop_act(const FpropActArgs& a, hipStream_t stream) {
     cost[i] = kShapes[i](a);
     if (cost[i] < cost[best]) best = i;
   }
-  if (a.m <= 64 && few_cost(a) < cost[best])
-    return a.m <= 16 ? launch_few<1>(a, stream) : a.m <= 32 ? launch_few<2>(a, stream) : launch_few<4>(a, stream);
+  const double few[3] = {few_cost<1>(a), few_cost<2>(a), few_cost<4>(a)};
+  const int least = few[1] < few[0] ? (few[2] < few[1] ? 2 : 1) : few[2] < few[0] ? 2 : 0;
+  if (a.m <= 1024 && few[least] < cost[best])  // (the grid is as high as the groups of tokens)
+    return least == 0 ? launch_few<1>(a, stream) : least == 1 ? launch_few<2>(a, stream) : launch_few<4>(a, stream);
   switch (best) {
     case 0: return launch_fprop_act_tiles<256, 256>(a, stream);
     case 1: return launch_fprop_act_tiles<256, 128>(a, stream);

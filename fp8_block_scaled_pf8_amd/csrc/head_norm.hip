@@ -202,23 +202,22 @@ struct Turns {
 #pragma unroll
     for (int i = 0; i < N; ++i) c[i] = 1.0f, s[i] = 0.0f;
     if (!p.pos) return;
-    double pos[MULTI ? kHeadMaxAxes : 1];
-#pragma unroll
-    for (int a = 0; a < (MULTI ? kHeadMaxAxes : 1); ++a) {
-      pos[a] = 0.0;
-      if (MULTI && a >= p.axes) continue;
+    auto position = [&](int a) {
+      if (MULTI && a >= p.axes) return 0.0;
       const int64_t k = token * p.pos_st + a * p.pos_sa;
       // a 64-bit position's low half and high half (or the sign of a 32-bit one)
       const int32_t* q = static_cast<const int32_t*>(p.pos) + (p.p64 ? 2 * k : k);
       const uint32_t low = static_cast<uint32_t>(q[0]);
       const int32_t high = p.p64 ? q[1] : q[0] >> 31;
-      pos[a] = __builtin_fma(static_cast<double>(high), 0x1p32, static_cast<double>(low));
-    }
+      return __builtin_fma(static_cast<double>(high), 0x1p32, static_cast<double>(low));
+    };
+    const double x0 = position(0), x1 = MULTI ? position(1) : 0.0, x2 = MULTI ? position(2) : 0.0,
+                 x3 = MULTI ? position(3) : 0.0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (!l.rot(i)) continue;
-      double x = pos[0];
-      if constexpr (MULTI) x = axis[i] == 0 ? pos[0] : axis[i] == 1 ? pos[1] : axis[i] == 2 ? pos[2] : pos[3];
+      double x = x0;
+      if constexpr (MULTI) x = axis[i] == 0 ? x0 : axis[i] == 1 ? x1 : axis[i] == 2 ? x2 : x3;
       x *= f[i];
       const float t = static_cast<float>(x - __builtin_rint(x));
       c[i] = __builtin_amdgcn_cosf(t) * p.scale;
@@ -271,7 +270,7 @@ template <Kind KIND, int G, int HC, bool MULTI>
 __global__ __launch_bounds__(256) void head_norm_fwd_kernel(HeadNormArgs p, unsigned blocks_q) {
   constexpr int N = Lane<KIND>::N;
   const int second = blockIdx.x >= blocks_q;
-  const HeadTensor& x = p.t[second];
+  const HeadTensor x = second ? p.t[1] : p.t[0];
   const Items items(p.tokens, x.heads, HC);
   const int64_t item = static_cast<int64_t>(blockIdx.x - (second ? blocks_q : 0)) * (256 / G) + threadIdx.x / G;
   if (item >= items.count) return;
@@ -329,7 +328,7 @@ __global__ __launch_bounds__(256) void head_norm_bwd_kernel(HeadNormArgs p) {
   const Turns<KIND, MULTI> turns(at, p);
   const float inv_n = 1.0f / static_cast<float>(p.dim);
   for (int k = 0; k < 2; ++k) {
-    const HeadTensor& x = p.t[k];
+    const HeadTensor x = k ? p.t[1] : p.t[0];  // (by an index, the arguments would be copied to scratch memory)
     if (!x.heads) continue;
     const Items items(p.tokens, x.heads, HC);
     float wa[N], wb[N], sa[N], sb[N];
@@ -442,12 +441,18 @@ static hipError_t by_shape(const HeadNormArgs& a, F f) {
 
 hipError_t launch_head_norm_fwd(const HeadNormArgs& a, hipStream_t stream) {
   return by_shape(a, [&](auto kind, auto lanes, auto multi) {
-    constexpr int G = decltype(lanes)::value, HC = 4;
-    auto blocks = [&](int heads) { return (a.tokens * ((heads + HC - 1) / HC) + 256 / G - 1) / (256 / G); };
-    const int64_t bq = blocks(a.t[0].heads), bk = blocks(a.t[1].heads);
-    hipLaunchKernelGGL((head_norm_fwd_kernel<decltype(kind)::value, G, HC, decltype(multi)::value>),
-                       dim3(static_cast<uint32_t>(bq + bk)), dim3(256), 0, stream, a, static_cast<unsigned>(bq));
-    return hipGetLastError();
+    constexpr int G = decltype(lanes)::value;
+    auto go = [&](auto hc) {
+      constexpr int HC = decltype(hc)::value;
+      auto blocks = [&](int heads) { return (a.tokens * ((heads + HC - 1) / HC) + 256 / G - 1) / (256 / G); };
+      const int64_t bq = blocks(a.t[0].heads), bk = blocks(a.t[1].heads);
+      hipLaunchKernelGGL((head_norm_fwd_kernel<decltype(kind)::value, G, HC, decltype(multi)::value>),
+                         dim3(static_cast<uint32_t>(bq + bk)), dim3(256), 0, stream, a, static_cast<unsigned>(bq));
+      return hipGetLastError();
+    };
+    // Four heads of a token share its angles where there is work enough to fill the card that way.
+    const int64_t heads = a.tokens * (a.t[0].heads + a.t[1].heads);
+    return heads * G >= 4 * 256 * 1024 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 1>{});
   });
 }
 

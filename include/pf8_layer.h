@@ -138,8 +138,8 @@ int64_t pf8_act_bwd_workspace(int64_t rows, int64_t cols, int gated);
  *
  * Operands, scales, alignment and limits are those of pf8_block_gemm with PF8_FPROP (m, n >= 1,
  * k % 128 == 0, power-of-two scales; b_dscale[(j / 128) * ld_bs + kb], ld_bs >= k / 128), and its accumulation
- * contract holds for z before its rounding. Up to 64 rows the sum over K is formed in parts, joined in a fixed order;
- * the same call gives the same bits each time.
+ * contract holds for z before its rounding. For few rows the sum over K is formed in parts, joined in a
+ * fixed order; the same call gives the same bits each time.
  * gated: 0 or 1; with 1, n is a multiple of 128 and the activation is not PF8_ACT_NONE.
  * bias: [n] of btype (PF8_BF16 or PF8_F32), or NULL.
  * residual: bf16, d's shape, pitch ldr, or NULL. May be d itself (same address and pitch).
