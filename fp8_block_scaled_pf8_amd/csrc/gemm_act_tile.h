@@ -380,6 +380,43 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
         if (c < cols) bias[j] = bias_at(p, second * cols + c);
       }
     }
+    // The thread's number, opaque: places in the epilogue are made from it there, not kept in registers over the K loop.
+    int te = t;
+    asm volatile("" : "+v"(te));
+    // ---- the residual's rows of a slab, by whole rows as d's; the first slab's are on their way during the last body ----
+    const int rows = static_cast<int>(min64(BM, p.m - m0));
+    const int left = static_cast<int>(min64(OUT, cols - n0));  // columns of d in the tile
+    // byte offset, in the tile's rows of an array of pitch ld, of a thread's first row; and of chunk `it` from there
+    auto row_offset = [&](int n, int ld2) { return (te / n / 32 * WM + te / n % 32) * ld2; };
+    auto step_offset = [&](int n, int i, int it, int ld2) {
+      const int s = 256 / n * it;
+      return (s / 32 * WM + s % 32 + 32 * i) * ld2;
+    };
+    v4i res[RES ? PER_D : 1];
+    auto load_residual = [&](int i) {
+      const int ld2 = static_cast<int>(p.ldr * 2), c = 8 * (te % CHD), room = left - c;
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(p.residual) + m0 * p.ldr + n0, 0, rows * ld2, kBufferFlags);
+      const int vo = row_offset(CHD, ld2) + 2 * c;
+      if (room >= 8) {
+#pragma unroll
+        for (int it = 0; it < PER_D; ++it)
+          res[it] = __builtin_bit_cast(
+              v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, vo + step_offset(CHD, i, it, ld2), 0, 0));
+      } else {
+#pragma unroll
+        for (int it = 0; it < PER_D; ++it) {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (e < room)
+              w[e / 2] |= static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
+                              rsrc, vo + step_offset(CHD, i, it, ld2) + 2 * e, 0, 0))) << (16 * (e % 2));
+          res[it] = v4i{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
+        }
+      }
+    };
+    if constexpr (RES) load_residual(0);
     // last body: its refills fetch the next tile's stages 0..3
     const int next = r + 1 < ntiles ? r + 1 : r;
     stage(I0{}, T{}, s + 3, T{}, 0, F{}, T{}, next, F{});
@@ -408,8 +445,6 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
 #pragma unroll
     for (int i = 0; i < TM; ++i) pin(i);
     constexpr int kWaitLgkm = 0xF | (0x7 << 4) | (0x3 << 14);  // lgkmcnt(0) only
-    const int rows = static_cast<int>(min64(BM, p.m - m0));
-    const int left = static_cast<int>(min64(OUT, cols - n0));  // columns of d in the tile
     // A lane's accumulator acc[i][j] holds, of row wm WM + 32 i + l32, the 4 columns 8 q4 + 4 half .. +3 of
     // block j for each q4. Gated, the first half of a wave's columns makes the gate. part: which half;
     // place: 8-column chunk of d's tile (less the wave's own offset).
@@ -423,22 +458,16 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
     const TileAct<ACT> act(p.act);
     // Staging: slab i holds rows wm WM + 32 i + l32 of both wave rows as row wm 32 + l32; chunk c of row sr lies at
     // chunk c ^ (sr mod CH). With a 512-byte aligned buffer a lane's address is one XOR of the chunk's constant bits.
-    const uint32_t wbase = (lds_addr(stg) + (wm * 32 + l32) * RP + 8 * half) |
-                           (((wn * (OUT / 16)) ^ (l32 & (CH - 1))) << 4);
+    const uint32_t wbase = (lds_addr(stg) + (wm * 32 + te % 32) * RP + 8 * (te / 32 % 2)) |
+                           (((wn * (OUT / 16)) ^ (te % 32 & (CH - 1))) << 4);
     // Whole rows: thread t takes chunk t mod N of rows t / N + 256 / N it.
     auto row_chunks = [&](auto n_c, uint32_t (&addr)[64 * decltype(n_c)::value / 256]) {
       constexpr int N = decltype(n_c)::value;
 #pragma unroll
       for (int it = 0; it < 64 * N / 256; ++it) {
-        const int row = t / N + 256 / N * it;
-        addr[it] = lds_addr(stg) + row * RP + (((t % N) ^ (row & (CH - 1))) << 4);
+        const int row = te / N + 256 / N * it;
+        addr[it] = lds_addr(stg) + row * RP + (((te % N) ^ (row & (CH - 1))) << 4);
       }
-    };
-    // byte offset, in the tile's rows of an array of pitch ld, of a thread's first row; and of chunk `it` from there
-    auto row_offset = [&](int n, int ld2) { return (t / n / 32 * WM + t / n % 32) * ld2; };
-    auto step_offset = [&](int n, int i, int it, int ld2) {
-      const int s = 256 / n * it;
-      return (s / 32 * WM + s % 32 + 32 * i) * ld2;
     };
     // stores of a thread's chunks of N to an array from its tile's first element on; c: the chunk's first column
     // there, room: the columns left from it
@@ -471,32 +500,8 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
     using ND = std::integral_constant<int, CHD>;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      v4i res[PER_D];
-      if constexpr (RES) {
-        const int ld2 = static_cast<int>(p.ldr * 2), c = 8 * (t % CHD), room = left - c;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p.residual) + m0 * p.ldr + n0, 0, rows * ld2, kBufferFlags);
-        const int vo = row_offset(CHD, ld2) + 2 * c;
-        if (room >= 8) {
-#pragma unroll
-          for (int it = 0; it < PER_D; ++it)
-            res[it] = __builtin_bit_cast(
-                v4i, __builtin_amdgcn_raw_buffer_load_b128(rsrc, vo + step_offset(CHD, i, it, ld2), 0, 0));
-        } else {
-#pragma unroll
-          for (int it = 0; it < PER_D; ++it) {
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 7; ++e)
-              if (e < room)
-                w[e / 2] |= static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
-                                rsrc, vo + step_offset(CHD, i, it, ld2) + 2 * e, 0, 0))) << (16 * (e % 2));
-            res[it] = v4i{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
-          }
-        }
-      }
+      pin(i);
       if (p.z) {
-        pin(i);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -505,7 +510,7 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
                        pack_bf16x2(acc[i][j][4 * q4], acc[i][j][4 * q4 + 1]),
                        pack_bf16x2(acc[i][j][4 * q4 + 2], acc[i][j][4 * q4 + 3]));
         fence();
-        const int c = t % CH, of = GATED ? c % (CH / 2) : c;  // chunk of the part
+        const int c = te % CH, of = GATED ? c % (CH / 2) : c;  // chunk of the part
         const int64_t second = GATED && c >= CH / 2 ? cols : 0;
         store_rows(NZ{}, p.z + m0 * p.ldz + n0, p.ldz, static_cast<int>(second) + 8 * of, left - 8 * of, i);
         fence();
@@ -516,9 +521,9 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
 #pragma unroll
         for (int it = 0; it < PER_D; ++it) stg_write16(addr[it], res[it]);
         fence();
+        if (i + 1 < TM) load_residual(i + 1);
       }
       // d's values, in the place of the first part's
-      pin(i);
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -544,7 +549,7 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
           stg_write8(a1, pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3]));
         }
       fence();
-      store_rows(ND{}, p.d + m0 * p.ldd + n0, p.ldd, 8 * (t % CHD), left - 8 * (t % CHD), i);
+      store_rows(ND{}, p.d + m0 * p.ldd + n0, p.ldd, 8 * (te % CHD), left - 8 * (te % CHD), i);
       if (i + 1 < TM) fence();  // every wave has read this slab back before the next one is staged
     }
     if (r + 1 == ntiles) break;

@@ -180,17 +180,18 @@ struct Turns {
       for (int i = 0; i < N; ++i)
         if (at.rot(i)) f[i] = static_cast<double>(static_cast<const float*>(p.freq)[at.pair(i)]);
     }
+    const int start = MULTI && p.cycled ? at.pair(0) % p.axes : 0, step = KIND == kSingle ? 64 % p.axes : 1;
+    int turn = start;  // the axis whose turn it is
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       f[i] *= 0.15915494309189533577;
       if constexpr (MULTI) {
         const int k = at.pair(i);
-        axis[i] = 0;
-        if (!at.rot(i)) continue;
         if (p.cycled) {
-          const int a = k % p.axes;
-          const int lim = a == 0 ? p.share[0] : a == 1 ? p.share[1] : a == 2 ? p.share[2] : p.share[3];
-          axis[i] = k < lim ? a : 0;
+          const int lim = turn == 0 ? p.share[0] : turn == 1 ? p.share[1] : turn == 2 ? p.share[2] : p.share[3];
+          axis[i] = k < lim ? turn : 0;
+          turn += step;
+          if (turn >= p.axes) turn -= p.axes;
         } else {
           axis[i] = (k >= p.share[0]) + (k >= p.share[1]) + (k >= p.share[2]);
         }

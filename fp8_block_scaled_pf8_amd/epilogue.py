@@ -171,7 +171,7 @@ def act_backward(dd: Tensor, z: Optional[Tensor], activation: Optional[str], gat
         shape = torch.Size((rows, width))
         pz, ldz = _rows(z, "z", shape, dev)
         if dz_out is None:
-            dz = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            dz = torch.empty_like(z, memory_format=torch.contiguous_format)
             po, ldo = dz.data_ptr(), width
         else:
             dz = dz_out

@@ -40,19 +40,20 @@ class QKNormRopeGrads(NamedTuple):
 
 def _heads(t: Tensor, name: str, shape, device) -> Tuple[int, int, int]:
     """(address, stride of tokens, stride of heads) of a bf16 [tokens, heads, head_dim] tensor after its checks."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    tokens, heads, dim = shape
     st, sh, sd = t.stride()
-    if shape[0] == 0:
+    if tokens == 0:
         return 0, 0, 0
-    if sd != 1 and shape[2] != 1:
+    if sd != 1 and dim != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
-    if shape[1] > 1 and sh < shape[2]:
-        raise ValueError(f"the heads of {name} overlap (stride {sh} for {shape[2]} values)")
+    if sh < dim and heads > 1:
+        raise ValueError(f"the heads of {name} overlap (stride {sh} for {dim} values)")
     return t.data_ptr(), st, sh
 
 
@@ -172,7 +173,7 @@ def _k_shape(k: Optional[Tensor], name: str, q: Tensor):
 def _result(out: Optional[Tensor], name: str, shape, like: Tensor) -> Tuple[Tensor, int, int, int]:
     if out is not None:
         return (out, *_heads(out, name, shape, like.device))
-    out = torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    out = torch.empty_like(like, memory_format=torch.contiguous_format)  # (half of what torch.empty takes)
     return out, out.data_ptr(), shape[1] * shape[2], shape[2]
 
 
@@ -199,7 +200,7 @@ def qk_norm_rope(q: Tensor, k: Optional[Tensor] = None, positions: Optional[Tens
     aq = _heads(q, "q", qs, dev)
     ak = (0, 0, 0) if k is None else _heads(k, "k", ks, dev)
     oq, *pq = _result(q_out, "q_out", qs, q)
-    ok, *pk = (None, 0, 0, 0) if k is None else _result(k_out, "k_out", ks, q)
+    ok, *pk = (None, 0, 0, 0) if k is None else _result(k_out, "k_out", ks, k)
     if tokens == 0:
         return oq, ok
     if q_out is not None or k_out is not None:
@@ -262,7 +263,7 @@ def qk_norm_rope_backward(dq: Tensor, dk: Optional[Tensor], q: Optional[Tensor],
     dw_q, pwq = vector(dw_q_out, "dw_q_out", w_q)
     dw_k, pwk = vector(dw_k_out, "dw_k_out", w_k)
     oq, *pq = _result(dq_out, "dq_out", qs, dq)
-    ok, *pk = (None, 0, 0, 0) if dk is None else _result(dk_out, "dk_out", ks, dq)
+    ok, *pk = (None, 0, 0, 0) if dk is None else _result(dk_out, "dk_out", ks, dk)
     sums = [t for t in (dw_q, dw_k) if t is not None]
     if tokens == 0:
         if not accumulate:
