@@ -114,9 +114,9 @@ pf8_status pf8_qk_norm_rope(int64_t tokens, int64_t head_dim, const void* q, int
   pf8::HeadNormArgs a = head_norm_args(tokens, head_dim, wtype, weight_offset, eps, positions, ptype, pos_st, pos_sa,
                                        inv_freq, ftype, pairs, axes, sections, order, interleaved, rotary_scale);
   a.t[0] = {static_cast<const uint16_t*>(q), q_st, q_sh, nullptr, 0, 0, static_cast<uint16_t*>(q_out), qo_st, qo_sh, w_q,
-            static_cast<int>(heads_q), -1};
+            static_cast<int>(heads_q), 0};
   a.t[1] = {static_cast<const uint16_t*>(k), k_st, k_sh, nullptr, 0, 0, static_cast<uint16_t*>(k_out), ko_st, ko_sh, w_k,
-            static_cast<int>(heads_k), -1};
+            static_cast<int>(heads_k), 0};
   return launch_status(pf8::launch_head_norm_fwd(a, static_cast<hipStream_t>(hip_stream)));
 }
 
@@ -124,7 +124,7 @@ int64_t pf8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads_q, int64_t 
   if (tokens <= 0 || heads_q <= 0 || heads_k < 0 || head_dim <= 0 || head_dim > PF8_HEAD_MAX_DIM ||
       heads_q > PF8_HEAD_MAX_HEADS || heads_k > PF8_HEAD_MAX_HEADS || tokens > kMaxDim / std::max(heads_q, heads_k))
     return 0;
-  return pf8::head_norm_bwd_blocks(tokens, heads_q, heads_k, head_dim) * 2 * head_dim * 4;
+  return pf8::head_norm_bwd_blocks(tokens, heads_q, heads_k) * head_dim * 4;
 }
 
 pf8_status pf8_qk_norm_rope_bwd(int64_t tokens, int64_t head_dim, const void* dq, int64_t dq_st, int64_t dq_sh,
@@ -163,9 +163,9 @@ pf8_status pf8_qk_norm_rope_bwd(int64_t tokens, int64_t head_dim, const void* dq
   pf8::HeadNormArgs a = head_norm_args(tokens, head_dim, wtype, weight_offset, eps, positions, ptype, pos_st, pos_sa,
                                        inv_freq, ftype, pairs, axes, sections, order, interleaved, rotary_scale);
   a.t[0] = {static_cast<const uint16_t*>(q), q_st, q_sh, static_cast<const uint16_t*>(dq), dq_st, dq_sh,
-            static_cast<uint16_t*>(dq_out), dqo_st, dqo_sh, w_q, dq_out || dw_q ? static_cast<int>(heads_q) : 0, -1};
+            static_cast<uint16_t*>(dq_out), dqo_st, dqo_sh, w_q, dq_out || dw_q ? static_cast<int>(heads_q) : 0, 0};
   a.t[1] = {static_cast<const uint16_t*>(k), k_st, k_sh, static_cast<const uint16_t*>(dk), dk_st, dk_sh,
-            static_cast<uint16_t*>(dk_out), dko_st, dko_sh, w_k, dk_out || dw_k ? static_cast<int>(heads_k) : 0, -1};
+            static_cast<uint16_t*>(dk_out), dko_st, dko_sh, w_k, dk_out || dw_k ? static_cast<int>(heads_k) : 0, 0};
   a.partial = static_cast<float*>(workspace);
   return launch_status(pf8::launch_head_norm_bwd(a, {dw_q, dw_k}, accumulate, static_cast<hipStream_t>(hip_stream)));
 }
@@ -195,8 +195,8 @@ pf8_status pf8_act_bwd(int64_t rows, int64_t cols, const void* dd, int64_t lddd,
   if (int e = device_status()) return e;
   const pf8::ActBwdArgs a{rows, static_cast<int>(cols), static_cast<const uint16_t*>(dd), lddd,
                           static_cast<const uint16_t*>(z), ldz, activation, gated, static_cast<uint16_t*>(dz), lddz,
-                          dbias ? static_cast<float*>(workspace) : nullptr};
-  return launch_status(pf8::launch_act_bwd(a, dbias, accumulate, static_cast<hipStream_t>(hip_stream)));
+                          dbias, accumulate, static_cast<float*>(workspace)};
+  return launch_status(pf8::launch_act_bwd(a, static_cast<hipStream_t>(hip_stream)));
 }
 
 pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* a_dscale,

@@ -91,9 +91,10 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int wide) {
       if (a.dz) store(a.dz + row * a.lddz, o);
     }
   }
-  if (!a.partial) return;
+  if (!a.dbias) return;
   __shared__ float sh[256][9];
-  float* out = a.partial + static_cast<int64_t>(blockIdx.y) * PARTS * cols;
+  const bool alone = gridDim.y == 1;  // the sums themselves, not a row of partial ones
+  float* out = alone ? a.dbias : a.partial + static_cast<int64_t>(blockIdx.y) * PARTS * cols;
 #pragma unroll
   for (int part = 0; part < PARTS; ++part) {
     if (high > 1) {
@@ -110,7 +111,10 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int wide) {
     if (ty == 0 && any) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k >= first && c + k < cols) out[part * cols + c + k] = sums[part][k];
+        if (k >= first && c + k < cols) {
+          float* o = out + part * cols + c + k;
+          *o = alone && a.accumulate ? *o + sums[part][k] : sums[part][k];
+        }
     }
   }
 }
@@ -138,9 +142,9 @@ static int64_t act_bwd_blocks(int64_t rows, int64_t cols, bool sums) {
 
 int64_t act_bwd_groups(int64_t rows, int64_t cols) { return act_bwd_blocks(rows, cols, true); }
 
-hipError_t launch_act_bwd(const ActBwdArgs& a, float* dbias, int accumulate, hipStream_t stream) {
-  const int wide = act_bwd_wide(a.cols, dbias != nullptr);
-  const int64_t strips = (a.cols + 8 * wide - 1) / (8 * wide), groups = act_bwd_blocks(a.rows, a.cols, dbias != nullptr);
+hipError_t launch_act_bwd(const ActBwdArgs& a, hipStream_t stream) {
+  const int wide = act_bwd_wide(a.cols, a.dbias != nullptr);
+  const int64_t strips = (a.cols + 8 * wide - 1) / (8 * wide), groups = act_bwd_blocks(a.rows, a.cols, a.dbias != nullptr);
   auto go = [&](auto act, auto gated, auto end) {
     hipLaunchKernelGGL((act_bwd_kernel<decltype(act)::value, decltype(gated)::value, decltype(end)::value>),
                        dim3(static_cast<uint32_t>(strips), static_cast<uint32_t>(groups)), dim3(256), 0, stream, a, wide);
@@ -157,10 +161,10 @@ hipError_t launch_act_bwd(const ActBwdArgs& a, float* dbias, int accumulate, hip
     }
     return by_end(act, std::false_type{});
   });
-  if (e != hipSuccess || !dbias) return e;
+  if (e != hipSuccess || !a.dbias || groups == 1) return e;
   const int width = a.gated ? 2 * a.cols : a.cols;
-  float* outs[3] = {dbias, nullptr, nullptr};
-  return launch_column_sums(a.partial, static_cast<int>(groups), width, width, outs, accumulate, stream);
+  float* outs[3] = {a.dbias, nullptr, nullptr};
+  return launch_column_sums(a.partial, static_cast<int>(groups), width, width, outs, a.accumulate, stream);
 }
 
 }  // namespace pf8

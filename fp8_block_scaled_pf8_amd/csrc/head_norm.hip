@@ -7,7 +7,6 @@
 // loads), so that both values of a pair are in the same lane and the sums of a head run over the group by
 // DPP. A group takes up to HC heads of one token after another with the same angles; all their loads go out first.
 #include "pf8_layer_launch.h"
-#include "pf8_train_launch.h"
 #include "row_device.h"
 
 namespace pf8 {
@@ -317,10 +316,11 @@ __global__ __launch_bounds__(256) void head_norm_fwd_kernel(HeadNormArgs p, unsi
   }
 }
 
-// Backward. Every workgroup takes its share of q's items, then of k's; each lane sums the weight's gradient at
-// its own values, the groups' sums meet in LDS, and a workgroup writes one row of partial sums for each weight.
+// Backward. The first workgroups take q's items, the others k's, in turn; each lane sums the weight's gradient at
+// its own values, the groups' sums meet in LDS, and a workgroup writes one row of partial sums. (With both tensors
+// in every workgroup a short batch waited for everything twice: 1537 tokens of 7 + 1 heads 12.2 us.)
 template <Kind KIND, int G, int HC, bool MULTI>
-__global__ __launch_bounds__(256) void head_norm_bwd_kernel(HeadNormArgs p) {
+__global__ __launch_bounds__(256) void head_norm_bwd_kernel(HeadNormArgs p, unsigned blocks_q) {
   constexpr int N = Lane<KIND>::N, GROUPS = 256 / G;
   // a group's sums, in the order of its lanes: [pair of the lane][a or b]
   __shared__ float sums[GROUPS][G][2 * N + 1];
@@ -328,80 +328,101 @@ __global__ __launch_bounds__(256) void head_norm_bwd_kernel(HeadNormArgs p) {
   const Lane<KIND> at(lane, p);
   const Turns<KIND, MULTI> turns(at, p);
   const float inv_n = 1.0f / static_cast<float>(p.dim);
-  for (int k = 0; k < 2; ++k) {
-    const HeadTensor x = k ? p.t[1] : p.t[0];  // (by an index, the arguments would be copied to scratch memory)
-    if (!x.heads) continue;
-    const Items items(p.tokens, x.heads, HC);
-    float wa[N], wb[N], sa[N], sb[N];
-    head_weights(x.w, p, at, wa, wb);
+  const int second = blockIdx.x >= blocks_q;
+  const HeadTensor x = second ? p.t[1] : p.t[0];  // (by an index, the arguments would be copied to scratch memory)
+  const Items items(p.tokens, x.heads, HC);
+  float wa[N], wb[N], sa[N], sb[N];
+  head_weights(x.w, p, at, wa, wb);
 #pragma unroll
-    for (int i = 0; i < N; ++i) sa[i] = sb[i] = 0.0f;
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * GROUPS + group; item < items.count;
-         item += static_cast<int64_t>(gridDim.x) * GROUPS) {
-      const uint32_t token = static_cast<uint32_t>(item) / static_cast<uint32_t>(items.per_token);
-      const int head = (static_cast<int>(item) - static_cast<int>(token) * items.per_token) * HC;
-      typename Lane<KIND>::Raw rx[HC], rd[HC];
-      const uint16_t* xs = x.x + token * x.x_st + head * x.x_sh;
-      const uint16_t* ds = x.d + token * x.d_st + head * x.d_sh;
+  for (int i = 0; i < N; ++i) sa[i] = sb[i] = 0.0f;
+  const unsigned block = blockIdx.x - (second ? blocks_q : 0), blocks = second ? gridDim.x - blocks_q : blocks_q;
+  for (int64_t item = static_cast<int64_t>(block) * GROUPS + group; item < items.count;
+       item += static_cast<int64_t>(blocks) * GROUPS) {
+    const uint32_t token = static_cast<uint32_t>(item) / static_cast<uint32_t>(items.per_token);
+    const int head = (static_cast<int>(item) - static_cast<int>(token) * items.per_token) * HC;
+    typename Lane<KIND>::Raw rx[HC], rd[HC];
+    const uint16_t* xs = x.x + token * x.x_st + head * x.x_sh;
+    const uint16_t* ds = x.d + token * x.d_st + head * x.d_sh;
 #pragma unroll
-      for (int j = 0; j < HC; ++j) {
-        rx[j] = rd[j] = Lane<KIND>::none();
-        if (head + j < x.heads && at.any()) {
-          if (x.w) rx[j] = at.load(xs + j * x.x_sh);
-          rd[j] = at.load(ds + j * x.d_sh);
-        }
+    for (int j = 0; j < HC; ++j) {
+      rx[j] = rd[j] = Lane<KIND>::none();
+      if (head + j < x.heads && at.any()) {
+        if (x.w) rx[j] = at.load(xs + j * x.x_sh);
+        rd[j] = at.load(ds + j * x.d_sh);
       }
-      float c[N], s[N];
-      turns.at(token, at, p, c, s);
-      uint16_t* dst = x.out + token * x.out_st + head * x.out_sh;
+    }
+    float c[N], s[N];
+    turns.at(token, at, p, c, s);
+    uint16_t* dst = x.out + token * x.out_st + head * x.out_sh;
 #pragma unroll
-      for (int j = 0; j < HC; ++j) {
-        if (head + j >= x.heads) break;
-        float a[N], b[N];
-        Lane<KIND>::unpack(rd[j], a, b);
+    for (int j = 0; j < HC; ++j) {
+      if (head + j >= x.heads) break;
+      float a[N], b[N];
+      Lane<KIND>::unpack(rd[j], a, b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float u = a[i] * c[i] + b[i] * s[i], v = b[i] * c[i] - a[i] * s[i];
+        a[i] = at.rot(i) ? u : a[i], b[i] = at.rot(i) ? v : b[i];
+      }
+      if (x.w) {
+        float ya[N], yb[N], sum = 0.0f, dot = 0.0f;
+        Lane<KIND>::unpack(rx[j], ya, yb);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float u = a[i] * c[i] + b[i] * s[i], v = b[i] * c[i] - a[i] * s[i];
-          a[i] = at.rot(i) ? u : a[i], b[i] = at.rot(i) ? v : b[i];
+          const float u = ya[i] * p.sq, v = yb[i] * p.sq;
+          const float both = __builtin_fmaf(u, u, v * v), with = __builtin_fmaf(a[i] * wa[i], u, b[i] * wb[i] * v);
+          if (at.own(i)) sum += both, dot += with;
         }
-        if (x.w) {
-          float ya[N], yb[N], sum = 0.0f, dot = 0.0f;
-          Lane<KIND>::unpack(rx[j], ya, yb);
+        sum = group_sum<G>(sum), dot = group_sum<G>(dot);
+        const float rho = inv_root(__builtin_fmaf(sum, p.inv_sum, p.eps));
+        const float mean = dot * rho * (inv_n / p.sq);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float u = ya[i] * p.sq, v = yb[i] * p.sq;
-            const float both = __builtin_fmaf(u, u, v * v), with = __builtin_fmaf(a[i] * wa[i], u, b[i] * wb[i] * v);
-            if (at.own(i)) sum += both, dot += with;
-          }
-          sum = group_sum<G>(sum), dot = group_sum<G>(dot);
-          const float rho = inv_root(__builtin_fmaf(sum, p.inv_sum, p.eps));
-          const float mean = dot * rho * (inv_n / p.sq);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float u = ya[i] * rho, v = yb[i] * rho;
-            sa[i] = __builtin_fmaf(a[i], u, sa[i]), sb[i] = __builtin_fmaf(b[i], v, sb[i]);
-            a[i] = rho * (a[i] * wa[i] - u * mean), b[i] = rho * (b[i] * wb[i] - v * mean);
-          }
+        for (int i = 0; i < N; ++i) {
+          const float u = ya[i] * rho, v = yb[i] * rho;
+          sa[i] = __builtin_fmaf(a[i], u, sa[i]), sb[i] = __builtin_fmaf(b[i], v, sb[i]);
+          a[i] = rho * (a[i] * wa[i] - u * mean), b[i] = rho * (b[i] * wb[i] - v * mean);
         }
-        if (x.out && at.any()) at.store(dst + j * x.out_sh, a, b);
       }
+      if (x.out && at.any()) at.store(dst + j * x.out_sh, a, b);
     }
-    if (x.slot < 0) continue;
-#pragma unroll
-    for (int i = 0; i < N; ++i) sums[group][lane][2 * i] = sa[i], sums[group][lane][2 * i + 1] = sb[i];
-    __syncthreads();
-    float* out = p.partial + (static_cast<int64_t>(blockIdx.x) * p.n_sums + x.slot) * p.dim;
-    for (int q = threadIdx.x; q < G * 2 * N; q += 256) {
-      const int l = q / (2 * N), i = q % (2 * N) / 2;
-      const Lane<KIND> to(l, p);
-      if (!to.any() || !to.own(i) || (q % 2 && !to.has_b(i))) continue;
-      float s = 0.0f;
-#pragma unroll 4
-      for (int g = 0; g < GROUPS; ++g) s += sums[g][l][q % (2 * N)];
-      out[q % 2 ? to.place_b(i) : to.place_a(i)] = s;
-    }
-    __syncthreads();  // before the next tensor's sums
   }
+  if (!x.sums) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) sums[group][lane][2 * i] = sa[i], sums[group][lane][2 * i + 1] = sb[i];
+  __syncthreads();
+  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.dim;
+  for (int q = threadIdx.x; q < G * 2 * N; q += 256) {
+    const int l = q / (2 * N), i = q % (2 * N) / 2;
+    const Lane<KIND> to(l, p);
+    if (!to.any() || !to.own(i) || (q % 2 && !to.has_b(i))) continue;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int g = 0; g < GROUPS; ++g) s += sums[g][l][q % (2 * N)];
+    out[q % 2 ? to.place_b(i) : to.place_a(i)] = s;
+  }
+}
+
+// Sums of the partial rows: q's of the first blocks_q, k's of the others. 32 threads a column take every 32nd row
+// each, and one adds their sums.
+constexpr int kSumCols = 32, kSumSlices = 32;
+__global__ __launch_bounds__(kSumCols * kSumSlices) void head_norm_sums_kernel(const float* partial, int blocks_q, int blocks,
+                                                                               int dim, float* dw_q, float* dw_k, int accumulate) {
+  __shared__ float sh[kSumSlices][kSumCols];
+  const int lane = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + lane;
+  float* dw = blockIdx.y ? dw_k : dw_q;
+  if (!dw) return;
+  const int first = blockIdx.y ? blocks_q : 0, end = blockIdx.y ? blocks : blocks_q;
+  float s = 0.0f;
+  if (c < dim) {
+#pragma unroll 8
+    for (int g = first + slice; g < end; g += kSumSlices) s += partial[static_cast<int64_t>(g) * dim + c];
+  }
+  sh[slice][lane] = s;
+  __syncthreads();
+  if (slice || c >= dim) return;
+#pragma unroll
+  for (int i = 1; i < kSumSlices; ++i) s += sh[i][lane];
+  dw[c] = accumulate ? dw[c] + s : s;
 }
 
 }  // namespace
@@ -457,25 +478,48 @@ hipError_t launch_head_norm_fwd(const HeadNormArgs& a, hipStream_t stream) {
   });
 }
 
-int64_t head_norm_bwd_blocks(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t) {
-  const int64_t most = tokens * (heads_q > heads_k ? heads_q : heads_k);
-  return most < 32 * 512 ? (most + 31) / 32 : 512;
+// Workgroups of q and k: 512 in all (two on a CU), fewer where there is not as much work, shared out by the heads.
+static void bwd_blocks(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t& q, int64_t& k) {
+  const int64_t heads = heads_q + heads_k, work = (tokens * heads + 31) / 32, all = work < 512 ? work : 512;
+  q = heads_q ? (all * heads_q + heads - 1) / heads : 0;
+  k = heads_k ? (all * heads_k + heads - 1) / heads : 0;
+}
+
+int64_t head_norm_bwd_blocks(int64_t tokens, int64_t heads_q, int64_t heads_k) {
+  int64_t q, k, most;
+  bwd_blocks(tokens, heads_q, heads_k, q, k);
+  most = q + k;
+  // one of the two alone, where the other's gradients are not wanted
+  bwd_blocks(tokens, heads_q, 0, q, k);
+  most = most < q ? q : most;
+  bwd_blocks(tokens, 0, heads_k, q, k);
+  return most < k ? k : most;
 }
 
 hipError_t launch_head_norm_bwd(HeadNormArgs a, float* const (&dw)[2], int accumulate, hipStream_t stream) {
-  float* outs[3] = {nullptr, nullptr, nullptr};
+  float* out[2];
   for (int k = 0; k < 2; ++k) {
-    a.t[k].slot = dw[k] && a.t[k].heads ? a.n_sums : -1;
-    if (a.t[k].slot >= 0) outs[a.n_sums++] = dw[k];
+    out[k] = a.t[k].heads ? dw[k] : nullptr;
+    a.t[k].sums = out[k] != nullptr;
   }
-  const int64_t blocks = head_norm_bwd_blocks(a.tokens, a.t[0].heads, a.t[1].heads, a.dim);
+  int64_t bq, bk;
+  bwd_blocks(a.tokens, a.t[0].heads, a.t[1].heads, bq, bk);
   const hipError_t e = by_shape(a, [&](auto kind, auto lanes, auto multi) {
-    hipLaunchKernelGGL((head_norm_bwd_kernel<decltype(kind)::value, decltype(lanes)::value, 2, decltype(multi)::value>),
-                       dim3(static_cast<uint32_t>(blocks)), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    auto go = [&](auto hc) {
+      hipLaunchKernelGGL(
+          (head_norm_bwd_kernel<decltype(kind)::value, decltype(lanes)::value, decltype(hc)::value, decltype(multi)::value>),
+          dim3(static_cast<uint32_t>(bq + bk)), dim3(256), 0, stream, a, static_cast<unsigned>(bq));
+      return hipGetLastError();
+    };
+    // two heads of a token share its angles where there is work enough to fill the card that way
+    const int64_t heads = a.tokens * (a.t[0].heads + a.t[1].heads);
+    return heads * decltype(lanes)::value >= 2 * 256 * 512 ? go(std::integral_constant<int, 2>{})
+                                                           : go(std::integral_constant<int, 1>{});
   });
-  if (e != hipSuccess || a.n_sums == 0) return e;
-  return launch_column_sums_deep(a.partial, static_cast<int>(blocks), a.n_sums * a.dim, a.dim, outs, accumulate, stream);
+  if (e != hipSuccess || (!out[0] && !out[1])) return e;
+  hipLaunchKernelGGL(head_norm_sums_kernel, dim3((a.dim + kSumCols - 1) / kSumCols, 2), dim3(kSumCols * kSumSlices), 0, stream,
+                     a.partial, static_cast<int>(bq), static_cast<int>(bq + bk), a.dim, out[0], out[1], accumulate);
+  return hipGetLastError();
 }
 
 }  // namespace pf8

@@ -507,10 +507,9 @@ __global__ __launch_bounds__(THREADS) void norm_bwd_kernel(NormBwdArgs a, int n_
   write_sum(Pre{}), write_sum(Post{}), write_sum(Gate{});
 }
 
-// Column sums of the workgroups' partial rows [groups][n_sums * cols], in a fixed order: 8 (or 32, for few columns of
-// many rows) threads per column take every eighth row each, and one adds their sums.
-constexpr int kSumCols = 32;
-template <int kSumSlices>
+// Column sums of the workgroups' partial rows [groups][n_sums * cols], in a fixed order: 8 threads
+// per column take every eighth row each, and one adds their eight sums.
+constexpr int kSumCols = 32, kSumSlices = 8;
 __global__ __launch_bounds__(kSumCols * kSumSlices) void norm_colsum_kernel(const float* partial, int groups, int width,
                                                                             int cols, float* o0, float* o1, float* o2,
                                                                             int accumulate) {
@@ -603,14 +602,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, hipStream_t stream) {
 
 hipError_t launch_column_sums(const float* partial, int groups, int width, int cols, float* const (&outs)[3],
                               int accumulate, hipStream_t stream) {
-  hipLaunchKernelGGL(norm_colsum_kernel<8>, dim3((width + kSumCols - 1) / kSumCols), dim3(kSumCols * 8), 0, stream,
-                     partial, groups, width, cols, outs[0], outs[1], outs[2], accumulate);
-  return hipGetLastError();
-}
-
-hipError_t launch_column_sums_deep(const float* partial, int groups, int width, int cols, float* const (&outs)[3],
-                                   int accumulate, hipStream_t stream) {
-  hipLaunchKernelGGL(norm_colsum_kernel<32>, dim3((width + kSumCols - 1) / kSumCols), dim3(kSumCols * 32), 0, stream,
+  hipLaunchKernelGGL(norm_colsum_kernel, dim3((width + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumSlices), 0, stream,
                      partial, groups, width, cols, outs[0], outs[1], outs[2], accumulate);
   return hipGetLastError();
 }

@@ -18,7 +18,7 @@ struct HeadTensor {
   int64_t out_st, out_sh;
   const void* w;  // or null: no norm
   int heads;      // 0: no such tensor
-  int slot;       // backward: which row of partial sums is this weight's; -1: none (the launcher fills it in)
+  int sums;       // backward: the weight's gradient is wanted (the launcher fills it in)
 };
 
 struct HeadNormArgs {
@@ -37,15 +37,14 @@ struct HeadNormArgs {
   int share[kHeadMaxAxes];  // blocked: the first pair behind axis a; cycled: axes * sections[a]
   int cycled, interleaved;
   float scale;
-  int n_sums;      // backward: weights' gradients wanted (the launcher fills it in)
-  float* partial;  // backward: [blocks][n_sums][dim]
+  float* partial;  // backward: [blocks][dim]
 };
 
 hipError_t launch_head_norm_fwd(const HeadNormArgs& args, hipStream_t stream);
 // dw: q's and k's, null where not wanted
 hipError_t launch_head_norm_bwd(HeadNormArgs args, float* const (&dw)[2], int accumulate, hipStream_t stream);
 // Workgroups of the backward pass, each with one row of partial sums.
-int64_t head_norm_bwd_blocks(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t dim);
+int64_t head_norm_bwd_blocks(int64_t tokens, int64_t heads_q, int64_t heads_k);
 
 struct ActBwdArgs {
   int64_t rows;
@@ -57,10 +56,12 @@ struct ActBwdArgs {
   int act, gated;
   uint16_t* dz;  // or null
   int64_t lddz;
-  float* partial;  // [groups][cols or 2 cols], or null where no sums are wanted
+  float* dbias;    // [cols or 2 cols], or null where no sums are wanted
+  int accumulate;
+  float* partial;  // [groups][cols or 2 cols]
 };
 
-hipError_t launch_act_bwd(const ActBwdArgs& args, float* dbias, int accumulate, hipStream_t stream);
+hipError_t launch_act_bwd(const ActBwdArgs& args, hipStream_t stream);
 int64_t act_bwd_groups(int64_t rows, int64_t cols);
 
 // The forward product with its epilogue; d is [m, gated ? n / 2 : n].

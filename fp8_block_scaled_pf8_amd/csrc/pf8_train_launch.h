@@ -61,9 +61,6 @@ int64_t norm_bwd_groups(int64_t rows, int64_t cols);
 // Column sums of partial rows [groups][width], in a fixed order, into outs[c / cols][c % cols]; accumulate: added.
 hipError_t launch_column_sums(const float* partial, int groups, int width, int cols, float* const (&outs)[3],
                               int accumulate, hipStream_t stream);
-// The same with four times the threads a column, in another (as fixed) order: few columns of many rows.
-hipError_t launch_column_sums_deep(const float* partial, int groups, int width, int cols, float* const (&outs)[3],
-                                   int accumulate, hipStream_t stream);
 
 // Newton-Schulz orthogonalisation; the launcher fills in what lies in the workspace.
 struct NsArgs {
