@@ -19,6 +19,8 @@ from ._lib import (
     PF8_WGRAD,
     pf8_abi_version,
     pf8_act_bwd,
+    pf8_act_bwd_quant,
+    pf8_act_bwd_quant_workspace,
     pf8_act_bwd_workspace,
     pf8_block_gemm,
     pf8_block_gemm_f32,
@@ -39,7 +41,7 @@ from ._lib import (
     pf8_quant_w_128x128,
     pf8_strerror,
 )
-from .epilogue import ActGrads, act_backward, fprop_act
+from .epilogue import ActGrads, ActQuantGrads, act_backward, act_backward_quant, fprop_act
 from .heads import (QKNormRope, QKNormRopeFunction, QKNormRopeGrads, fp8_qk_norm_rope, qk_norm_rope,
                     qk_norm_rope_backward)
 from .linear import Fp8Linear, Fp8LinearActFunction, Fp8LinearFunction, fp8_linear, fp8_linear_act
@@ -61,5 +63,6 @@ __all__ = [
     "fp8_block_norm", "pf8_newton_schulz", "pf8_newton_schulz_workspace", "newton_schulz",
     "pf8_qk_norm_rope", "pf8_qk_norm_rope_bwd", "pf8_qk_norm_rope_bwd_workspace", "pf8_act_bwd", "pf8_act_bwd_workspace",
     "QKNormRope", "QKNormRopeFunction", "QKNormRopeGrads", "fp8_qk_norm_rope", "qk_norm_rope", "qk_norm_rope_backward",
-    "pf8_fprop_act", "ActGrads", "act_backward", "fprop_act",
+    "pf8_fprop_act", "pf8_act_bwd_quant", "pf8_act_bwd_quant_workspace",
+    "ActGrads", "ActQuantGrads", "act_backward", "act_backward_quant", "fprop_act",
 ]

@@ -86,6 +86,10 @@ LAYER_SIGNATURES = {
     "pf8_act_bwd": (
         _int, [_i64, _i64, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp, _int, _vp, _i64, _vp]),
     "pf8_act_bwd_workspace": (_i64, [_i64, _i64, _int]),
+    "pf8_act_bwd_quant": (
+        _int, [_i64, _i64, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _vp, _i64,
+               _vp]),
+    "pf8_act_bwd_quant_workspace": (_i64, [_i64, _i64, _int]),
     "pf8_fprop_act": (
         _int, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _int, _int, _vp, _i64, _vp, _i64,
                _vp, _i64, _vp]),
@@ -188,6 +192,8 @@ pf8_qk_norm_rope_bwd = LIB.pf8_qk_norm_rope_bwd
 pf8_qk_norm_rope_bwd_workspace = LIB.pf8_qk_norm_rope_bwd_workspace
 pf8_act_bwd = LIB.pf8_act_bwd
 pf8_act_bwd_workspace = LIB.pf8_act_bwd_workspace
+pf8_act_bwd_quant = LIB.pf8_act_bwd_quant
+pf8_act_bwd_quant_workspace = LIB.pf8_act_bwd_quant_workspace
 pf8_fprop_act = LIB.pf8_fprop_act
 
 

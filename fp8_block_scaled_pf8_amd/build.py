@@ -18,7 +18,7 @@ from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
-SOURCES = ["quant.hip", "gemm.hip", "norm.hip", "newton_schulz.hip", "head_norm.hip", "act.hip", "gemm_act.hip",
+SOURCES = ["quant.hip", "gemm.hip", "norm.hip", "newton_schulz.hip", "head_norm.hip", "act.hip", "act_quant.hip", "gemm_act.hip",
            "gemm_act_256.hip", "gemm_act_128.hip", "abi.hip", "abi_train.hip", "abi_layer.hip"]
 LIB_NAME = "libpf8.so"
 ARCH = "gfx950"

@@ -199,6 +199,40 @@ pf8_status pf8_act_bwd(int64_t rows, int64_t cols, const void* dd, int64_t lddd,
   return launch_status(pf8::launch_act_bwd(a, static_cast<hipStream_t>(hip_stream)));
 }
 
+int64_t pf8_act_bwd_quant_workspace(int64_t rows, int64_t cols, int gated) {
+  if (rows <= 0 || cols <= 0 || (gated != 0 && gated != 1) || any_too_big(rows, cols) ||
+      any_too_big((gated ? 2 : 1) * cols) || rows % 128 || cols % 128 || rows / 128 > 65535)
+    return 0;
+  return rows / 128 * (gated ? 2 : 1) * cols * 4;
+}
+
+pf8_status pf8_act_bwd_quant(int64_t rows, int64_t cols, const void* dd, int64_t lddd, const void* z, int64_t ldz,
+                             pf8_activation activation, int gated, void* q_row, int64_t ldq_row, float* dscale_row,
+                             int64_t ld_sr, void* q_col, int64_t ldq_col, float* dscale_col, int64_t ld_sc,
+                             float* dbias, int accumulate, void* workspace, int64_t workspace_bytes, void* hip_stream) {
+  if (!dd || !q_row || !dscale_row || !q_col || !dscale_col || rows <= 0 || cols <= 0) return PF8_EINVAL;
+  if ((gated != 0 && gated != 1) || (accumulate != 0 && accumulate != 1)) return PF8_EINVAL;
+  if (activation < PF8_ACT_NONE || activation > PF8_ACT_GELU_TANH || (gated && activation == PF8_ACT_NONE) ||
+      (!z) != (activation == PF8_ACT_NONE))
+    return PF8_EINVAL;
+  if (any_too_big(rows, cols, lddd, z ? ldz : 0, ldq_row, ld_sr, ldq_col, ld_sc)) return PF8_ESHAPE;
+  const int64_t width = gated ? 2 * cols : cols;
+  if (lddd < cols || (z && ldz < width) || ldq_row < width || ld_sr < rows || ldq_col < rows || ld_sc < width)
+    return PF8_EINVAL;
+  if (rows % 128 || cols % 128 || rows / 128 > 65535 || width > kMaxDim) return PF8_ESHAPE;
+  if (dbias && (!workspace || workspace_bytes < pf8_act_bwd_quant_workspace(rows, cols, gated))) return PF8_EINVAL;
+  if (!aligned(dd, 16) || lddd % 8 || !aligned(z, 16) || (z && ldz % 8) || !aligned(q_row, 16) || ldq_row % 16 ||
+      !aligned(q_col, 16) || ldq_col % 16 || !aligned(dscale_row, 4) || !aligned(dscale_col, 4) || !aligned(dbias, 4) ||
+      (dbias && !aligned(workspace, 16)))
+    return PF8_EALIGN;
+  if (int e = device_status()) return e;
+  const pf8::ActQuantArgs a{rows, cols, static_cast<const uint16_t*>(dd), lddd, static_cast<const uint16_t*>(z), ldz,
+                            activation, gated, static_cast<uint8_t*>(q_row), ldq_row, dscale_row, ld_sr,
+                            static_cast<uint8_t*>(q_col), ldq_col, dscale_col, ld_sc, dbias, accumulate,
+                            static_cast<float*>(workspace)};
+  return launch_status(pf8::launch_act_bwd_quant(a, static_cast<hipStream_t>(hip_stream)));
+}
+
 pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* a_dscale,
                          int64_t ld_as, const void* b, int64_t ldb, const float* b_dscale, int64_t ld_bs,
                          const void* bias, pf8_dtype btype, pf8_activation activation, int gated,

@@ -272,47 +272,50 @@ __global__ __launch_bounds__(256) void head_norm_fwd_kernel(HeadNormArgs p, unsi
   const int second = blockIdx.x >= blocks_q;
   const HeadTensor x = second ? p.t[1] : p.t[0];
   const Items items(p.tokens, x.heads, HC);
-  const int64_t item = static_cast<int64_t>(blockIdx.x - (second ? blocks_q : 0)) * (256 / G) + threadIdx.x / G;
-  if (item >= items.count) return;
   const Lane<KIND> at(threadIdx.x % G, p);
-  const uint32_t token = static_cast<uint32_t>(item) / static_cast<uint32_t>(items.per_token);
-  const int head = (static_cast<int>(item) - static_cast<int>(token) * items.per_token) * HC;
+  const unsigned block = blockIdx.x - (second ? blocks_q : 0), blocks = second ? gridDim.x - blocks_q : blocks_q;
+  // (one item each, but for tensors of more than 2^22 workgroups)
+  for (int64_t item = static_cast<int64_t>(block) * (256 / G) + threadIdx.x / G; item < items.count;
+       item += static_cast<int64_t>(blocks) * (256 / G)) {
+    const uint32_t token = static_cast<uint32_t>(item) / static_cast<uint32_t>(items.per_token);
+    const int head = (static_cast<int>(item) - static_cast<int>(token) * items.per_token) * HC;
 
-  typename Lane<KIND>::Raw raw[HC];
-  const uint16_t* src = x.x + token * x.x_st + head * x.x_sh;
+    typename Lane<KIND>::Raw raw[HC];
+    const uint16_t* src = x.x + token * x.x_st + head * x.x_sh;
 #pragma unroll
-  for (int j = 0; j < HC; ++j) {
-    raw[j] = Lane<KIND>::none();
-    if (head + j < x.heads && at.any()) raw[j] = at.load(src + j * x.x_sh);
-  }
-  const Turns<KIND, MULTI> turns(at, p);
-  float c[N], s[N], wa[N], wb[N];
-  turns.at(token, at, p, c, s);
-  head_weights(x.w, p, at, wa, wb);
-  uint16_t* dst = x.out + token * x.out_st + head * x.out_sh;
+    for (int j = 0; j < HC; ++j) {
+      raw[j] = Lane<KIND>::none();
+      if (head + j < x.heads && at.any()) raw[j] = at.load(src + j * x.x_sh);
+    }
+    const Turns<KIND, MULTI> turns(at, p);
+    float c[N], s[N], wa[N], wb[N];
+    turns.at(token, at, p, c, s);
+    head_weights(x.w, p, at, wa, wb);
+    uint16_t* dst = x.out + token * x.out_st + head * x.out_sh;
 #pragma unroll
-  for (int j = 0; j < HC; ++j) {
-    if (head + j >= x.heads) break;
-    float a[N], b[N];
-    Lane<KIND>::unpack(raw[j], a, b);
-    if (x.w) {
-      float sum = 0.0f;
+    for (int j = 0; j < HC; ++j) {
+      if (head + j >= x.heads) break;
+      float a[N], b[N];
+      Lane<KIND>::unpack(raw[j], a, b);
+      if (x.w) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float u = a[i] * p.sq, v = b[i] * p.sq;
+          const float both = __builtin_fmaf(u, u, v * v);
+          if (at.own(i)) sum += both;
+        }
+        const float rho = inv_root(__builtin_fmaf(group_sum<G>(sum), p.inv_sum, p.eps));
+#pragma unroll
+        for (int i = 0; i < N; ++i) a[i] = a[i] * rho * wa[i], b[i] = b[i] * rho * wb[i];
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float u = a[i] * p.sq, v = b[i] * p.sq;
-        const float both = __builtin_fmaf(u, u, v * v);
-        if (at.own(i)) sum += both;
+        const float u = a[i] * c[i] - b[i] * s[i], v = a[i] * s[i] + b[i] * c[i];
+        a[i] = at.rot(i) ? u : a[i], b[i] = at.rot(i) ? v : b[i];
       }
-      const float rho = inv_root(__builtin_fmaf(group_sum<G>(sum), p.inv_sum, p.eps));
-#pragma unroll
-      for (int i = 0; i < N; ++i) a[i] = a[i] * rho * wa[i], b[i] = b[i] * rho * wb[i];
+      if (at.any()) at.store(dst + j * x.out_sh, a, b);
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float u = a[i] * c[i] - b[i] * s[i], v = a[i] * s[i] + b[i] * c[i];
-      a[i] = at.rot(i) ? u : a[i], b[i] = at.rot(i) ? v : b[i];
-    }
-    if (at.any()) at.store(dst + j * x.out_sh, a, b);
   }
 }
 
@@ -466,7 +469,10 @@ hipError_t launch_head_norm_fwd(const HeadNormArgs& a, hipStream_t stream) {
     constexpr int G = decltype(lanes)::value;
     auto go = [&](auto hc) {
       constexpr int HC = decltype(hc)::value;
-      auto blocks = [&](int heads) { return (a.tokens * ((heads + HC - 1) / HC) + 256 / G - 1) / (256 / G); };
+      auto blocks = [&](int heads) {
+        const int64_t all = (a.tokens * ((heads + HC - 1) / HC) + 256 / G - 1) / (256 / G), most = int64_t{1} << 22;
+        return all < most ? all : most;  // (a grid has under 2^32 threads)
+      };
       const int64_t bq = blocks(a.t[0].heads), bk = blocks(a.t[1].heads);
       hipLaunchKernelGGL((head_norm_fwd_kernel<decltype(kind)::value, G, HC, decltype(multi)::value>),
                          dim3(static_cast<uint32_t>(bq + bk)), dim3(256), 0, stream, a, static_cast<unsigned>(bq));

@@ -64,6 +64,28 @@ struct ActBwdArgs {
 hipError_t launch_act_bwd(const ActBwdArgs& args, hipStream_t stream);
 int64_t act_bwd_groups(int64_t rows, int64_t cols);
 
+struct ActQuantArgs {
+  int64_t rows, cols;  // of dd: multiples of 128
+  const uint16_t* dd;
+  int64_t lddd;
+  const uint16_t* z;
+  int64_t ldz;
+  int act, gated;
+  uint8_t* q_row;
+  int64_t ldq_row;
+  float* s_row;
+  int64_t ld_sr;
+  uint8_t* q_col;
+  int64_t ldq_col;
+  float* s_col;
+  int64_t ld_sc;
+  float* dbias;
+  int accumulate;
+  float* partial;  // [rows / 128][cols or 2 cols]
+};
+
+hipError_t launch_act_bwd_quant(const ActQuantArgs& args, hipStream_t stream);
+
 // The forward product with its epilogue; d is [m, gated ? n / 2 : n].
 struct FpropActArgs {
   int64_t m, n, k;

@@ -14,7 +14,7 @@ import torch
 
 from . import _lib as L
 from .norm import _call, _may_write, _rows, _rows_at, _rows_meet, _vector
-from .ops import GROUP, out_pitch
+from .ops import GROUP, code_buffer, out_pitch
 
 Tensor = torch.Tensor
 
@@ -25,6 +25,15 @@ ACTIVATIONS = {None: L.PF8_ACT_NONE, "relu": L.PF8_ACT_RELU, "relu2": L.PF8_ACT_
 class ActGrads(NamedTuple):
     """Gradients of an activation: bf16 dz; float32 dbias, the column sums of dz before its rounding."""
     dz: Tensor
+    dbias: Optional[Tensor]
+
+
+class ActQuantGrads(NamedTuple):
+    """An activation's gradient as ``quant_act_dual`` has it: codes and scales along the rows, and transposed; dbias."""
+    q: Tensor
+    s: Tensor
+    qt: Tensor
+    st: Tensor
     dbias: Optional[Tensor]
 
 
@@ -138,6 +147,25 @@ def fprop_act(qx: Tensor, sx: Tensor, qw: Tensor, sw: Tensor, bias: Optional[Ten
     return out if z is None else (out, z)
 
 
+def _dbias(bias_grad, dbias_out, accumulate, width, dev) -> Tuple[Optional[Tensor], int]:
+    """A bias's gradient, new or as given, and its address."""
+    if not bias_grad:
+        if dbias_out is not None or accumulate:
+            raise ValueError("dbias_out and accumulate need bias_grad")
+        return None, 0
+    if dbias_out is not None:
+        return dbias_out, _vector(dbias_out, "dbias_out", width, torch.float32, dev)
+    if accumulate:
+        raise ValueError("accumulate needs dbias_out")
+    dbias = torch.empty(width, dtype=torch.float32, device=dev)
+    return dbias, dbias.data_ptr()
+
+
+def _alone(dbias_out: Optional[Tensor], dd: Tensor, z: Optional[Tensor]) -> None:
+    if dbias_out is not None and any(_rows_meet(_rows_at(dbias_out), _rows_at(t)) for t in (dd, z) if t is not None):
+        raise ValueError("dbias_out overlaps another operand")
+
+
 def act_backward(dd: Tensor, z: Optional[Tensor], activation: Optional[str], gated: bool = False,
                  bias_grad: bool = False, dz_out: Optional[Tensor] = None, dbias_out: Optional[Tensor] = None,
                  accumulate: bool = False) -> ActGrads:
@@ -176,29 +204,54 @@ def act_backward(dd: Tensor, z: Optional[Tensor], activation: Optional[str], gat
         else:
             dz = dz_out
             po, ldo = _rows(dz_out, "dz_out", shape, dev)
-    dbias, pb, ws, nws = None, 0, None, 0
-    if bias_grad:
-        dbias = dbias_out
-        if dbias is None:
-            if accumulate:
-                raise ValueError("accumulate needs dbias_out")
-            dbias = torch.empty(width, dtype=torch.float32, device=dev)
-            pb = dbias.data_ptr()
-        else:
-            pb = _vector(dbias_out, "dbias_out", width, torch.float32, dev)
-    elif dbias_out is not None or accumulate:
-        raise ValueError("dbias_out and accumulate need bias_grad")
+    dbias, pb = _dbias(bias_grad, dbias_out, accumulate, width, dev)
     if rows == 0:
         if bias_grad and not accumulate:
             dbias.zero_()
         return ActGrads(dz, dbias)
     if dz_out is not None:
         _may_write(dz_out, "dz_out", [(z, True), (dd, not gated), (dbias, False)])
-    if dbias_out is not None and any(_rows_meet(_rows_at(dbias), _rows_at(t)) for t in (dd, z) if t is not None):
-        raise ValueError("dbias_out overlaps another operand")
+    _alone(dbias_out, dd, z)
+    ws, nws = None, 0
     if bias_grad:
         nws = L.pf8_act_bwd_workspace(rows, cols, int(gated))
         ws = torch.empty(nws, dtype=torch.uint8, device=dev)
     _call(L.pf8_act_bwd, dev, rows, cols, pd, ldd, pz, ldz, code, int(gated), po, ldo, pb, int(accumulate),
           0 if ws is None else ws.data_ptr(), nws)
     return ActGrads(dz, dbias)
+
+
+def act_backward_quant(dd: Tensor, z: Optional[Tensor], activation: Optional[str], gated: bool = False,
+                       bias_grad: bool = False, dbias_out: Optional[Tensor] = None, accumulate: bool = False
+                       ) -> ActQuantGrads:
+    """``act_backward`` with dz as the codes of both groupings, what ``dgrad`` and ``wgrad`` take.
+
+    Bit for bit ``quant_act_dual(act_backward(...).dz)``, without dz in memory; rows and columns of dd are multiples of
+    128. Without an activation the codes are those of dd, and z is None. dbias comes as from ``act_backward``, its sums
+    formed in another fixed order.
+    """
+    if not isinstance(dd, Tensor) or dd.dim() != 2:
+        raise ValueError("dd must be a 2-D tensor")
+    if not dd.is_cuda:
+        raise ValueError("dd must be on a HIP device")
+    code = _activation(activation, gated)
+    (rows, cols), dev = dd.shape, dd.device
+    if rows % GROUP or cols % GROUP or not rows or not cols:
+        raise ValueError(f"act_backward_quant needs multiples of {GROUP} rows and columns, got {tuple(dd.shape)}")
+    if (z is None) != (code == 0):
+        raise ValueError("z comes with an activation")
+    width = 2 * cols if gated else cols
+    pd, ldd = _aligned_rows(dd, "dd", dd.shape, dev)
+    pz, ldz = (0, 0) if z is None else _aligned_rows(z, "z", torch.Size((rows, width)), dev)
+    dbias, pb = _dbias(bias_grad, dbias_out, accumulate, width, dev)
+    _alone(dbias_out, dd, z)
+    q, qt = code_buffer(rows, width, dev), code_buffer(width, rows, dev)
+    s = torch.empty((width // GROUP, rows), dtype=torch.float32, device=dev)
+    st = torch.empty((rows // GROUP, width), dtype=torch.float32, device=dev)
+    ws, nws = None, 0
+    if bias_grad:
+        nws = L.pf8_act_bwd_quant_workspace(rows, cols, int(gated))
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    _call(L.pf8_act_bwd_quant, dev, rows, cols, pd, ldd, pz, ldz, code, int(gated), q.data_ptr(), q.stride(0), s.data_ptr(),
+          rows, qt.data_ptr(), qt.stride(0), st.data_ptr(), width, pb, int(accumulate), 0 if ws is None else ws.data_ptr(), nws)
+    return ActQuantGrads(q, s, qt, st, dbias)

@@ -20,7 +20,7 @@ update through ``weight.data`` bypasses that counter; call ``invalidate_weight_c
 Bias, activation and residual: ``fp8_linear_act`` and an ``Fp8Linear`` made with them run the product's
 epilogue (``epilogue.fprop_act``): d = act(X . W^T + bias) + residual, or gated act(g) * u + residual from the
 two halves of W's rows. For an activation the backward pass keeps z = X . W^T + bias in BF16; its gradient dz
-(``epilogue.act_backward``, with the bias's in FP32) takes dY's place above. ``Fp8Linear.infer`` runs any number of
+(``epilogue.act_backward_quant``, with the bias's in FP32) is made as codes and takes dY's place above. ``Fp8Linear.infer`` runs any number of
 tokens without gradients.
 
 Tokens (the product of the leading dimensions), N and K must be multiples of 128. Zero tokens give
@@ -157,22 +157,24 @@ class Fp8LinearActFunction(torch.autograd.Function):
         qxt, sxt, qwt, sw, z = ctx.saved_tensors
         n = qwt.shape[1]
         dz = _rows(dd.to(torch.bfloat16), n // 2 if ctx.gated else n)
-        dbias = None
-        if z is not None or need[2]:
-            add = need[2] and ctx.bias_main_grad is not None
-            g = epilogue.act_backward(dz, z, ctx.activation, ctx.gated, bias_grad=need[2],
-                                      dbias_out=ctx.bias_main_grad if add else None, accumulate=add)
-            dz, dbias = g.dz, None if add or g.dbias is None else g.dbias.to(ctx.bias)
-        dx = dw = None
-        if need[0] or need[1]:
+        if not any(need[:3]):
+            return (None, None, None, dres, *none)
+        add = need[2] and ctx.bias_main_grad is not None
+        bias = dict(bias_grad=need[2], dbias_out=ctx.bias_main_grad if add else None, accumulate=add)
+        if dz.shape[1] % GROUP:  # a gate over an odd number of 64 columns: a scale's columns are of both halves
+            dz, dbias = epilogue.act_backward(dz, z, ctx.activation, ctx.gated, **bias)
             qdz, sdz, qdzt, sdzt = ops.quant_act_dual(dz)
-            if need[0]:
-                dx = ops.dgrad(qdz, sdz, qwt, sw, out=torch.empty((dz.shape[0], ctx.k), dtype=torch.bfloat16,
-                                                                  device=dz.device)).reshape(*ctx.lead, ctx.k)
-            if need[1] and ctx.main_grad is not None:
-                ops.wgrad_f32(qdzt, sdzt, qxt, sxt, out=ctx.main_grad, accumulate=True)
-            elif need[1]:
-                dw = ops.wgrad(qdzt, sdzt, qxt, sxt, out=torch.empty((n, ctx.k), dtype=torch.bfloat16, device=dz.device))
+        else:
+            qdz, sdz, qdzt, sdzt, dbias = epilogue.act_backward_quant(dz, z, ctx.activation, ctx.gated, **bias)
+        dbias = None if add or dbias is None else dbias.to(ctx.bias)
+        dx = dw = None
+        if need[0]:
+            dx = ops.dgrad(qdz, sdz, qwt, sw, out=torch.empty((dz.shape[0], ctx.k), dtype=torch.bfloat16,
+                                                              device=dz.device)).reshape(*ctx.lead, ctx.k)
+        if need[1] and ctx.main_grad is not None:
+            ops.wgrad_f32(qdzt, sdzt, qxt, sxt, out=ctx.main_grad, accumulate=True)
+        elif need[1]:
+            dw = ops.wgrad(qdzt, sdzt, qxt, sxt, out=torch.empty((n, ctx.k), dtype=torch.bfloat16, device=dz.device))
         return (dx, dw, dbias, dres, *none)
 
 
@@ -256,11 +258,12 @@ class Fp8Linear(torch.nn.Module):
             torch.nn.init.normal_(weight, std=0.02)
         self.weight = torch.nn.Parameter(weight)
         self.activation, self.gated = activation, bool(gated)
-        self.bias = torch.nn.Parameter(torch.zeros(out_features, dtype=bias_dtype, device=self.weight.device)) if bias else None
+        rows = self.weight.shape[0]
+        self.bias = torch.nn.Parameter(torch.zeros(rows, dtype=bias_dtype, device=self.weight.device)) if bias else None
         if fp32_main_grad:
             self.weight.main_grad = torch.zeros(self.weight.shape, dtype=torch.float32, device=self.weight.device)
             if bias:
-                self.bias.main_grad = torch.zeros(out_features, dtype=torch.float32, device=self.weight.device)
+                self.bias.main_grad = torch.zeros(rows, dtype=torch.float32, device=self.weight.device)
         self._codes = None
         self._codes_key = None
         self._codes_ready = None  # event recorded on the stream that made the codes

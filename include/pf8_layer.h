@@ -59,7 +59,7 @@ typedef int pf8_activation;
  * fraction of a turn from FP64 (right at any position below 2^52), one rounding to BF16 at the end.
  *
  * q, k: bf16 [tokens, heads, head_dim] with strides _st between tokens and _sh between heads, head
- *   values contiguous. k NULL (with heads_k 0): queries alone. 1 <= head_dim <= 512.
+ *   values contiguous. k NULL (with heads_k 0): queries alone. 1 <= head_dim <= 512, tokens * heads < 2^31.
  * w_q, w_k: [head_dim] of wtype (PF8_BF16 or PF8_F32), or NULL: no norm of that tensor.
  * positions: integers of ptype; that of a token on an axis at token * pos_st + axis * pos_sa. NULL (with
  *   pairs 0): no rotation. Positions are not checked.
@@ -126,6 +126,24 @@ pf8_status pf8_act_bwd(int64_t rows, int64_t cols, const void* dd, int64_t lddd,
 
 /* Bytes of the workspace of pf8_act_bwd; 0 for sizes that it refuses. Needs no device. */
 int64_t pf8_act_bwd_workspace(int64_t rows, int64_t cols, int gated);
+
+/*
+ * pf8_act_bwd with dz as the codes of both groupings, for the data and the weight gradient: exactly
+ * pf8_act_bwd (dz rounded to BF16), then pf8_quant_act_dual of that dz, without dz in memory.
+ *
+ * rows and cols are multiples of 128. dd, z: 16-byte aligned, pitches multiples of 8. With width = cols, or 2 cols
+ * with a gate: q_row [rows, width], dscale_row[g * ld_sr + r], q_col [width, rows], dscale_col[g * ld_sc + c], as
+ * pf8_quant_act_dual writes them (16-byte aligned codes with pitches of multiples of 16). z NULL with
+ * PF8_ACT_NONE: the codes of dd. dbias as in pf8_act_bwd, its sums formed in another fixed order; workspace of
+ * pf8_act_bwd_quant_workspace bytes where it is wanted.
+ */
+pf8_status pf8_act_bwd_quant(int64_t rows, int64_t cols, const void* dd, int64_t lddd, const void* z, int64_t ldz,
+                             pf8_activation activation, int gated, void* q_row, int64_t ldq_row, float* dscale_row,
+                             int64_t ld_sr, void* q_col, int64_t ldq_col, float* dscale_col, int64_t ld_sc,
+                             float* dbias, int accumulate, void* workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* Bytes of the workspace of pf8_act_bwd_quant; 0 for sizes that it refuses. Needs no device. */
+int64_t pf8_act_bwd_quant_workspace(int64_t rows, int64_t cols, int gated);
 
 /*
  * Block-scaled FP8 product with bias, activation and residual in its epilogue:

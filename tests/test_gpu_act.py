@@ -156,3 +156,75 @@ def test_no_rows_and_refusals():
         pf8.act_backward(buf[:, :64], z, "silu", dz_out=buf[:, 32:96])
     with pytest.raises(ValueError, match="overlap"):
         pf8.act_backward(buf[:, :64], buf[:, 64:192], "silu", gated=True, dz_out=buf[:, 63:191])
+
+
+@pytest.mark.parametrize("act", ACTS + [None])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,cols", [(128, 128), (256, 384), (640, 128), (1152, 256)])
+def test_codes_are_the_quantised_gradient(act, gated, rows, cols):
+    """Codes and scales equal those of the two steps bit for bit; the bias's sums to the tolerance above."""
+    if gated and act is None:
+        pytest.skip("a gate needs an activation")
+    w = 2 * cols if gated else cols
+    buf = _rand((rows, cols + w + 24), 11, 2.0)
+    dd, z = buf[:, 8:8 + cols], None if act is None else buf[:, cols + 16:cols + 16 + w]
+    dd[3, :] = 0  # a row and a column group without a value
+    dd[:128, 5] = 0
+    keep = buf.clone()
+    two = pf8.act_backward(dd, z, act, gated=gated, bias_grad=True)
+    want = pf8.quant_act_dual(two.dz.contiguous())
+    got = pf8.act_backward_quant(dd, z, act, gated=gated, bias_grad=True)
+    for a, b in zip(got[:4], want):
+        assert a.shape == b.shape and torch.equal(a, b)
+    _check(dd, z, act, gated, pf8.ActGrads(two.dz, got.dbias))
+    plain = pf8.act_backward_quant(dd, z, act, gated=gated)
+    assert plain.dbias is None and all(torch.equal(a, b) for a, b in zip(plain[:4], want))
+    assert torch.equal(buf, keep)
+
+
+def test_codes_of_values_that_are_no_numbers():
+    rows, cols = 128, 256
+    dd, z = _rand((rows, cols), 1), _rand((rows, 2 * cols), 2)
+    dd[1, 7], z[5, 9], z[6, 300], z[7, 11] = float("nan"), float("inf"), float("-inf"), float("nan")
+    want = pf8.quant_act_dual(pf8.act_backward(dd, z, "silu", gated=True).dz)
+    got = pf8.act_backward_quant(dd, z, "silu", gated=True)
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], want))
+
+
+def test_codes_accumulate_replay_and_another_stream():
+    dd, z = _rand((384, 256), 1), _rand((384, 512), 2)
+    a = pf8.act_backward_quant(dd, z, "gelu", gated=True, bias_grad=True)
+    base = torch.ones(512, dtype=torch.float32, device=DEV)
+    c = pf8.act_backward_quant(dd, z, "gelu", gated=True, bias_grad=True, dbias_out=base, accumulate=True)
+    assert c.dbias is base and torch.equal(base, 1 + a.dbias)
+    one = torch.full((512,), 2.0, dtype=torch.float32, device=DEV)  # a single row of tiles adds without partial sums
+    s = pf8.act_backward_quant(dd[:128], z[:128], "gelu", gated=True, bias_grad=True)
+    pf8.act_backward_quant(dd[:128], z[:128], "gelu", gated=True, bias_grad=True, dbias_out=one, accumulate=True)
+    assert torch.equal(one, 2 + s.dbias)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        b = pf8.act_backward_quant(dd, z, "gelu", gated=True, bias_grad=True)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = pf8.act_backward_quant(dd, z, "gelu", gated=True, bias_grad=True)
+    for i in range(3):
+        dd.copy_(_rand((384, 256), 20 + i))
+        graph.replay()
+        e = pf8.act_backward_quant(dd, z, "gelu", gated=True, bias_grad=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(g, e))
+
+
+def test_codes_refusals():
+    dd, z = _rand((128, 128), 1), _rand((128, 128), 2)
+    bad = [dict(dd=dd[:64], z=z[:64]), dict(dd=dd[:0], z=z[:0]), dict(dd=dd[:, :64], z=z[:, :64]), dict(z=None),
+           dict(activation=None), dict(gated=True), dict(dbias_out=torch.zeros(128, device=DEV)), dict(accumulate=True),
+           dict(dd=_rand((128, 136), 3)[:, 1:129]), dict(z=_rand((128, 132), 3)[:, :128])]
+    for kw in bad:
+        with pytest.raises((ValueError, TypeError)):
+            pf8.act_backward_quant(**{**dict(dd=dd, z=z, activation="silu"), **kw})
+    with pytest.raises((ValueError, TypeError)):
+        pf8.act_backward_quant(dd.cpu(), z, "silu")

@@ -39,7 +39,10 @@ def test_linear_layer_is_its_steps(activation, gated, bias, residual):
     assert torch.equal(d.reshape(m, cols), want)
     dz, dbias = dd.reshape(m, cols), None
     if activation is not None or b is not None:
-        dz, dbias = pf8.act_backward(dz, z if activation else None, activation, gated, bias_grad=b is not None)
+        z = z if activation else None
+        if b is not None:
+            dbias = pf8.act_backward_quant(dz, z, activation, gated, bias_grad=True).dbias
+        dz = pf8.act_backward(dz, z, activation, gated, bias_grad=b is not None).dz
     q, s, qt, st = pf8.quant_act_dual(dz)
     assert torch.equal(x.grad.reshape(m, k), pf8.dgrad(q, s, qwt, sw))
     assert torch.equal(w.grad, pf8.wgrad(qt, st, qxt, sxt))
@@ -47,6 +50,37 @@ def test_linear_layer_is_its_steps(activation, gated, bias, residual):
         assert torch.equal(b.grad, dbias.to(bias))
     if r is not None:
         assert torch.equal(r.grad, dd)
+
+
+@pytest.mark.parametrize("n", [128, 384])
+def test_gate_over_half_a_group(n):
+    """A gate's half may end inside a scale's 128 columns; the layer still is its steps."""
+    m, k = 128, 256
+    x, w, b = _rand((m, k), 1).requires_grad_(), _rand((n, k), 2, 0.05).requires_grad_(), _rand((n,), 3).requires_grad_()
+    dd = _rand((m, n // 2), 5, 1e-2)
+    pf8.fp8_linear_act(x, w, b, "silu", True).backward(dd)
+    qx, sx, qxt, sxt = pf8.quant_act_dual(x.detach())
+    qw, qwt, sw = pf8.quant_w_128x128(w.detach())
+    z = pf8.fprop_act(qx, sx, qw, sw, b.detach(), "silu", True, save_z=True)[1]
+    dz, dbias = pf8.act_backward(dd, z, "silu", True, bias_grad=True)
+    q, s, qt, st = pf8.quant_act_dual(dz)
+    assert torch.equal(x.grad, pf8.dgrad(q, s, qwt, sw)) and torch.equal(w.grad, pf8.wgrad(qt, st, qxt, sxt))
+    assert torch.equal(b.grad, dbias.to(BF))
+
+
+def test_gradients_of_a_subset():
+    """Only the asked-for gradients are made, each the same as among all of them."""
+    m, k, n = 128, 256, 512
+    w, x, b, r = _rand((n, k), 2, 0.05), _rand((m, k), 1), _rand((n,), 3), _rand((m, n // 2), 4)
+    dd = _rand((1, n // 2), 5, 1e-2).expand(m, n // 2)  # broadcast: one row for all tokens
+    def grads(flags):
+        ts = [t.clone().requires_grad_(f) for t, f in zip((x, w, b, r), flags)]
+        pf8.fp8_linear_act(ts[0], ts[1], ts[2], "silu", True, ts[3]).backward(dd)
+        return [t.grad for t in ts]
+    every = grads((True,) * 4)
+    for i in range(4):
+        got = grads(tuple(j == i for j in range(4)))
+        assert torch.equal(got[i], every[i]) and all(g is None for j, g in enumerate(got) if j != i)
 
 
 def test_linear_layer_main_grads_and_inference():

@@ -146,6 +146,43 @@ def test_act_workspace():
         assert _act(z=0, act=0, gated=0, dz=0) == L.PF8_ENODEV
 
 
+def _act_quant(**kw):
+    a = dict(rows=256, cols=128, dd=P[0], lddd=128, z=P[1], ldz=256, act=3, gated=1, qr=P[2], ldqr=256, sr=P[3], ld_sr=256,
+             qc=P[4], ldqc=256, sc=P[5], ld_sc=256, dbias=P[6], accumulate=0, ws=P[7],
+             ws_bytes=L.pf8_act_bwd_quant_workspace(256, 128, 1))
+    a.update(kw)
+    return L.pf8_act_bwd_quant(*a.values(), 0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    *((dict([(p, 0)]), "EINVAL") for p in ("dd", "z", "qr", "sr", "qc", "sc", "rows", "cols", "ws")),
+    (dict(rows=-128), "EINVAL"), (dict(act=6), "EINVAL"), (dict(act=-1), "EINVAL"), (dict(act=0), "EINVAL"),
+    (dict(act=0, gated=0), "EINVAL"), (dict(z=0, act=3, gated=0), "EINVAL"), (dict(gated=2), "EINVAL"),
+    (dict(accumulate=2), "EINVAL"), (dict(lddd=127), "EINVAL"), (dict(ldz=255), "EINVAL"), (dict(ldqr=255), "EINVAL"),
+    (dict(ld_sr=255), "EINVAL"), (dict(ldqc=255), "EINVAL"), (dict(ld_sc=255), "EINVAL"), (dict(ws_bytes=16), "EINVAL"),
+    (dict(rows=192), "ESHAPE"), (dict(cols=64), "ESHAPE"), (dict(rows=BIG, ld_sr=BIG, ldqc=BIG), "ESHAPE"),
+    (dict(ldz=BIG), "ESHAPE"), (dict(rows=65536 * 128, ld_sr=65536 * 128, ldqc=65536 * 128), "ESHAPE"),
+    (dict(cols=BIG // 2, lddd=BIG // 2, ldz=BIG - 1, ldqr=BIG - 1, ld_sc=BIG - 1), "EINVAL"),
+    (dict(dd=P[0] + 2), "EALIGN"), (dict(z=P[1] + 8), "EALIGN"), (dict(lddd=132), "EALIGN"), (dict(ldz=260), "EALIGN"),
+    (dict(qr=P[2] + 8), "EALIGN"), (dict(qc=P[4] + 8), "EALIGN"), (dict(ldqr=264), "EALIGN"), (dict(ldqc=264), "EALIGN"),
+    (dict(sr=P[3] + 2), "EALIGN"), (dict(sc=P[5] + 2), "EALIGN"), (dict(dbias=P[6] + 2), "EALIGN"), (dict(ws=P[7] + 8), "EALIGN"),
+])
+def test_act_quant_refuses(kw, want):
+    assert _act_quant(**kw) == _status(want)
+
+
+def test_act_quant_workspace():
+    f = L.pf8_act_bwd_quant_workspace
+    assert f(256, 128, 0) == 2 * 128 * 4 and f(256, 128, 1) == 2 * f(256, 128, 0)
+    for bad in ((0, 128, 0), (128, 0, 0), (128, 128, 2), (64, 128, 0), (128, 64, 0), (BIG, 128, 0), (128, BIG // 2, 1),
+                (65536 * 128, 128, 0)):
+        assert f(*bad) == 0
+    if not _gpu():
+        assert _act_quant() == L.PF8_ENODEV
+        assert _act_quant(dbias=0, ws=0) == L.PF8_ENODEV
+        assert _act_quant(z=0, act=0, gated=0) == L.PF8_ENODEV
+
+
 def _prod(**kw):
     a = dict(m=8, n=256, k=256, a=P[0], lda=256, a_ds=P[1], ld_as=8, b=P[2], ldb=256, b_ds=P[3], ld_bs=2, bias=P[4], btype=0,
              act=3, gated=1, residual=P[5], ldr=128, z=P[6], ldz=256, d=P[7], ldd=128)
