@@ -3,7 +3,8 @@
 // include/pf8_layer.h.
 //
 // Bound: HBM. Without a gate 6 bytes a value of dd (dd, z in, two codes out), with one 10; through a BF16 dz in
-// memory it would be 10 and 18. 8192 x 6144 gated: 110 us, against 97 + 72 us by act.hip and the quantiser.
+// memory it would be 10 and 18. 8192 x 6144 with a gate and a bias: 90 us (5.6 TB/s), without a
+// gate 59 us, against 176 and 97 us by act.hip and the quantiser after it.
 // A workgroup takes a 128 x 128 tile of dd and makes one such tile of dz, or the gate's and the factor's one after
 // the other. Column sums over the tile's rows go to one row of partial sums for each 128 rows.
 #include "act_device.h"

@@ -91,12 +91,17 @@ constexpr int kTilesPerCu = 160 * 1024 / (4 * (BM + BN) * 64 + 128 * BN);
 // The persistent pipeline of gemm_mx_persistent_kernel (the ring of stage buffers that runs on across
 // tiles, the explicit waits, the order of tiles and of K) with three differences:
 //  * Any sizes: row offsets are in the lanes' offsets, so that the buffer range check turns rows past the edge into
-//    zeros (a variant for whole tiles alone was no faster: 8192 x 12288 x 2048 gated 178 against 178 us); K blocks past the end, up to whole bodies of four stages and two bodies, are fetched
-//    through a buffer of no size and count as zeros too.
+//    zeros (a variant for whole tiles alone was no faster: 8192 x 12288 x 2048 gated 178 against 178 us); K blocks past
+//    the end, up to whole bodies of four stages and two bodies, are fetched through a buffer of no size and count as
+//    zeros too.
 //  * GATED: a tile of BN rows of W is, for each of the two waves of columns, BN / 4 rows that make the gate and the
 //    BN / 4 that make what it multiplies, so that a lane holds both values of a column of d.
 //  * The epilogue works on the accumulators where they are: bias, rounded z, activation and gate, residual. Every
 //    bf16 slab of 64 rows passes through the staging buffer, out (and the residual in) by whole rows.
+// Bound: matrix instructions at the clock that the power allows, and at 256 x 256 the epilogue, which nothing hides: one
+// tile's accumulators fill a CU's registers, so the matrix cores wait while its results leave. 8192 x 12288 x 2048 gated:
+// 204 us (2.0 PFLOP/s), without z (0.2 GB less to write) 182; the plain product of that size 165. 8192 x 2048 x 6144
+// with bias, onto a residual: 91 us (2.3 PFLOP/s), without both 80.
 template <int BM, int BN, bool GATED, bool RES, ActClass ACT>
 __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_kernel(FpropActArgs p, int tiles_m, int tiles_n) {
   constexpr int BK = 64;
