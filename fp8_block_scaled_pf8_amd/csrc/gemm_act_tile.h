@@ -111,14 +111,14 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
   constexpr int SB = GATED && TN > 1 ? 2 : 1;  // scales of W: a wave's rows of a part lie in one 128-row tile
   constexpr int SS = TM + SB;
   constexpr int OUT = GATED ? BN / 2 : BN;     // columns of d
-  constexpr int RP = BN * 2, CH = BN / 8;      // staged row in bytes and 16-byte chunks
-  constexpr int CHD = OUT / 8;                 // chunks of a row of d
-  constexpr int PER_D = 64 * CHD / 256;       // chunks of d per thread and slab
+  constexpr int RP = WN * 2, CH = WN / 8;      // a wave's staged row in bytes and 16-byte chunks
+  constexpr int CHD = OUT / 16;                // chunks of its row of d
+  constexpr int PER_D = 32 * CHD / 64;         // chunks of d per lane and slab
   __shared__ __align__(16) uint8_t buf0[ST];
   __shared__ __align__(16) uint8_t buf1[ST];
   __shared__ __align__(16) uint8_t buf2[ST];
   __shared__ __align__(16) uint8_t buf3[ST];
-  __shared__ __align__(512) uint8_t stg[64 * RP];
+  __shared__ __align__(512) uint8_t stg[4 * 32 * RP];
 
   const int t0 = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(t0 >> 6);
@@ -390,19 +390,17 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
     asm volatile("" : "+v"(te));
     // ---- the residual's rows of a slab, by whole rows as d's; the first slab's are on their way during the last body ----
     const int rows = static_cast<int>(min64(BM, p.m - m0));
-    const int left = static_cast<int>(min64(OUT, cols - n0));  // columns of d in the tile
-    // byte offset, in the tile's rows of an array of pitch ld, of a thread's first row; and of chunk `it` from there
-    auto row_offset = [&](int n, int ld2) { return (te / n / 32 * WM + te / n % 32) * ld2; };
-    auto step_offset = [&](int n, int i, int it, int ld2) {
-      const int s = 256 / n * it;
-      return (s / 32 * WM + s % 32 + 32 * i) * ld2;
-    };
+    const int first = wn * (OUT / 2);                                  // the wave's first column of d in the tile
+    const int left = static_cast<int>(min64(OUT, cols - n0)) - first;  // and its columns from there on
+    // byte offset, in the tile's rows of an array of pitch ld, of a lane's first row; and of chunk `it` from there
+    auto row_offset = [&](int n, int ld2) { return (wm * WM + te % 64 / n) * ld2; };
+    auto step_offset = [&](int n, int i, int it, int ld2) { return (64 / n * it + 32 * i) * ld2; };
     v4i res[RES ? PER_D : 1];
     auto load_residual = [&](int i) {
       const int ld2 = static_cast<int>(p.ldr * 2), c = 8 * (te % CHD), room = left - c;
       const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<uint16_t*>(p.residual) + m0 * p.ldr + n0, 0, rows * ld2, kBufferFlags);
-      const int vo = row_offset(CHD, ld2) + 2 * c;
+      const int vo = row_offset(CHD, ld2) + 2 * (first + c);
       if (room >= 8) {
 #pragma unroll
         for (int it = 0; it < PER_D; ++it)
@@ -449,35 +447,33 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
     };
 #pragma unroll
     for (int i = 0; i < TM; ++i) pin(i);
-    constexpr int kWaitLgkm = 0xF | (0x7 << 4) | (0x3 << 14);  // lgkmcnt(0) only
     // A lane's accumulator acc[i][j] holds, of row wm WM + 32 i + l32, the 4 columns 8 q4 + 4 half .. +3 of
     // block j for each q4. Gated, the first half of a wave's columns makes the gate. part: which half;
     // place: 8-column chunk of d's tile (less the wave's own offset).
     auto part = [](int j, int q4) { return !GATED ? 0 : TN > 1 ? (j >= TN / 2 ? 1 : 0) : q4 >> 1; };
     auto place = [](int j, int q4) { return !GATED ? 4 * j + q4 : TN > 1 ? 4 * (j % (TN / 2 ? TN / 2 : 1)) + q4 : q4 & 1; };
-    auto fence = [&]() {  // all waves' staging accesses are done (and nothing of the next slab is computed ahead: registers)
-      __builtin_amdgcn_s_waitcnt(kWaitLgkm);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-    };
+    // nothing of what follows is computed ahead, for which there are no registers
+    auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
     const TileAct<ACT> act(p.act);
-    // Staging: slab i holds rows wm WM + 32 i + l32 of both wave rows as row wm 32 + l32; chunk c of row sr lies at
-    // chunk c ^ (sr mod CH). With a 512-byte aligned buffer a lane's address is one XOR of the chunk's constant bits.
-    const uint32_t wbase = (lds_addr(stg) + (wm * 32 + te % 32) * RP + 8 * (te / 32 % 2)) |
-                           (((wn * (OUT / 16)) ^ (te % 32 & (CH - 1))) << 4);
-    // Whole rows: thread t takes chunk t mod N of rows t / N + 256 / N it.
-    auto row_chunks = [&](auto n_c, uint32_t (&addr)[64 * decltype(n_c)::value / 256]) {
+    // Staging, each wave in a quarter of its own, so that no wave waits for another (LDS accesses of a wave keep their
+    // order): slab i's row wm WM + 32 i + r is row r; its chunk c lies at chunk c ^ key(r), which spreads 16 rows over all
+    // banks. With a 512-byte aligned buffer a lane's address is one XOR of the chunk's constant bits.
+    auto key = [](int r) { return r / (16 / CH) & (CH - 1); };
+    const uint32_t base_w = lds_addr(stg) + wave * 32 * RP;
+    const uint32_t wbase = (base_w + te % 32 * RP + 8 * (te / 32 % 2)) | (key(te % 32) << 4);
+    // Whole rows: lane l takes chunk l mod N of rows l / N + 64 / N it.
+    auto row_chunks = [&](auto n_c, uint32_t (&addr)[32 * decltype(n_c)::value / 64]) {
       constexpr int N = decltype(n_c)::value;
 #pragma unroll
-      for (int it = 0; it < 64 * N / 256; ++it) {
-        const int row = te / N + 256 / N * it;
-        addr[it] = lds_addr(stg) + row * RP + (((te % N) ^ (row & (CH - 1))) << 4);
+      for (int it = 0; it < 32 * N / 64; ++it) {
+        const int row = te % 64 / N + 64 / N * it;
+        addr[it] = base_w + row * RP + ((te % N ^ key(row)) << 4);
       }
     };
     // stores of a thread's chunks of N to an array from its tile's first element on; c: the chunk's first column
     // there, room: the columns left from it
     auto store_rows = [&](auto n_c, uint16_t* base, int64_t ld, int c, int room, int i) {
-      constexpr int N = decltype(n_c)::value, PER = 64 * N / 256;
+      constexpr int N = decltype(n_c)::value, PER = 32 * N / 64;
       uint32_t addr[PER];
       v4i v[PER];
       row_chunks(n_c, addr);
@@ -517,7 +513,7 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
         fence();
         const int c = te % CH, of = GATED ? c % (CH / 2) : c;  // chunk of the part
         const int64_t second = GATED && c >= CH / 2 ? cols : 0;
-        store_rows(NZ{}, p.z + m0 * p.ldz + n0, p.ldz, static_cast<int>(second) + 8 * of, left - 8 * of, i);
+        store_rows(NZ{}, p.z + m0 * p.ldz + n0, p.ldz, static_cast<int>(second) + first + 8 * of, left - 8 * of, i);
         fence();
       }
       if constexpr (RES) {
@@ -554,8 +550,8 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
           stg_write8(a1, pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3]));
         }
       fence();
-      store_rows(ND{}, p.d + m0 * p.ldd + n0, p.ldd, 8 * (te % CHD), left - 8 * (te % CHD), i);
-      if (i + 1 < TM) fence();  // every wave has read this slab back before the next one is staged
+      store_rows(ND{}, p.d + m0 * p.ldd + n0, p.ldd, first + 8 * (te % CHD), left - 8 * (te % CHD), i);
+      if (i + 1 < TM) fence();
     }
     if (r + 1 == ntiles) break;
     // the next tile's first body: all of its stage 3 came with the last refills (no PREV in
