@@ -89,7 +89,7 @@ template <int BM, int BN>
 constexpr int kTilesPerCu = 160 * 1024 / (4 * (BM + BN) * 64 + 128 * BN);
 
 // The persistent pipeline of gemm_mx_persistent_kernel (the ring of stage buffers that runs on across
-// tiles, the explicit waits, the order of tiles and of K) with three differences:
+// tiles, the explicit waits, the order of tiles and of K) with four differences:
 //  * Any sizes: row offsets are in the lanes' offsets, so that the buffer range check turns rows past the edge into
 //    zeros (a variant for whole tiles alone was no faster: 8192 x 12288 x 2048 gated 178 against 178 us); K blocks past
 //    the end, up to whole bodies of four stages and two bodies, are fetched through a buffer of no size and count as
@@ -98,10 +98,12 @@ constexpr int kTilesPerCu = 160 * 1024 / (4 * (BM + BN) * 64 + 128 * BN);
 //    BN / 4 that make what it multiplies, so that a lane holds both values of a column of d.
 //  * The epilogue works on the accumulators where they are: bias, rounded z, activation and gate, residual. Every
 //    bf16 slab of 64 rows passes through the staging buffer, out (and the residual in) by whole rows.
+//  * All workgroups start together: with half of them a third of a tile late, 8192 x 12288 x 2048 gated with z took 199 us
+//    instead of 196, without z 179 instead of 174.
 // Bound: matrix instructions at the clock that the power allows, and at 256 x 256 the epilogue, which nothing hides: one
 // tile's accumulators fill a CU's registers, so the matrix cores wait while its results leave. 8192 x 12288 x 2048 gated:
-// 204 us (2.0 PFLOP/s), without z (0.2 GB less to write) 182; the plain product of that size 165. 8192 x 2048 x 6144
-// with bias, onto a residual: 91 us (2.3 PFLOP/s), without both 80.
+// 196 us (2.1 PFLOP/s), without z (0.2 GB less to write) 174; the plain product of that size 165. 8192 x 2048 x 6144
+// with bias, onto a residual: 89 us (2.3 PFLOP/s); the plain product 83.
 template <int BM, int BN, bool GATED, bool RES, ActClass ACT>
 __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_kernel(FpropActArgs p, int tiles_m, int tiles_n) {
   constexpr int BK = 64;
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
   if (ntiles == 0) return;
   auto tile_origin = [&](int r, int64_t& m0, int64_t& n0) {
     const int bid = xcd_base + slot + slots * r;
-    constexpr int kGroupM = 8;
+    constexpr int kGroupM = 4;  // (8192 x 2048 x 6144 90 us, with 8 92; 8192 x 12288 x 2048 the same)
     const int per_group = kGroupM * tiles_n;
     const int grp = bid / per_group;
     const int first_m = grp * kGroupM;
@@ -350,10 +352,6 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
   issue_part(I3{}, 3, PA{});
   issue_part(I3{}, 3, PB{});
   __builtin_amdgcn_sched_barrier(0);
-  // staggered start, as in gemm_mx_persistent_kernel
-  if (ntiles >= 4 && (slot & 1)) {
-    for (int z = 0; z < ns; ++z) __builtin_amdgcn_s_sleep(TM * TN / 2);
-  }
   PF8_WAIT_VM_LGKM0(D + (D + SS) + D);  // after stage 0: stages 1, 2 and 3
   __builtin_amdgcn_s_barrier();
   read_frags(buf0, fa[0], fb[0]);
