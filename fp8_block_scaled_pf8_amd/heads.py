@@ -342,7 +342,8 @@ class QKNormRopeFunction(torch.autograd.Function):
             return g.dq, None if add or w is None or not wanted else g.dw_q.to(w.dtype)
 
         adds = [w is not None and m is not None and n for w, m, n in zip((w_q, w_k), main, need[2:])]
-        if dq is None or dk is None or adds[0] != adds[1]:
+        shared = all(adds) and main[0].data_ptr() == main[1].data_ptr()  # of one weight for both: one after the other
+        if dq is None or dk is None or adds[0] != adds[1] or shared:
             gq, gwq = one(dq, q, w_q, main[0], need[2])
             gk, gwk = one(dk, k, w_k, main[1], need[3])
         else:
@@ -373,7 +374,9 @@ def fp8_qk_norm_rope(q: Tensor, k: Optional[Tensor] = None, positions: Optional[
     lead = q.shape[:-2]
     if positions is not None:
         axis = () if sections is None else (positions.shape[0],)
-        positions = positions.expand(*axis, *lead).reshape(*axis, -1)
+        rest = positions.shape[len(axis):]
+        ones = (1,) * (len(lead) - len(rest))  # dimensions that the leading shape has more, behind the axes
+        positions = positions.reshape(*axis, *ones, *rest).expand(*axis, *lead).reshape(*axis, -1)
     if main_grads is not None:
         for m, w in zip(main_grads, (w_q, w_k)):
             if m is not None and (w is None or m.dtype != torch.float32 or m.shape != w.shape):

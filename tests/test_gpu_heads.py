@@ -216,6 +216,33 @@ def test_accumulates_and_repeats():
     assert c.dw_q is base[0] and torch.equal(base[0], want[0]) and torch.equal(base[1], want[1])
 
 
+@pytest.mark.parametrize("batch", [1, 2, 3, 4])
+def test_positions_broadcast_behind_their_axes(batch):
+    """[axes, seq] for q [batch, seq, ...] are every batch's positions, whatever the batch's size is."""
+    q = _rand((batch, 5, 2, 64), 3)
+    pos = torch.randint(0, 100, (3, 5), generator=torch.Generator().manual_seed(1)).to(DEV)
+    rot = dict(inv_freq=torch.linspace(1, 0.01, 32, device=DEV), sections=(16, 8, 8))
+    got = pf8.fp8_qk_norm_rope(q, None, pos, **rot)[0]
+    for i in range(batch):
+        assert torch.equal(got[i], pf8.qk_norm_rope(q[i], None, pos, **rot)[0])
+    assert torch.equal(got, pf8.fp8_qk_norm_rope(q, None, pos[:, None], **rot)[0])
+    one = pf8.fp8_qk_norm_rope(q, None, pos[0], rot["inv_freq"])[0]
+    assert torch.equal(one[batch - 1], pf8.qk_norm_rope(q[batch - 1], None, pos[0], rot["inv_freq"])[0])
+    with pytest.raises((RuntimeError, ValueError)):
+        pf8.fp8_qk_norm_rope(q, None, pos[:, :4], **rot)
+
+
+def test_one_weight_for_both_with_one_main_grad():
+    q, k, w = _rand((9, 4, 64), 1).requires_grad_(), _rand((9, 2, 64), 2).requires_grad_(), _rand((64,), 3)
+    dq, dk = _rand((9, 4, 64), 4), _rand((9, 2, 64), 5)
+    a, b, m = (torch.zeros(64, device=DEV) for _ in range(3))
+    for main in ((a, b), (m, m)):
+        ww = w.clone().requires_grad_()
+        torch.autograd.backward(pf8.fp8_qk_norm_rope(q, k, w_q=ww, w_k=ww, main_grads=main), [dq, dk])
+        assert ww.grad is None
+    assert torch.equal(m, a + b)
+
+
 def test_module_gradients_against_differences_of_the_oracle():
     """The module's gradients along random directions against central differences of the float64 oracle, from bf16
     gradients: each of n products is off by 2^-8 of its own (gradient's rounding)."""
