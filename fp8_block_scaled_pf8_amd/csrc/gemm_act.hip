@@ -20,23 +20,24 @@ __device__ __forceinline__ float act_any(int act, float z) {
   }
 }
 
-// Few tokens. A workgroup of 8 waves owns 16 columns of d (and the 16 or 32 rows of W that make them) for up
-// to 16 MT tokens; its waves take the 128-wide K blocks in turn, each with its own loads straight into registers: no
+// Few tokens. A workgroup of 8 waves owns 16 columns of d (and the 16 or 32 rows of W that make them) for `per`
+// tokens, up to 16 MT; its waves take the 128-wide K blocks in turn, each with its own loads straight into registers: no
 // row of W is read by two waves, so LDS would only be a detour. One v_mfma_f32_16x16x128_f8f6f4 covers a K block of 16
 // rows of W and 16 tokens; its partial is scaled into the wave's FP32 sum. The waves' sums meet in LDS, added in
 // the waves' order.
-// Bound: W's bytes, once for each group of tokens (from L2 past the first). One token of 12288 x 2048 gated: 6.9 us, 25
-// MB at 3.6 TB/s; 33 tokens of 2048 x 6144 onto a residual: 11.8 us, two groups over 256 workgroups, each of which
-// waits twice for 128-wide loads and once for the join. 16 waves, 4 or 8 rows of W a workgroup and loads of whole
-// cache lines a quarter wave were no faster.
+// Bound: what a CU reads, its rows of W and of X, some 30 bytes a nanosecond. One token of 12288 x 2048 gated: 6.8 us, 25
+// MB at 3.7 TB/s; 33 tokens of 2048 x 6144 onto a residual: 9.4 us, two groups over 256 workgroups, 0.2 MB each. 16 waves, 4
+// or 8 rows of W a workgroup, loads of whole cache lines a quarter wave and 3 to 8 K blocks in flight (gated, 6 took
+// 8.5 us instead of 6.8) were no faster.
 template <int MT, bool GATED>
-__global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
+__global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p, int per) {
   constexpr int WAVES = 8, PARTS = GATED ? 2 : 1, U = MT == 4 ? 2 : 4;  // U: K blocks whose loads go out together
   __shared__ v4f red[WAVES][PARTS][MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, quarter = lane >> 4;
   const int64_t cols = GATED ? p.n / 2 : p.n;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, m0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, m0 = static_cast<int64_t>(blockIdx.y) * per;
+  const int64_t m1 = min64(m0 + per, p.m);  // one behind its tokens
   const int nk = static_cast<int>(p.k / kGroup);
   const uint8_t* w[PARTS];
   const float* sw[PARTS];
@@ -50,7 +51,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   const float* sx[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
-    const int64_t row = min64(m0 + 16 * t + l16, p.m - 1);
+    const int64_t row = min64(m0 + 16 * t + l16, m1 - 1);
     x[t] = p.a + row * p.lda + quarter * 32;
     sx[t] = p.a_dscale + row;
   }
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
   const int t = threadIdx.x >> 6;
   if (t >= MT) return;
   const int64_t m = m0 + 16 * t + l16, n = n0 + 4 * quarter;
-  if (m >= p.m || n >= cols) return;
+  if (m >= m1 || n >= cols) return;
   const int left = static_cast<int>(min64(4, cols - n));
   float v[PARTS][4];
 #pragma unroll
@@ -142,12 +143,26 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p) {
 
 }  // namespace
 
+// Workgroups along the columns.
+static int64_t few_blocks(const FpropActArgs& a) { return ((a.gated ? a.n / 2 : a.n) + 15) / 16; }
+
+// Groups of tokens: as many as there have to be, more where a CU each is left for them, and even ones (33 tokens as 17 and
+// 16, not 32 and 1): a workgroup's time goes by the bytes that it reads, its rows of W and of X, which a CU takes at
+// some 30 GB/s whatever is in flight. 33 x 2048 x 6144 9.4 us, with 32 and 1 tokens 11.3; 16 x 2048 x 6144 by two
+// groups of 8 on 256 workgroups 7.4 us, by one on 128 8.4.
+template <int MT>
+static int64_t few_groups(const FpropActArgs& a) {
+  const int64_t least = (a.m + 16 * MT - 1) / (16 * MT), fill = 256 / few_blocks(a);
+  return least > fill ? least : fill < a.m ? fill : a.m;
+}
+
 template <int MT>
 static hipError_t launch_few(const FpropActArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(((a.gated ? a.n / 2 : a.n) + 15) / 16), static_cast<uint32_t>((a.m + 16 * MT - 1) / (16 * MT))),
+  const int64_t groups = few_groups<MT>(a), per = (a.m + groups - 1) / groups;
+  const dim3 grid(static_cast<uint32_t>(few_blocks(a)), static_cast<uint32_t>((a.m + per - 1) / per)),
       block(512);
-  if (a.gated) hipLaunchKernelGGL((fprop_act_few_kernel<MT, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((fprop_act_few_kernel<MT, false>), grid, block, 0, stream, a);
+  if (a.gated) hipLaunchKernelGGL((fprop_act_few_kernel<MT, true>), grid, block, 0, stream, a, static_cast<int>(per));
+  else hipLaunchKernelGGL((fprop_act_few_kernel<MT, false>), grid, block, 0, stream, a, static_cast<int>(per));
   return hipGetLastError();
 }
 
@@ -160,9 +175,9 @@ static hipError_t launch_few(const FpropActArgs& a, hipStream_t stream) {
 // CUs share the memory's rate.
 template <int MT>
 static double few_cost(const FpropActArgs& a) {
-  const int64_t groups = (a.m + 16 * MT - 1) / (16 * MT);
+  const int64_t groups = few_groups<MT>(a);
   const double share = static_cast<double>(a.n) / 16 / 256 * static_cast<double>(groups);
-  const double tokens = static_cast<double>(a.m < 16 * MT ? a.m : 16 * MT);
+  const double tokens = static_cast<double>((a.m + groups - 1) / groups);
   return 3.0 + (share > 1.0 ? share : 1.0) * static_cast<double>(a.k) / 1024 * (0.5 + 0.028 * tokens);
 }
 

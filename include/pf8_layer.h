@@ -163,6 +163,7 @@ int64_t pf8_act_bwd_quant_workspace(int64_t rows, int64_t cols, int gated);
  * residual: bf16, d's shape, pitch ldr, or NULL. May be d itself (same address and pitch).
  * z: bf16 [m, n], pitch ldz, what pf8_act_bwd takes; or NULL: not wanted. Overlaps nothing.
  * d, z and residual: 16-byte aligned, pitches multiples of 8.
+ * Pitches: lda and ldb up to 8388607, ldd, ldr and ldz up to half of that, where there is a single row too.
  */
 pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* a_dscale,
                          int64_t ld_as, const void* b, int64_t ldb, const float* b_dscale, int64_t ld_bs,
