@@ -38,14 +38,19 @@ class QKNormRopeGrads(NamedTuple):
     dw_k: Optional[Tensor]
 
 
-def _heads(t: Tensor, name: str, shape, device) -> Tuple[int, int, int]:
-    """(address, stride of tokens, stride of heads) of a bf16 [tokens, heads, head_dim] tensor after its checks."""
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+def _like(t: Tensor, name: str, shape, device) -> Tuple[int, int, int]:
+    """``_heads`` of a tensor that has to have another one's shape and device."""
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return _heads(t, name, shape)
+
+
+def _heads(t: Tensor, name: str, shape) -> Tuple[int, int, int]:
+    """(address, stride of tokens, stride of heads) of a bf16 [tokens, heads, head_dim] tensor after its checks."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     tokens, heads, dim = shape
     st, sh, sd = t.stride()
     if tokens == 0:
@@ -133,11 +138,12 @@ def _common(q, k, dims, positions, inv_freq, w_q, w_k, sections, section_order, 
         raise TypeError(f"inv_freq must be float32 or float64, got {inv_freq.dtype}")
     if ptype is None:
         raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 1 <= inv_freq.shape[0] <= dim // 2:
-        raise ValueError(f"inv_freq must be a contiguous vector of 1 to {dim // 2} pairs, got {tuple(inv_freq.shape)}")
+    freqs = inv_freq.shape
+    if len(freqs) != 1 or not inv_freq.is_contiguous() or not 1 <= freqs[0] <= dim // 2:
+        raise ValueError(f"inv_freq must be a contiguous vector of 1 to {dim // 2} pairs, got {tuple(freqs)}")
     if inv_freq.device != dev or positions.device != dev:
         raise ValueError(f"positions and inv_freq must be on {dev}")
-    pairs = inv_freq.shape[0]
+    pairs = freqs[0]
     if sections is None:
         axes, array, want = 1, None, (tokens,)
     else:
@@ -152,27 +158,30 @@ def _common(q, k, dims, positions, inv_freq, w_q, w_k, sections, section_order, 
 
 
 def _shape(t: Tensor, name: str):
-    if not isinstance(t, Tensor) or t.dim() != 3:
+    shape = t.shape if isinstance(t, Tensor) else ()
+    if len(shape) != 3:
         raise ValueError(f"{name} must be a [tokens, heads, head_dim] tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device")
-    if not 1 <= t.shape[1] <= L.PF8_HEAD_MAX_HEADS:
-        raise ValueError(f"{name} must have 1 to {L.PF8_HEAD_MAX_HEADS} heads, got {t.shape[1]}")
-    return t.shape
+    if not 1 <= shape[1] <= L.PF8_HEAD_MAX_HEADS:
+        raise ValueError(f"{name} must have 1 to {L.PF8_HEAD_MAX_HEADS} heads, got {shape[1]}")
+    return shape
 
 
-def _k_shape(k: Optional[Tensor], name: str, q: Tensor):
+def _k_shape(k: Optional[Tensor], name: str, qs, device):
     if k is None:
         return None
     ks = _shape(k, name)
-    if ks[0] != q.shape[0] or ks[2] != q.shape[2]:
-        raise ValueError(f"queries {tuple(q.shape)} and keys {tuple(ks)} differ in tokens or head_dim")
+    if k.device != device:
+        raise ValueError(f"{name} must be on {device}, got {k.device}")
+    if ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError(f"queries {tuple(qs)} and keys {tuple(ks)} differ in tokens or head_dim")
     return ks
 
 
 def _result(out: Optional[Tensor], name: str, shape, like: Tensor) -> Tuple[Tensor, int, int, int]:
     if out is not None:
-        return (out, *_heads(out, name, shape, like.device))
+        return (out, *_like(out, name, shape, like.device))
     out = torch.empty_like(like, memory_format=torch.contiguous_format)  # (half of what torch.empty takes)
     return out, out.data_ptr(), shape[1] * shape[2], shape[2]
 
@@ -191,14 +200,14 @@ def qk_norm_rope(q: Tensor, k: Optional[Tensor] = None, positions: Optional[Tens
     themselves. No tokens: empty results.
     """
     qs = _shape(q, "q")
-    ks = _k_shape(k, "k", q)
     dev, tokens, dim = q.device, qs[0], qs[2]
+    ks = _k_shape(k, "k", qs, dev)
     args = _common(q, k, (tokens, dim, dev), positions, inv_freq, w_q, w_k, sections, section_order, interleaved,
                    rotary_scale, eps, unit_offset)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    aq = _heads(q, "q", qs, dev)
-    ak = (0, 0, 0) if k is None else _heads(k, "k", ks, dev)
+    aq = _heads(q, "q", qs)
+    ak = (0, 0, 0) if k is None else _heads(k, "k", ks)
     oq, *pq = _result(q_out, "q_out", qs, q)
     ok, *pk = (None, 0, 0, 0) if k is None else _result(k_out, "k_out", ks, k)
     if tokens == 0:
@@ -230,8 +239,8 @@ def qk_norm_rope_backward(dq: Tensor, dk: Optional[Tensor], q: Optional[Tensor],
     there, or with ``accumulate`` added to what is there.
     """
     qs = _shape(dq, "dq")
-    ks = _k_shape(dk, "dk", dq)
     dev, tokens, dim = dq.device, qs[0], qs[2]
+    ks = _k_shape(dk, "dk", qs, dev)
     args = _common(dq, dk, (tokens, dim, dev), positions, inv_freq, w_q, w_k, sections, section_order, interleaved,
                    rotary_scale, eps, unit_offset)
     if dk is None and (k is not None or dk_out is not None):
@@ -242,11 +251,11 @@ def qk_norm_rope_backward(dq: Tensor, dk: Optional[Tensor], q: Optional[Tensor],
             return (0, 0, 0)
         if t is None:
             raise ValueError(f"the weight's gradient needs {name}")
-        return _heads(t, name, shape, dev)
+        return _like(t, name, shape, dev)
 
     aq, ak = values(q, "q", w_q, qs), values(k, "k", w_k, ks)
-    gq = _heads(dq, "dq", qs, dev)
-    gk = (0, 0, 0) if dk is None else _heads(dk, "dk", ks, dev)
+    gq = _heads(dq, "dq", qs)
+    gk = (0, 0, 0) if dk is None else _heads(dk, "dk", ks)
 
     def vector(out, name, w):
         if w is None:

@@ -142,23 +142,21 @@ def _may_write(out: Tensor, name: str, others) -> None:
             raise ValueError(f"{name} overlaps another operand")
 
 
-# The current stream's handle without the Stream object around it (which costs as much as half a launch).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(device: torch.device) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle and the current device's number without the objects and checks around them (which cost
+# as much as half a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, device: torch.device, *args) -> None:
     """A library call that enqueues on the current stream of a device, made the current one where it is not."""
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(device))
+    index = device.index
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, _stream(device))
+            status = fn(*args, _raw_stream(index))
     if status != L.PF8_OK:
         L.check(status, fn.__name__)
 
