@@ -82,10 +82,11 @@ def _scales(t: Tensor, name: str, rows: int, cols: int, device) -> Tuple[int, in
 
 
 def _new_result(rows: int, cols: int, device) -> Tuple[Tensor, int, int]:
-    """A bf16 result in rows of 16 bytes or a multiple of it (a view of a wider buffer where cols asks for it)."""
+    """A bf16 result in rows that are multiples of 16 bytes apart (in one call: a slice of a wider tensor takes as long
+    as the tensor)."""
     pitch = out_pitch(cols, 2) if rows > 1 else -(-cols // 8) * 8
-    t = torch.empty((rows, pitch), dtype=torch.bfloat16, device=device)
-    return (t if pitch == cols else t[:, :cols]), t.data_ptr(), pitch
+    t = torch.empty_strided((rows, cols), (pitch, 1), dtype=torch.bfloat16, device=device)
+    return t, t.data_ptr(), pitch
 
 
 def fprop_act(qx: Tensor, sx: Tensor, qw: Tensor, sw: Tensor, bias: Optional[Tensor] = None,
