@@ -29,8 +29,10 @@ struct TileAct {
     } else if constexpr (C == kIdentity) {
       return z;
     } else if constexpr (C == kSigmoid) {
-      // far out the cube overflows to an infinity of z's sign, and the sigmoid is 0 or 1
-      return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c3 * z, z, c1)));
+      // Far out the cube overflows to an infinity of z's sign, and the sigmoid is 0 or 1; the square stays finite, as
+      // c3 may be 0.
+      const float z2 = fminf(z * z, 3.0e38f);
+      return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c3, z2, c1)));
     } else {
       return act_value<PF8_ACT_GELU>(z);
     }

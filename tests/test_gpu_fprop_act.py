@@ -217,6 +217,29 @@ def test_infinities_and_not_a_number_stay_in_their_rows(m):
     assert got[0].isnan().all() and torch.equal(got[1:], want[1:])
 
 
+@pytest.mark.parametrize("act", ACTS + [None])
+@pytest.mark.parametrize("m", [3, 300, 2100])
+def test_infinite_bias(m, act):
+    """An activation of an infinite value is its limit, and the other columns are as without one."""
+    op = _operands(m, 512, 256)
+    bias = _rand((512,), 3, 0.5)
+    far = bias.clone()
+    far[[1, 40, 300]] = float("inf")
+    got, want = (pf8.fprop_act(*op, bias=b, activation=act) for b in (far, bias))
+    assert (got[:, [1, 40, 300]] == float("inf")).all()
+    if act == "relu":
+        far[7] = -float("inf")
+        assert (pf8.fprop_act(*op, bias=far, activation=act)[:, 7] == 0).all()
+    got[:, [1, 40, 300]] = want[:, [1, 40, 300]]
+    assert torch.equal(got, want)
+    if act:
+        got, want = (pf8.fprop_act(*op, bias=b, activation=act, gated=True) for b in (far, bias))
+        assert got[:, [1, 40]].isinf().all()  # (of the factor's sign)
+        assert act != "silu" or got[:, 300 - 256].isinf().all()  # (other gates vanish far below zero: 0 times infinity)
+        keep = [c for c in range(256) if c not in (1, 7, 40, 44)]
+        assert torch.equal(got[:, keep], want[:, keep])
+
+
 def test_no_tokens_and_refusals():
     op = _operands(4, 256, 256)
     qx, sx, qw, sw = op
