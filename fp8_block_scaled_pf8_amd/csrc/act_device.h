@@ -17,13 +17,17 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
 }
 
-// tanh(u) = 2 sigmoid(2 u) - 1, so that z (1 + tanh(u)) / 2 = z sigmoid(2 u): no difference of near values for
+// tanh(u) = 2 sigmoid(2 u) - 1, so that z (1 + tanh(u)) / 2 = z s with s = sigmoid(2 u): no difference of near values for
 // z far below zero. u is a polynomial of z, taken at -20 or 20 beyond that, where the sigmoid is 0 or 1 anyway
 // and the cube would overflow.
 constexpr float kTanhScale = 0.79788456080286535588f, kTanhCube = 0.044715f;
-__device__ __forceinline__ float tanh_argument2(float& z) {
-  z = z > 20.0f ? 20.0f : z < -20.0f ? -20.0f : z;  // NaN stays NaN, which the median instruction would drop
-  return 2.0f * kTanhScale * z * __builtin_fmaf(kTanhCube * z, z, 1.0f);
+__device__ __forceinline__ float tanh_sigmoid(float& z, float& z2) {
+  const float near = __builtin_amdgcn_fmed3f(z, -20.0f, 20.0f);
+  z = z == z ? near : z;  // the median would drop NaN (and comparisons with both ends came out as branches)
+  z2 = z * z;
+  constexpr float c1 = static_cast<float>(-2.0 * 1.44269504088896341 * 0.79788456080286535588);
+  constexpr float c3 = static_cast<float>(-2.0 * 1.44269504088896341 * 0.79788456080286535588 * 0.044715);
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * __builtin_fmaf(c3, z2, c1)));
 }
 
 // The normal distribution Phi(z) = (1 + erf(z / sqrt 2)) / 2, and e = exp(-z^2 / 2). Below zero Phi = e h(|z|) with
@@ -55,8 +59,8 @@ __device__ __forceinline__ float act_value(float z) {
     return z * normal_cdf(z, e);
   }
   if constexpr (ACT == PF8_ACT_GELU_TANH) {
-    float y = z;
-    return z * sigmoid(tanh_argument2(y));
+    float y = z, y2;
+    return z * tanh_sigmoid(y, y2);
   }
   return z;
 }
@@ -80,10 +84,10 @@ __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
     value = z * p;
     slope = __builtin_fmaf(z * 0.39894228040143267794f, e, p);
   } else if constexpr (ACT == PF8_ACT_GELU_TANH) {
-    float y = z;
-    const float s = sigmoid(tanh_argument2(y));
+    float y = z, y2;
+    const float s = tanh_sigmoid(y, y2);
     value = z * s;
-    slope = __builtin_fmaf(y * s * (1.0f - s), 2.0f * kTanhScale * __builtin_fmaf(3.0f * kTanhCube * y, y, 1.0f), s);
+    slope = __builtin_fmaf(y * (s * (1.0f - s)), __builtin_fmaf(6.0f * kTanhScale * kTanhCube, y2, 2.0f * kTanhScale), s);
   } else {
     value = z;
     slope = 1.0f;
