@@ -56,25 +56,28 @@ def _aligned_rows(t: Tensor, name: str, shape, device) -> Tuple[int, int]:
     return p, ld
 
 
-def _codes(t: Tensor, name: str) -> Tuple[int, int]:
-    if not isinstance(t, Tensor) or t.dim() != 2 or t.dtype != torch.uint8:
+def _codes(t: Tensor, name: str) -> Tuple[int, int, int, int]:
+    """(rows, columns, address, pitch) of a tensor of codes after its checks."""
+    shape = t.shape if isinstance(t, Tensor) else ()
+    if len(shape) != 2 or t.dtype is not torch.uint8:
         raise TypeError(f"{name} must be a 2-D uint8 tensor of codes")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a HIP device")
-    rows, cols = t.shape
+    rows, cols = shape
     ld, one = t.stride()
     if one != 1 or rows > 1 and ld < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return t.data_ptr(), cols if rows == 1 else ld
+    return rows, cols, t.data_ptr(), cols if rows == 1 else ld
 
 
 def _scales(t: Tensor, name: str, rows: int, cols: int, device) -> Tuple[int, int]:
-    if not isinstance(t, Tensor) or t.dtype != torch.float32 or t.dim() != 2:
+    shape = t.shape if isinstance(t, Tensor) else ()
+    if len(shape) != 2 or t.dtype is not torch.float32:
         raise TypeError(f"{name} must be a 2-D float32 tensor")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape[0] < rows or t.shape[1] < cols:
-        raise ValueError(f"{name} must cover [{rows}, {cols}], got {tuple(t.shape)}")
+    if shape[0] < rows or shape[1] < cols:
+        raise ValueError(f"{name} must cover [{rows}, {cols}], got {tuple(shape)}")
     ld, one = t.stride()
     if one != 1 and cols > 1 or rows > 1 and ld < cols:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
@@ -100,12 +103,11 @@ def fprop_act(qx: Tensor, sx: Tensor, qw: Tensor, sw: Tensor, bias: Optional[Ten
     shape. d is bf16, and so is z = X W^T + bias, which ``act_backward`` takes: returned as (d, z) with ``save_z`` or
     z_out. out may be residual itself. No tokens: empty results.
     """
-    pa, lda = _codes(qx, "qx")
-    pb, ldb = _codes(qw, "qw")
+    m, k, pa, lda = _codes(qx, "qx")
+    n, kw, pb, ldb = _codes(qw, "qw")
     dev = qx.device
-    (m, k), n = qx.shape, qw.shape[0]
-    if qw.shape[1] != k:
-        raise ValueError(f"reduction dims differ: qx {tuple(qx.shape)}, qw {tuple(qw.shape)}")
+    if kw != k:
+        raise ValueError(f"reduction dims differ: qx {(m, k)}, qw {(n, kw)}")
     if qw.device != dev:
         raise ValueError(f"qw must be on {dev}, got {qw.device}")
     if k < GROUP or k % GROUP:
@@ -124,7 +126,7 @@ def fprop_act(qx: Tensor, sx: Tensor, qw: Tensor, sw: Tensor, bias: Optional[Ten
             raise TypeError(f"bias must be bfloat16 or float32, got {bias.dtype}")
         pbias = _vector(bias, "bias", n, bias.dtype, dev)
         btype = L.PF8_F32 if bias.dtype == torch.float32 else L.PF8_BF16
-    shape = torch.Size((m, cols))
+    shape = (m, cols)
     pr = ldr = pz = ldz = 0
     if residual is not None:
         pr, ldr = _aligned_rows(residual, "residual", shape, dev)
