@@ -471,7 +471,8 @@ __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_ker
       }
     };
     // stores of a thread's chunks of N to an array from its tile's first element on; c: the chunk's first column
-    // there, room: the columns left from it
+    // there, room: the columns left from it. Non-temporal: with d cached 8192 x 12288 x 2048 gated takes 193 us instead of 178,
+    // with the quantiser that reads d after it 224 instead of 212 (d of 33 MB, all one round of tiles: 4 us the other way)
     auto store_rows = [&](auto n_c, uint16_t* base, int64_t ld, int c, int room, int i) {
       constexpr int N = decltype(n_c)::value, PER = 32 * N / 64;
       uint32_t addr[PER];

@@ -76,6 +76,8 @@ struct Lane {
     } else {
       u = pack8(a), v = pack8(b);
     }
+    // (cached: non-temporal stores take the forward of 8192 tokens from 24.6 to 21.7 us and make whoever reads the
+    // result next 11 us slower)
     *reinterpret_cast<u128_a2*>(x + e0) = u128_a2{u.x, u.y, u.z, u.w};
     *reinterpret_cast<u128_a2*>(x + e1) = u128_a2{v.x, v.y, v.z, v.w};
   }
