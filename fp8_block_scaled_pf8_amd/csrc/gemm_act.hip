@@ -63,7 +63,7 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p, int 
   const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int kb = wave; kb < nk; kb += WAVES * U) {
     v8i fw[U][PARTS], fx[U][MT];
-    float a[U][MT], b[U][PARTS];
+    uint32_t a[U][MT], b[U][PARTS];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = kb + u * WAVES;
@@ -71,12 +71,12 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p, int 
 #pragma unroll
       for (int i = 0; i < PARTS; ++i) {
         fw[u][i] = lds_read32(w[i] + at * kGroup, 0, 16);
-        b[u][i] = sw[i][at];
+        b[u][i] = __float_as_uint(sw[i][at]);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         fx[u][t] = lds_read32(x[t] + at * kGroup, 0, 16);
-        a[u][t] = sx[t][at * p.ld_as];
+        a[u][t] = __float_as_uint(sx[t][at * p.ld_as]);
       }
     }
 #pragma unroll
@@ -86,9 +86,11 @@ __global__ __launch_bounds__(512) void fprop_act_few_kernel(FpropActArgs p, int 
       for (int i = 0; i < PARTS; ++i)
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
+          // the two powers of two by their exponents: their product may be past FP32's range where the partial times it is not
+          const int exponent = static_cast<int>(a[u][t] >> 23) + static_cast<int>(b[u][i] >> 23) - 254;
           const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[u][i], fx[u][t], zero, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][t][r] = __builtin_fmaf(part[r], a[u][t] * b[u][i], acc[i][t][r]);
+          for (int r = 0; r < 4; ++r) acc[i][t][r] += __builtin_ldexpf(part[r], exponent);
         }
     }
   }
