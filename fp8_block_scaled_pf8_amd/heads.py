@@ -344,6 +344,8 @@ class QKNormRopeFunction(torch.autograd.Function):
             """(dx, dw) of one tensor, as a call for queries alone."""
             if d is None:
                 return None, None
+            if w is None and positions is None:  # neither normalised nor rotated: a copy
+                return d.to(torch.bfloat16), None
             d3 = _as_heads(d.to(torch.bfloat16))
             add = w is not None and m is not None and wanted
             g = qk_norm_rope_backward(d3, None, x, None, positions, inv_freq, w, None, **ctx.options,
