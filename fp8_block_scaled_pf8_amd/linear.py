@@ -107,34 +107,40 @@ def _rows(t: torch.Tensor, cols: int) -> torch.Tensor:
     return t
 
 
+def _act_forward(x, w, bias, residual, activation, gated, w_codes, keep):
+    """(d, what the backward pass needs beside the arguments: None where it is not kept)."""
+    lead, k, n = x.shape[:-1], x.shape[-1], w.shape[0]
+    cols = n // 2 if gated else n
+    x2 = _rows(x, k)
+    _check_shapes(x2.shape[0], n, k)
+    if x2.shape[0] == 0:
+        return x.new_empty((*lead, cols)), None
+    if keep:
+        qx, sx, qxt, sxt = ops.quant_act_dual(x2)
+    else:
+        qx, sx = ops.quant_act_1x128(x2)
+    qw, qwt, sw = w_codes if w_codes is not None else ops.quant_w_128x128(w.contiguous(), transposed=keep)
+    d = torch.empty((x2.shape[0], cols), dtype=torch.bfloat16, device=x.device)
+    got = epilogue.fprop_act(qx, sx, qw, sw, bias, activation, gated, None if residual is None else _rows(residual, cols),
+                             save_z=keep and activation is not None, out=d)
+    saved = (qxt, sxt, qwt, sw, got[1] if activation is not None else None) if keep else None
+    return d.reshape(*lead, cols), saved
+
+
 class Fp8LinearActFunction(torch.autograd.Function):
     """Autograd function of the FP8 linear layer with its epilogue (see the module docstring)."""
 
     @staticmethod
     def forward(ctx, x, w, bias, residual, activation, gated, main_grad, bias_main_grad, w_codes):
-        lead, k, n = x.shape[:-1], x.shape[-1], w.shape[0]
-        cols = n // 2 if gated else n
-        x2 = _rows(x, k)
-        _check_shapes(x2.shape[0], n, k)
-        ctx.lead, ctx.k, ctx.activation, ctx.gated = lead, k, activation, gated
+        ctx.lead, ctx.k, ctx.n, ctx.activation, ctx.gated = x.shape[:-1], x.shape[-1], w.shape[0], activation, gated
         ctx.main_grad, ctx.bias_main_grad, ctx.bias = main_grad, bias_main_grad, None if bias is None else bias.dtype
         ctx.leaves = [t is not None and t.requires_grad and t.is_leaf for t in (x, w, bias, residual)]
-        ctx.empty = x2.shape[0] == 0
-        if ctx.empty:
-            ctx.n = n
-            return x.new_empty((*lead, cols))
-        keep = any(ctx.needs_input_grad)
-        if keep:
-            qx, sx, qxt, sxt = ops.quant_act_dual(x2)
-        else:
-            qx, sx = ops.quant_act_1x128(x2)
-        qw, qwt, sw = w_codes if w_codes is not None else ops.quant_w_128x128(w.contiguous(), transposed=True)
-        d = torch.empty((x2.shape[0], cols), dtype=torch.bfloat16, device=x.device)
-        got = epilogue.fprop_act(qx, sx, qw, sw, bias, activation, gated, None if residual is None else _rows(residual, cols),
-                                 save_z=keep and activation is not None, out=d)
-        if keep:
-            ctx.save_for_backward(qxt, sxt, qwt, sw, got[1] if activation is not None else None)
-        return d.reshape(*lead, cols)
+        ctx.empty = x.numel() == 0
+        # (a gradient of the residual alone is the result's)
+        d, saved = _act_forward(x, w, bias, residual, activation, gated, w_codes, any(ctx.needs_input_grad[:3]))
+        if saved is not None:
+            ctx.save_for_backward(*saved)
+        return d
 
     @staticmethod
     @once_differentiable
@@ -154,11 +160,11 @@ class Fp8LinearActFunction(torch.autograd.Function):
             dw = dd.new_zeros((ctx.n, ctx.k), dtype=torch.bfloat16) if need[1] and ctx.main_grad is None else None
             db = dd.new_zeros((ctx.n,), dtype=ctx.bias) if need[2] and ctx.bias_main_grad is None else None
             return (dx, dw, db, dres, *none)
-        qxt, sxt, qwt, sw, z = ctx.saved_tensors
-        n = qwt.shape[1]
-        dz = _rows(dd.to(torch.bfloat16), n // 2 if ctx.gated else n)
         if not any(need[:3]):
             return (None, None, None, dres, *none)
+        qxt, sxt, qwt, sw, z = ctx.saved_tensors
+        n = ctx.n
+        dz = _rows(dd.to(torch.bfloat16), n // 2 if ctx.gated else n)
         add = need[2] and ctx.bias_main_grad is not None
         bias = dict(bias_grad=need[2], dbias_out=ctx.bias_main_grad if add else None, accumulate=add)
         if dz.shape[1] % GROUP:  # a gate over an odd number of 64 columns: a scale's columns are of both halves
@@ -217,6 +223,9 @@ def fp8_linear_act(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     _check_layer(x, w, bias, residual, activation, gated, main_grad, bias_main_grad)
     if w_codes is not None:
         _check_codes(w, w_codes)
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, w, bias, residual))):
+        # (a function's own needs_input_grad is true of a parameter under no_grad, too)
+        return _act_forward(x, w, bias, residual, activation, bool(gated), w_codes, False)[0]
     return Fp8LinearActFunction.apply(x, w, bias, residual, activation, bool(gated), main_grad, bias_main_grad, w_codes)
 
 
