@@ -288,7 +288,8 @@ class Fp8Linear(torch.nn.Module):
         key = (w.data_ptr(), w._version, tuple(w.shape), w.device)
         cur = torch.cuda.current_stream(w.device)
         if self._codes is None or self._codes_key != key:
-            with torch.no_grad():
+            # (codes made in inference mode could not be saved for a later training pass)
+            with torch.inference_mode(False), torch.no_grad():
                 self._codes = ops.quant_w_128x128(w.detach().contiguous(), transposed=True)
             self._codes_key = key
             self._codes_ready = torch.cuda.Event()

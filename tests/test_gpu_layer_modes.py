@@ -1,0 +1,38 @@
+"""A layer that is first used without gradients, then trained."""
+import pytest
+import torch
+
+import fp8_block_scaled_pf8_amd as pf8
+from tests.gpu_helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def _rand(shape, seed, scale=1.0, dtype=BF):
+    return (torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * scale).to(dtype).to(DEV)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+@pytest.mark.parametrize("first", ["infer", "call"])
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="silu", gated=True)])
+def test_trained_after(mode, first, kw):
+    """The weight's codes that a pass without gradients made serve the training passes after it."""
+    torch.manual_seed(1)
+    lin, other = pf8.Fp8Linear(256, 512, device=DEV, **kw), pf8.Fp8Linear(256, 512, device=DEV, **kw)
+    with torch.no_grad():
+        other.weight.copy_(lin.weight)
+    x = _rand((128, 256), 1).requires_grad_()
+    with mode():
+        y = lin.infer(x[:5]) if first == "infer" else lin(x)
+    assert y.shape[0] == (5 if first == "infer" else 128)
+    codes = lin.weight_codes()
+    grads = []
+    for m in (lin, other):
+        d = m(x)
+        d.backward(_rand(d.shape, 2, 1e-2))
+        grads.append([x.grad, m.weight.grad])
+        x.grad = None
+    assert lin.weight_codes() is codes
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
