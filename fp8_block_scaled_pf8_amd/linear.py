@@ -283,14 +283,18 @@ class Fp8Linear(torch.nn.Module):
 
         They are made on the current stream. A later call from another stream makes that stream
         wait for them, and marks them as used there, so that the allocator keeps their memory
-        until that stream's work is done even after new codes replace them."""
+        until that stream's work is done even after new codes replace them. Codes that are made while
+        the stream is being captured belong to that graph and are not kept."""
         w = self.weight
         key = (w.data_ptr(), w._version, tuple(w.shape), w.device)
         cur = torch.cuda.current_stream(w.device)
         if self._codes is None or self._codes_key != key:
             # (codes made in inference mode could not be saved for a later training pass)
             with torch.inference_mode(False), torch.no_grad():
-                self._codes = ops.quant_w_128x128(w.detach().contiguous(), transposed=True)
+                codes = ops.quant_w_128x128(w.detach().contiguous(), transposed=True)
+            if torch.cuda.is_current_stream_capturing():
+                return codes  # made by the graph's replays, in its memory: not there for an eager pass
+            self._codes = codes
             self._codes_key = key
             self._codes_ready = torch.cuda.Event()
             self._codes_ready.record(cur)

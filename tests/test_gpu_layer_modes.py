@@ -36,3 +36,27 @@ def test_trained_after(mode, first, kw):
         x.grad = None
     assert lin.weight_codes() is codes
     assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, activation="silu", gated=True)])
+def test_first_used_in_a_capture(kw):
+    """Codes that a graph makes are the graph's: an eager pass makes its own, before a replay as after one."""
+    torch.manual_seed(1)
+    lin, other = pf8.Fp8Linear(256, 512, device=DEV, **kw), pf8.Fp8Linear(256, 512, device=DEV, **kw)
+    with torch.no_grad():
+        other.weight.copy_(lin.weight)
+    x = _rand((3, 256), 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin.infer(x)
+    for i in range(3):
+        e = _rand((5, 256), 10 + i)
+        assert torch.equal(lin.infer(e), other.infer(e))
+        x.copy_(_rand((3, 256), 20 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, other.infer(x))
+        if i == 1:  # the graph follows the weight
+            with torch.no_grad():
+                lin.weight.mul_(2), other.weight.mul_(2)
