@@ -277,6 +277,7 @@ class Fp8Linear(torch.nn.Module):
         self._codes_key = None
         self._codes_ready = None  # event recorded on the stream that made the codes
         self._codes_users = set()  # streams the codes were handed to
+        self._codes_held = []  # codes that graphs were captured with
 
     def weight_codes(self) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
         """W's codes, transposed codes and tile scales, made once per version of the weight.
@@ -284,15 +285,18 @@ class Fp8Linear(torch.nn.Module):
         They are made on the current stream. A later call from another stream makes that stream
         wait for them, and marks them as used there, so that the allocator keeps their memory
         until that stream's work is done even after new codes replace them. Codes that are made while
-        the stream is being captured belong to that graph and are not kept."""
+        the stream is being captured belong to that graph and are not kept. A graph that is captured with
+        kept codes reads those at every replay, whatever becomes of the weight: they stay in memory as
+        long as the layer, and the graph is to be captured again after an update."""
         w = self.weight
         key = (w.data_ptr(), w._version, tuple(w.shape), w.device)
         cur = torch.cuda.current_stream(w.device)
+        capturing = torch.cuda.is_current_stream_capturing()
         if self._codes is None or self._codes_key != key:
             # (codes made in inference mode could not be saved for a later training pass)
             with torch.inference_mode(False), torch.no_grad():
                 codes = ops.quant_w_128x128(w.detach().contiguous(), transposed=True)
-            if torch.cuda.is_current_stream_capturing():
+            if capturing:
                 return codes  # made by the graph's replays, in its memory: not there for an eager pass
             self._codes = codes
             self._codes_key = key
@@ -304,6 +308,8 @@ class Fp8Linear(torch.nn.Module):
             for t in self._codes:
                 t.record_stream(cur)
             self._codes_users.add(cur.cuda_stream)
+        if capturing and not any(c is self._codes for c in self._codes_held):
+            self._codes_held.append(self._codes)
         return self._codes
 
     def invalidate_weight_codes(self) -> None:

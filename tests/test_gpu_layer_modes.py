@@ -60,3 +60,29 @@ def test_first_used_in_a_capture(kw):
         if i == 1:  # the graph follows the weight
             with torch.no_grad():
                 lin.weight.mul_(2), other.weight.mul_(2)
+
+
+def test_graph_keeps_the_codes_it_was_captured_with():
+    """Codes made before a capture are baked into its graph: their memory stays theirs when new ones replace them."""
+    torch.manual_seed(1)
+    lin = pf8.Fp8Linear(256, 512, device=DEV, bias=True, activation="silu", gated=True)
+    x = _rand((3, 256), 1)
+    lin.infer(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lin.infer(x)
+    old = pf8.Fp8Linear(256, 512, device=DEV, bias=True, activation="silu", gated=True, weight=lin.weight.detach().clone())
+    held = [t.data_ptr() for t in lin.weight_codes()]
+    for i in range(3):
+        with torch.no_grad():
+            lin.weight.add_(1)
+        if i == 1:
+            lin.invalidate_weight_codes()
+        new = lin.weight_codes()
+        filled = [torch.full_like(t, 3) for t in new]  # would take the old codes' place
+        assert not {t.data_ptr() for t in (*new, *filled)} & set(held)
+        x.copy_(_rand((3, 256), 20 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, old.infer(x))
