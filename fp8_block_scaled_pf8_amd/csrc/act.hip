@@ -23,8 +23,9 @@ template <int ACT, bool GATED, RowEnd END>
 __global__ __launch_bounds__(256) void act_bwd_kernel(ActBwdArgs a, int wide) {
   const int tx = threadIdx.x & (wide - 1), ty = threadIdx.x / wide, high = 256 / wide;
   const int cols = a.cols;
-  int c = 8 * (static_cast<int>(blockIdx.x) * wide + tx);
-  const int n = cols - c;  // columns from here
+  const uint32_t c0 = 8 * (blockIdx.x * wide + tx);  // (past 2^31 for the last threads of the widest rows)
+  const int n = static_cast<int>(cols - c0);          // columns from here: under 1 for threads behind the row
+  int c = static_cast<int>(c0);
   const int first = END == kTiny || n >= 8 ? 0 : n <= 0 ? 8 : 8 - n;
   if (END == kOdd && n < 8) c = cols - 8;
   const bool any = n > 0;
@@ -150,7 +151,7 @@ int64_t act_bwd_groups(int64_t rows, int64_t cols) { return act_bwd_blocks(rows,
 
 hipError_t launch_act_bwd(const ActBwdArgs& a, hipStream_t stream) {
   const int wide = act_bwd_wide(a.cols, a.dbias != nullptr);
-  const int64_t strips = (a.cols + 8 * wide - 1) / (8 * wide), groups = act_bwd_blocks(a.rows, a.cols, a.dbias != nullptr);
+  const int64_t strips = (int64_t{a.cols} + 8 * wide - 1) / (8 * wide), groups = act_bwd_blocks(a.rows, a.cols, a.dbias != nullptr);
   auto go = [&](auto act, auto gated, auto end) {
     hipLaunchKernelGGL((act_bwd_kernel<decltype(act)::value, decltype(gated)::value, decltype(end)::value>),
                        dim3(static_cast<uint32_t>(strips), static_cast<uint32_t>(groups)), dim3(256), 0, stream, a, wide);
