@@ -18,6 +18,9 @@ using pf8::device_status;
 using pf8::kMaxDim;
 using pf8::launch_status;
 
+// Partial column sums are joined by 32 threads a column, and a grid has under 2^32 of them.
+constexpr int64_t kMaxSumWidth = int64_t{1} << 27;
+
 // One of the [tokens, heads, head_dim] arrays: its address and strides.
 int check_heads(const void* p, int64_t heads, int64_t dim, int64_t st, int64_t sh, int64_t tokens_written = 0) {
   if (!p || st < (tokens_written > 1 ? dim : 0) || (heads > 1 && sh < dim)) return PF8_EINVAL;
@@ -220,6 +223,7 @@ pf8_status pf8_act_bwd_quant(int64_t rows, int64_t cols, const void* dd, int64_t
   if (lddd < cols || (z && ldz < width) || ldq_row < width || ld_sr < rows || ldq_col < rows || ld_sc < width)
     return PF8_EINVAL;
   if (rows % 128 || cols % 128 || rows / 128 > 65535 || width > kMaxDim) return PF8_ESHAPE;
+  if (dbias && rows > 128 && width >= kMaxSumWidth) return PF8_ESHAPE;
   if (dbias && (!workspace || workspace_bytes < pf8_act_bwd_quant_workspace(rows, cols, gated))) return PF8_EINVAL;
   if (!aligned(dd, 16) || lddd % 8 || !aligned(z, 16) || (z && ldz % 8) || !aligned(q_row, 16) || ldq_row % 16 ||
       !aligned(q_col, 16) || ldq_col % 16 || !aligned(dscale_row, 4) || !aligned(dscale_col, 4) || !aligned(dbias, 4) ||

@@ -135,7 +135,7 @@ int64_t pf8_act_bwd_workspace(int64_t rows, int64_t cols, int gated);
  * with a gate: q_row [rows, width], dscale_row[g * ld_sr + r], q_col [width, rows], dscale_col[g * ld_sc + c], as
  * pf8_quant_act_dual writes them (16-byte aligned codes with pitches of multiples of 16). z NULL with
  * PF8_ACT_NONE: the codes of dd. dbias as in pf8_act_bwd, its sums formed in another fixed order; workspace of
- * pf8_act_bwd_quant_workspace bytes where it is wanted.
+ * pf8_act_bwd_quant_workspace bytes where it is wanted, and with more than 128 rows width < 2^27 there (PF8_ESHAPE).
  */
 pf8_status pf8_act_bwd_quant(int64_t rows, int64_t cols, const void* dd, int64_t lddd, const void* z, int64_t ldz,
                              pf8_activation activation, int gated, void* q_row, int64_t ldq_row, float* dscale_row,
