@@ -67,7 +67,8 @@ def _bytes_at(t: Tensor) -> Tuple[int, int, int, int]:
     as rows where the heads of a token lie within its stride, else all of it as one."""
     first = t.data_ptr()
     if t.dim() != 3:
-        return first, first + 4 * t.numel(), 4 * t.numel(), 0
+        size = t.numel() * t.element_size()
+        return first, first + size, size, 0
     (n, h, d), (st, sh, _) = t.shape, t.stride()
     width = (h - 1) * sh + d
     if n == 1 or st >= width:
