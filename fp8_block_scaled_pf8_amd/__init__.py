@@ -29,6 +29,7 @@ from ._lib import (
     pf8_block_norm_bwd,
     pf8_block_norm_bwd_workspace,
     pf8_fprop_act,
+    pf8_fprop_act_tile,
     pf8_gemm_bf16,
     pf8_newton_schulz,
     pf8_newton_schulz_workspace,
@@ -63,6 +64,6 @@ __all__ = [
     "fp8_block_norm", "pf8_newton_schulz", "pf8_newton_schulz_workspace", "newton_schulz",
     "pf8_qk_norm_rope", "pf8_qk_norm_rope_bwd", "pf8_qk_norm_rope_bwd_workspace", "pf8_act_bwd", "pf8_act_bwd_workspace",
     "QKNormRope", "QKNormRopeFunction", "QKNormRopeGrads", "fp8_qk_norm_rope", "qk_norm_rope", "qk_norm_rope_backward",
-    "pf8_fprop_act", "pf8_act_bwd_quant", "pf8_act_bwd_quant_workspace",
+    "pf8_fprop_act", "pf8_fprop_act_tile", "pf8_act_bwd_quant", "pf8_act_bwd_quant_workspace",
     "ActGrads", "ActQuantGrads", "act_backward", "act_backward_quant", "fprop_act",
 ]

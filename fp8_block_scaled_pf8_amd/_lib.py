@@ -31,7 +31,7 @@ PF8_HEAD_MAX_DIM, PF8_HEAD_MAX_AXES, PF8_HEAD_MAX_HEADS = 512, 4, 65536
 PF8_ACT_NONE, PF8_ACT_RELU, PF8_ACT_RELU2, PF8_ACT_SILU, PF8_ACT_GELU, PF8_ACT_GELU_TANH = range(6)
 PF8_NORM_MAX_COLS = 16384
 PF8_NS_MAX_SHORT, PF8_NS_MAX_LONG, PF8_NS_MAX_BATCH, PF8_NS_MAX_STEPS = 32768, 1048576, 65535, 64
-ABI_VERSION = 7
+ABI_VERSION = 8
 
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
@@ -93,6 +93,7 @@ LAYER_SIGNATURES = {
     "pf8_fprop_act": (
         _int, [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _int, _int, _vp, _i64, _vp, _i64,
                _vp, _i64, _vp]),
+    "pf8_fprop_act_tile": (_i64, [_i64, _i64, _i64, _int]),
 }
 
 
@@ -195,6 +196,7 @@ pf8_act_bwd_workspace = LIB.pf8_act_bwd_workspace
 pf8_act_bwd_quant = LIB.pf8_act_bwd_quant
 pf8_act_bwd_quant_workspace = LIB.pf8_act_bwd_quant_workspace
 pf8_fprop_act = LIB.pf8_fprop_act
+pf8_fprop_act_tile = LIB.pf8_fprop_act_tile
 
 
 def pf8_strerror(status: int) -> str:

@@ -267,4 +267,14 @@ pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t
   return launch_status(pf8::launch_fprop_act(args, static_cast<hipStream_t>(hip_stream)));
 }
 
+int64_t pf8_fprop_act_tile(int64_t m, int64_t n, int64_t k, int gated) {
+  if (m <= 0 || n <= 0 || k <= 0 || (gated != 0 && gated != 1) || any_too_big(m, n, k) || k % 128 != 0 ||
+      (gated && n % 128 != 0) || (m + 63) / 64 > 65535 * int64_t{64})
+    return 0;
+  pf8::FpropActArgs args{};
+  args.m = m, args.n = n, args.k = k, args.gated = gated;
+  const pf8::FpropActTile t = pf8::fprop_act_tile(args);
+  return int64_t{t.bm} * 65536 + t.bn;
+}
+
 }  // extern "C"

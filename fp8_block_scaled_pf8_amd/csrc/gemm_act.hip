@@ -196,7 +196,7 @@ struct TileCost {
   }
 };
 
-hipError_t launch_fprop_act(const FpropActArgs& a, hipStream_t stream) {
+FpropActTile fprop_act_tile(const FpropActArgs& a) {
   constexpr TileCost kShapes[] = {{256, 256, 7.0, 8.1, 12.2, 3.0},
                                   {256, 128, 7.0, 4.4, 8.0, 1.0},
                                   {128, 128, 6.0, 2.65, 4.7, 0.0},
@@ -209,14 +209,16 @@ hipError_t launch_fprop_act(const FpropActArgs& a, hipStream_t stream) {
   }
   const double few[3] = {few_cost<1>(a), few_cost<2>(a), few_cost<4>(a)};
   const int least = few[1] < few[0] ? (few[2] < few[1] ? 2 : 1) : few[2] < few[0] ? 2 : 0;
-  if (a.m <= 1024 && few[least] < cost[best])  // (the grid is as high as the groups of tokens)
-    return least == 0 ? launch_few<1>(a, stream) : least == 1 ? launch_few<2>(a, stream) : launch_few<4>(a, stream);
-  switch (best) {
-    case 0: return launch_fprop_act_tiles<256, 256>(a, stream);
-    case 1: return launch_fprop_act_tiles<256, 128>(a, stream);
-    case 2: return launch_fprop_act_tiles<128, 128>(a, stream);
-    default: return launch_fprop_act_tiles<64, 64>(a, stream);
-  }
+  if (a.m <= 1024 && few[least] < cost[best]) return {16 << least, 16};  // (the grid is as high as the groups of tokens)
+  return {kShapes[best].bm, kShapes[best].bn};
+}
+
+hipError_t launch_fprop_act(const FpropActArgs& a, hipStream_t stream) {
+  const FpropActTile t = fprop_act_tile(a);
+  if (t.bn == 16) return t.bm == 16 ? launch_few<1>(a, stream) : t.bm == 32 ? launch_few<2>(a, stream) : launch_few<4>(a, stream);
+  if (t.bn == 256) return launch_fprop_act_tiles<256, 256>(a, stream);
+  if (t.bm == 256) return launch_fprop_act_tiles<256, 128>(a, stream);
+  return t.bm == 128 ? launch_fprop_act_tiles<128, 128>(a, stream) : launch_fprop_act_tiles<64, 64>(a, stream);
 }
 
 }  // namespace pf8

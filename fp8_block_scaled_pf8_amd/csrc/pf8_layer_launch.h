@@ -109,6 +109,12 @@ struct FpropActArgs {
 };
 
 hipError_t launch_fprop_act(const FpropActArgs& args, hipStream_t stream);
+// What launch_fprop_act runs for m, n, k and gated: tiles of bm rows and bn rows of W, or for few tokens up to bm of them and
+// bn = 16 columns of d a workgroup.
+struct FpropActTile {
+  int bm, bn;
+};
+FpropActTile fprop_act_tile(const FpropActArgs& args);
 // By tiles of BM rows and BN rows of W.
 template <int BM, int BN>
 hipError_t launch_fprop_act_tiles(const FpropActArgs& args, hipStream_t stream);

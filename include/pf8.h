@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define PF8_ABI_VERSION 7
+#define PF8_ABI_VERSION 8
 
 /* The status, grouping-axis and layout types are plain ints, so that an out-of-range value
    reaches the library intact and is refused with PF8_EINVAL (a C enum parameter need not be

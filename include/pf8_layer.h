@@ -171,6 +171,13 @@ pf8_status pf8_fprop_act(int64_t m, int64_t n, int64_t k, const void* a, int64_t
                          const void* residual, int64_t ldr, void* z, int64_t ldz, void* d, int64_t ldd,
                          void* hip_stream);
 
+/*
+ * Which kernel pf8_fprop_act runs for a size: 65536 * rows + columns of what a workgroup works on. 64, 128 or 256 rows of
+ * 64, 128 or 256 rows of W: the tile kernels; 16, 32 or 64 rows of 16 columns of d: the kernel for few tokens. 0
+ * for sizes that it refuses. For tests and measurements that mean one of them. Needs no device.
+ */
+int64_t pf8_fprop_act_tile(int64_t m, int64_t n, int64_t k, int gated);
+
 #ifdef __cplusplus
 }
 #endif
