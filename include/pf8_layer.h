@@ -56,7 +56,8 @@ typedef int pf8_activation;
  *
  * and the head's further values as they are in n. Pair i holds the values i and pairs + i, or with
  * `interleaved` 2 i and 2 i + 1. The position is that of the token on the pair's axis. FP32, the angle's
- * fraction of a turn from FP64 (right at any position below 2^52), one rounding to BF16 at the end.
+ * fraction of a turn from FP64 (off by up to 2^-51.4 of the angle: 2^-11 radians at 2^40, nothing is left of it at
+ * 2^52), one rounding to BF16 at the end.
  *
  * q, k: bf16 [tokens, heads, head_dim] with strides _st between tokens and _sh between heads, head
  *   values contiguous. k NULL (with heads_k 0): queries alone. 1 <= head_dim <= 512, tokens * heads < 2^31.
