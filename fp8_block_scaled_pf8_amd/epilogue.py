@@ -49,7 +49,7 @@ def _activation(activation: Optional[str], gated: bool) -> int:
 def _aligned_rows(t: Tensor, name: str, shape, device) -> Tuple[int, int]:
     """(address, pitch) of a bf16 matrix that the product's epilogue reads or writes 16 bytes at a time."""
     p, ld = _rows(t, name, shape, device)
-    if shape[0] == 1:
+    if shape[0] <= 1:  # no second row: a pitch of any size
         ld = -(-shape[1] // 8) * 8
     if p % 16 or ld % 8:
         raise ValueError(f"{name} must be 16-byte aligned with a row pitch of a multiple of 8")
