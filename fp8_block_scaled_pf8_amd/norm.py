@@ -21,7 +21,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib as L
-from .ops import GROUP, code_buffer
+from .ops import GROUP, _call, code_buffer
 
 Tensor = torch.Tensor
 
@@ -140,25 +140,6 @@ def _may_write(out: Tensor, name: str, others) -> None:
         b = _rows_at(o)
         if _rows_meet(a, b) and not (same_ok and a[0] == b[0] and a[3] == b[3]):
             raise ValueError(f"{name} overlaps another operand")
-
-
-# The current stream's handle and the current device's number without the objects and checks around them (which cost
-# as much as half a launch).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _call(fn, device: torch.device, *args) -> None:
-    """A library call that enqueues on the current stream of a device, made the current one where it is not."""
-    index = device.index
-    if index == _current_device():
-        status = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(index))
-    if status != L.PF8_OK:
-        L.check(status, fn.__name__)
 
 
 def _forward(h, y, w_pre, w_post, gate, residual_scale, branch_scale, eps, unit_offset, r_out, x_out, codes):

@@ -24,8 +24,23 @@ from . import _lib as L
 GROUP = 128
 
 
-def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+# The current stream's handle and the current device's number without the objects and checks around them (which cost
+# as much as half a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(fn, device: torch.device, *args, name: Optional[str] = None) -> None:
+    """A library call that enqueues on the current stream of a device, made the current one where it is not."""
+    index = device.index
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index))
+    if status != L.PF8_OK:
+        L.check(status, name or fn.__name__)
 
 
 def _check_2d(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
@@ -116,8 +131,8 @@ def quant_act_1x128(x: torch.Tensor, along: str = "cols") -> Tuple[torch.Tensor,
         s = torch.empty((max(rows // GROUP, 1), cols), dtype=torch.float32, device=x.device)
     else:
         raise ValueError("along must be 'cols' or 'rows'")
-    L.check(L.pf8_quant_act_1x128(x.data_ptr(), rows, cols, x.stride(0), axis, q.data_ptr(), q.stride(0),
-                                  s.data_ptr(), s.stride(0), _stream(x)), "pf8_quant_act_1x128")
+    _call(L.pf8_quant_act_1x128, x.device, x.data_ptr(), rows, cols, x.stride(0), axis, q.data_ptr(), q.stride(0),
+          s.data_ptr(), s.stride(0))
     return q, s
 
 
@@ -132,9 +147,8 @@ def quant_act_dual(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.T
     e = lambda *sh, dt=torch.uint8: torch.empty(sh, dtype=dt, device=x.device)  # noqa: E731
     qr, sr = code_buffer(rows, cols, x.device), e(max(cols // GROUP, 1), rows, dt=torch.float32)
     qc, sc = code_buffer(cols, rows, x.device), e(max(rows // GROUP, 1), cols, dt=torch.float32)
-    L.check(L.pf8_quant_act_dual(x.data_ptr(), rows, cols, x.stride(0), qr.data_ptr(), qr.stride(0), sr.data_ptr(),
-                                 sr.stride(0), qc.data_ptr(), qc.stride(0), sc.data_ptr(), sc.stride(0), _stream(x)),
-            "pf8_quant_act_dual")
+    _call(L.pf8_quant_act_dual, x.device, x.data_ptr(), rows, cols, x.stride(0), qr.data_ptr(), qr.stride(0), sr.data_ptr(),
+          sr.stride(0), qc.data_ptr(), qc.stride(0), sc.data_ptr(), sc.stride(0))
     return qr, sr, qc, sc
 
 
@@ -146,9 +160,8 @@ def quant_w_128x128(w: torch.Tensor, transposed: bool = True
     q = code_buffer(n, k, w.device)
     qt = code_buffer(k, n, w.device) if transposed else None
     s = torch.empty((max(n // GROUP, 1), max(k // GROUP, 1)), dtype=torch.float32, device=w.device)
-    L.check(L.pf8_quant_w_128x128(w.data_ptr(), n, k, w.stride(0), q.data_ptr(), q.stride(0),
-                                  qt.data_ptr() if qt is not None else 0, qt.stride(0) if qt is not None else 0,
-                                  s.data_ptr(), s.stride(0), _stream(w)), "pf8_quant_w_128x128")
+    _call(L.pf8_quant_w_128x128, w.device, w.data_ptr(), n, k, w.stride(0), q.data_ptr(), q.stride(0),
+          qt.data_ptr() if qt is not None else 0, qt.stride(0) if qt is not None else 0, s.data_ptr(), s.stride(0))
     return q, qt, s
 
 
@@ -172,9 +185,9 @@ def block_gemm(layout: int, a: torch.Tensor, a_dscale: torch.Tensor, b: torch.Te
     _check_2d(out, torch.bfloat16, "out")
     if tuple(out.shape) != (m, n):
         raise ValueError("out has the wrong shape")
-    L.check(L.pf8_block_gemm_variant(variant, layout, m, n, k, a.data_ptr(), a.stride(0), a_dscale.data_ptr(),
-                                     a_dscale.stride(0), b.data_ptr(), b.stride(0), b_dscale.data_ptr(), sb_n, sb_k,
-                                     out.data_ptr(), out.stride(0), _stream(a)), "pf8_block_gemm")
+    _call(L.pf8_block_gemm_variant, a.device, variant, layout, m, n, k, a.data_ptr(), a.stride(0), a_dscale.data_ptr(),
+          a_dscale.stride(0), b.data_ptr(), b.stride(0), b_dscale.data_ptr(), sb_n, sb_k, out.data_ptr(), out.stride(0),
+          name="pf8_block_gemm")
     return out
 
 
@@ -202,9 +215,9 @@ def block_gemm_f32(layout: int, a: torch.Tensor, a_dscale: torch.Tensor, b: torc
     _check_2d(out, torch.float32, "out")
     if tuple(out.shape) != (m, n):
         raise ValueError("out has the wrong shape")
-    L.check(L.pf8_block_gemm_f32(layout, m, n, k, a.data_ptr(), a.stride(0), a_dscale.data_ptr(), a_dscale.stride(0),
-                                 b.data_ptr(), b.stride(0), b_dscale.data_ptr(), sb_n, sb_k, out.data_ptr(),
-                                 out.stride(0), int(accumulate), _stream(a)), "pf8_block_gemm_f32")
+    _call(L.pf8_block_gemm_f32, a.device, layout, m, n, k, a.data_ptr(), a.stride(0), a_dscale.data_ptr(),
+          a_dscale.stride(0), b.data_ptr(), b.stride(0), b_dscale.data_ptr(), sb_n, sb_k, out.data_ptr(), out.stride(0),
+          int(accumulate))
     return out
 
 
@@ -221,8 +234,8 @@ def gemm_bf16(a: torch.Tensor, b: torch.Tensor, out: Optional[torch.Tensor] = No
     _check_2d(out, torch.bfloat16, "out")
     if tuple(out.shape) != (m, n):
         raise ValueError("out has the wrong shape")
-    L.check(L.pf8_gemm_bf16(m, n, k, a.data_ptr(), a.stride(0), b.data_ptr(), b.stride(0), out.data_ptr(),
-                            out.stride(0), _stream(a)), "pf8_gemm_bf16")
+    _call(L.pf8_gemm_bf16, a.device, m, n, k, a.data_ptr(), a.stride(0), b.data_ptr(), b.stride(0), out.data_ptr(),
+          out.stride(0))
     return out
 
 
