@@ -33,7 +33,8 @@ __device__ __forceinline__ float tanh_sigmoid(float& z, float& z2) {
 // The normal distribution Phi(z) = (1 + erf(z / sqrt 2)) / 2, and e = exp(-z^2 / 2). Below zero Phi = e h(|z|) with
 // h(a) = exp(a^2 / 2) Phi(-a), a smooth function that falls as 1 / a: h(a) = t P(t), t = 1 / (1 + 0.3 a), with P of
 // degree 7 fitted for the least relative error on 0 .. 14 (1.5e-7, in FP32 5e-7; beyond, e vanishes). No difference of
-// near values below zero, one minus that above. 16 instructions with two slow ones; erff takes some 50.
+// near values below zero, one minus that above. Below zero the roundings of e's argument count, too: together 5e-7 + 2^-24 z^2
+// of Phi, 3e-6 at -6 and 1e-5 at -13. 16 instructions with two slow ones; erff takes some 50.
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
   e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170368f);
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, __builtin_fabsf(z), 1.0f));

@@ -25,8 +25,9 @@ __device__ __forceinline__ float act_any(int act, float z) {
 // row of W is read by two waves, so LDS would only be a detour. One v_mfma_f32_16x16x128_f8f6f4 covers a K block of 16
 // rows of W and 16 tokens; its partial is scaled into the wave's FP32 sum. The waves' sums meet in LDS, added in
 // the waves' order.
-// Bound: what a CU reads, its rows of W and of X, some 30 bytes a nanosecond. One token of 12288 x 2048 gated: 6.8 us, 25
-// MB at 3.7 TB/s; 33 tokens of 2048 x 6144 onto a residual: 9.4 us, two groups over 256 workgroups, 0.2 MB each. 16 waves, 4
+// Bound: what a CU reads, its rows of W and of X, some 30 bytes a nanosecond. On the same operands again (in brackets on
+// operands from memory): one token of 12288 x 2048 gated 6.9 us (8.5), 25 MB at 3.6 TB/s (3.0); 33 tokens of 2048 x 6144 with a bias
+// onto a residual 10.1 us (12.0), two groups over 256 workgroups, 0.2 MB each. 16 waves, 4
 // or 8 rows of W a workgroup, loads of whole cache lines a quarter wave and 3 to 8 K blocks in flight (gated, 6 took
 // 8.5 us instead of 6.8) were no faster.
 template <int MT, bool GATED>

@@ -105,7 +105,10 @@ constexpr int kTilesPerCu = 160 * 1024 / (4 * (BM + BN) * 64 + 128 * BN);
 // Bound: matrix instructions at the clock that the power allows, and at 256 x 256 the epilogue, which nothing hides: one
 // tile's accumulators fill a CU's registers, so the matrix cores wait while its results leave. 8192 x 12288 x 2048 gated:
 // 196 us (2.1 PFLOP/s), without z (0.2 GB less to write) 174; the plain product of that size 165. 8192 x 2048 x 6144
-// with bias, onto a residual: 89 us (2.3 PFLOP/s); the plain product 83.
+// with bias, onto a residual: 89 us (2.3 PFLOP/s) on the same operands again, 102 on operands from memory; the plain
+// product 83. Those are one box's; others took up to 206 and 92.
+// At 256 x 256 102 to 156 scalar registers are kept in lanes of vector registers (in the plain product's kernel 53 to 70),
+// hardly any of them over the K loop; no vector register is spilled.
 template <int BM, int BN, bool GATED, bool RES, ActClass ACT>
 __global__ __launch_bounds__(256, (kTilesPerCu<BM, BN>)) void fprop_act_tile_kernel(FpropActArgs p, int tiles_m, int tiles_n) {
   constexpr int BK = 64;

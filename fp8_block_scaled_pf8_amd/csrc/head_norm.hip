@@ -2,9 +2,12 @@
 // (gfx950). Formulas in include/pf8_layer.h.
 //
 // Bound: HBM. Forward 4 bytes a value (in and out), backward 6 (values, gradients, result); some ten FP32
-// operations a value, and for each token and pair an angle, its sine and cosine. 8192 tokens of 16 + 8 heads of 128:
-// forward 21 us (4.8 TB/s), backward 31 us (4.8 TB/s). Short batches are bound by one trip through memory and its FP64 angles:
-// one token 3.0 us, 1003 tokens of 14 + 2 heads with three axes 7.
+// operations a value, and for each token and pair an angle, its sine and cosine.
+// All times in this file are the GPU's alone, of 16 + 8 heads of 128 unless stated, on operands that come from memory
+// (sets of over 1 GB in turn); in brackets on the same operands again, of which the caches hold a part. 8192 tokens: forward
+// 26.0 us (22.1), 101 MB at 3.9 TB/s; backward 35.0 us (31.0), of which 3.5 are the sums of the weights' gradients, 151 MB at
+// 4.8 TB/s without those. Short batches are bound by one trip through memory and its FP64 angles: one token 3.0 us (2.9),
+// 1003 tokens of 14 + 2 heads of 80 with three axes 8.3 (7.1).
 // A head belongs to a group of lanes of one wave; each lane holds 8 rotated pairs (16 values, two 16-byte
 // loads), so that both values of a pair are in the same lane and the sums of a head run over the group by
 // DPP. A group takes up to HC heads of one token after another with the same angles; all their loads go out first.
@@ -76,8 +79,8 @@ struct Lane {
     } else {
       u = pack8(a), v = pack8(b);
     }
-    // (cached: non-temporal stores take the forward of 8192 tokens from 24.6 to 21.7 us and make whoever reads the
-    // result next 11 us slower)
+    // (cached: with non-temporal stores the forward of 8192 tokens takes 20.8 us instead of 26.0, but with a copy of its
+    // result after it 45.8 instead of 44.5: whoever reads the result next then reads it from memory)
     *reinterpret_cast<u128_a2*>(x + e0) = u128_a2{u.x, u.y, u.z, u.w};
     *reinterpret_cast<u128_a2*>(x + e1) = u128_a2{v.x, v.y, v.z, v.w};
   }
@@ -325,7 +328,8 @@ __global__ __launch_bounds__(256) void head_norm_fwd_kernel(HeadNormArgs p, unsi
 
 // Backward. The first workgroups take q's items, the others k's, in turn; each lane sums the weight's gradient at
 // its own values, the groups' sums meet in LDS, and a workgroup writes one row of partial sums. (With both tensors
-// in every workgroup a short batch waited for everything twice: 1537 tokens of 7 + 1 heads 12.2 us.)
+// in every workgroup a short batch waited for everything twice: 1537 tokens of 7 + 1 heads of 96 with three axes (12.2) us,
+// now 11.9 (9.9).)
 template <Kind KIND, int G, int HC, bool MULTI>
 __global__ __launch_bounds__(256) void head_norm_bwd_kernel(HeadNormArgs p, unsigned blocks_q) {
   constexpr int N = Lane<KIND>::N, GROUPS = 256 / G;
@@ -482,16 +486,18 @@ hipError_t launch_head_norm_fwd(const HeadNormArgs& a, hipStream_t stream) {
                          dim3(static_cast<uint32_t>(bq + bk)), dim3(256), 0, stream, a, static_cast<unsigned>(bq));
       return hipGetLastError();
     };
-    // Four heads of a token share its angles where there is work enough to fill the card that way: 16 + 8 heads of 128,
-    // 8192 tokens 20.8 us and 22.2 head by head, 2048 tokens 7.4 and 8.1, 1024 tokens 5.9 and 5.4, 64 tokens 5.0 and 3.6.
+    // Four heads of a token share its angles where there is work enough to fill the card that way: 8192 tokens 26.0 us (22.1)
+    // and 26.6 (21.8) head by head, 4096 tokens 15.5 (11.8) and 16.3 (13.4), 2048 tokens 10.4 (8.0) and 10.7 (8.1); 1024
+    // tokens, head by head, 6.8 (5.5) and 7.6 (6.0) by fours, 64 tokens 3.8 (3.6) and 5.3 (5.1).
     const int64_t heads = a.tokens * (a.t[0].heads + a.t[1].heads);
     return heads * G >= 5 * 256 * 256 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 1>{});
   });
 }
 
 // Workgroups of q and k: 768 in all (three on a CU), fewer where there is not as much work, shared out by the heads. More
-// of them hide more of the loads and leave more rows of partial sums: 8192 tokens of 16 + 8 heads of 128, 256, 512,
-// 768 and 1024 workgroups 39.4, 29.3, 25.9 and 28.3 us, 1536 tokens 14.5, 12.7, 10.9 and 13.4.
+// of them hide more of the loads and leave more rows of partial sums. With the sums, 8192 tokens by 256, 512, 768 and 1024
+// workgroups: 49.6, 37.7, 35.0 and 39.8 us (43.0, 33.2, 31.0 and 33.3), 1536 tokens 19.0, 16.8, 14.2 and 17.1 (15.4, 13.7, 11.6
+// and 14.3).
 static void bwd_blocks(int64_t tokens, int64_t heads_q, int64_t heads_k, int64_t& q, int64_t& k) {
   const int64_t heads = heads_q + heads_k, work = (tokens * heads + 31) / 32, all = work < 768 ? work : 768;
   q = heads_q ? (all * heads_q + heads - 1) / heads : 0;
@@ -524,8 +530,9 @@ hipError_t launch_head_norm_bwd(HeadNormArgs a, float* const (&dw)[2], int accum
           dim3(static_cast<uint32_t>(bq + bk)), dim3(256), 0, stream, a, static_cast<unsigned>(bq));
       return hipGetLastError();
     };
-    // Two heads of a token share its angles where there is work enough to fill the card that way: 8192 tokens 25.9 us
-    // and 29.4 head by head, 1536 tokens 10.9 and 11.6, 1024 tokens 9.6 and 9.3, 64 tokens 7.6 and 6.8.
+    // Two heads of a token share its angles where there is work enough to fill the card that way. With the sums, 8192 tokens
+    // 35.0 us (31.0) and 36.5 (31.1) head by head, 1536 tokens 14.2 (11.6) and 14.3 (12.3); 1024 tokens, head by
+    // head, 11.4 (9.9) and 12.2 (10.1) by twos, 64 tokens 7.4 (7.1) and 8.1 (7.9).
     const int64_t heads = a.tokens * (a.t[0].heads + a.t[1].heads);
     return heads * decltype(lanes)::value >= 2 * 256 * 512 ? go(std::integral_constant<int, 2>{})
                                                            : go(std::integral_constant<int, 1>{});
